@@ -51,7 +51,8 @@
 extern "C" {
 #endif
 
-typedef enum { SSM_F32 = 0, SSM_BF16 = 1 } ssm_dtype_t;
+/* SSM_I8 is a type of the attention cache only: int8 codes with one fp32 scale per row. */
+typedef enum { SSM_F32 = 0, SSM_BF16 = 1, SSM_I8 = 2 } ssm_dtype_t;
 
 enum {
     SSM_OK = 0,
@@ -66,7 +67,9 @@ enum {
 enum {
     SSM_DEV_WAIT_TIMEOUT = 1u,  /* a bounded wait on a TMA copy expired; the block stopped early */
     SSM_DEV_BAD_SLOT = 2u,      /* a decode request named a state slot outside [0, n_slots) */
-    SSM_DEV_SMEM_ALIGN = 4u     /* shared memory was not 128-byte aligned; the prefill did nothing */
+    SSM_DEV_SMEM_ALIGN = 4u,    /* shared memory was not 128-byte aligned; the prefill did nothing */
+    SSM_DEV_BAD_INDEX = 8u      /* an attention call met a position, slot, page or length outside its
+                                   table; that token or page was skipped, that length cut */
 };
 
 /* ABI version of this header (major * 100 + minor). */
@@ -450,6 +453,149 @@ int ssd_decode_step(int batch, int n_heads, int head_dim, int n_groups, int d_st
                     const float* A, const float* Dskip, const float* dt_bias,
                     float* conv_state, float* ssm_state, int n_slots, const int32_t* state_slot,
                     void* out, void* cuda_stream);
+
+/*
+ * The attention block of a hybrid layer.  The pages name the model families the mixer serves
+ * (Overview: Mamba, Falcon-Mamba, Zamba); Zamba-like models put attention blocks between the
+ * SSM mixers.  These calls are that block between its projections: rotary positions, the key
+ * and value cache that prefill fills and decode continues from (the counterpart of the state
+ * cache of Methodology 3), and causal softmax attention with grouped heads.
+ *
+ *   H = n_q_heads, Hk = n_kv_heads, H % Hk == 0; query head h reads kv head h / (H / Hk).
+ *   D = head_dim: a multiple of 16, 16 .. 128.
+ *   Activations are SSM_BF16 [tokens][heads][D] views: element (t, h, d) at
+ *   t*stride_t + h*stride_h + d, 16-byte aligned, strides multiples of 8 elements and >= D
+ *   (a slice of a fused projection's rows is allowed).
+ *
+ * The cache is paged.  k_cache and v_cache are [n_pages][Hk][page_size][D], contiguous and
+ * 16-byte aligned, page_size a multiple of 16 up to 4096; token p of a sequence lies in page
+ * page_table[p / page_size] at row p % page_size, so slot = page * page_size + row names a
+ * token's place (n_pages * page_size < 2^31; bytes are addressed in 64 bits).  cache_dtype:
+ *   SSM_BF16   the rows themselves (k_scale, v_scale NULL)
+ *   SSM_I8     int8 codes with k_scale, v_scale [n_pages][Hk][page_size] float32, one scale per
+ *              token and kv head: amax = max |x|; scale = amax / 127; code = round_half_even(
+ *              x * (127 / amax)) clamped to [-127, 127], IEEE fp32; amax == 0 gives scale and
+ *              codes 0.  A NaN is ignored by amax and gets code 0; a row holding an infinity
+ *              gets scale +inf and codes 0, and reads back as NaN.
+ * Rows that no sequence has written are never read: they may hold anything.
+ */
+
+/*
+ * attn_rope_table -- the cosines and sines of rotary positions 0 .. n_pos-1, made once per model:
+ * cos_out[p][i] = scale * cos(p * inv_freq[i]), sin_out likewise; angles in 64 bits, rounded once
+ * to float32, so that long positions keep their low bits.  Scaled positions (interpolation,
+ * per-frequency ramps) are a matter of inv_freq and scale.
+ *
+ *   n_pos, half          1 .. 2^26 positions, 1 .. 64 frequencies (rot_dim / 2)
+ *   inv_freq             HOST array [half], finite
+ *   cos_out, sin_out     [n_pos][half] float32 (device)
+ */
+int attn_rope_table(int64_t n_pos, int half, const double* inv_freq, double scale, float* cos_out,
+                    float* sin_out, void* cuda_stream);
+
+/*
+ * attn_append -- rotary positions on q and k, and k and v written into the cache at their slots.
+ * With half = rot_dim / 2, c_i = cos[positions[t]][i], s_i = sin[positions[t]][i], for i < half:
+ *   (a, b) = (x_i, x_{i+half}), or (x_{2i}, x_{2i+1}) when interleaved is nonzero
+ *   (a, b) -> (a c_i - b s_i, b c_i + a s_i)      (IEEE fp32, products rounded before the sum)
+ * Elements from rot_dim on pass through.  q_out and k_out are rounded to bf16; the int8 codes are
+ * taken from the fp32 values.
+ *
+ *   n_tokens             >= 0 (0 does nothing)
+ *   rot_dim              0 (no rotation; cos, sin, positions may be NULL) or a multiple of 8 up to D
+ *   positions            [n_tokens] int32 in [0, n_pos)        cos, sin: [n_pos][half] float32
+ *   slots                [n_tokens] int32 in [0, n_pages * page_size), distinct; -1 marks a padding
+ *                        token, of which nothing is read or written.  Any other slot or position
+ *                        outside its range skips the token and sets SSM_DEV_BAD_INDEX.
+ *   q, q_out             NULL (both) or views; q_out may be q itself with q's strides
+ *   k, v                 required views        k_out: NULL or a view, may be k itself
+ */
+int attn_append(int64_t n_tokens, int n_q_heads, int n_kv_heads, int head_dim, int rot_dim, int interleaved,
+                const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                const void* k, int64_t k_stride_t, int64_t k_stride_h,
+                const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                const int32_t* positions, const float* cos, const float* sin, int64_t n_pos,
+                const int32_t* slots, ssm_dtype_t cache_dtype, void* k_cache, void* v_cache,
+                float* k_scale, float* v_scale, int n_pages, int page_size,
+                void* q_out, int64_t qo_stride_t, int64_t qo_stride_h,
+                void* k_out, int64_t ko_stride_t, int64_t ko_stride_h, void* cuda_stream);
+
+/*
+ * attn_cache_read -- rows of the cache back as packed tokens, dequantized: code * scale in fp32,
+ * then rounded to nearest even for bf16.  Sequence b's tokens first[b] .. first[b] + n_b - 1, n_b =
+ * cu_len[b+1] - cu_len[b], go to rows cu_len[b] .. of k_out and v_out.
+ *
+ *   batch, n_tokens      1..65535 sequences; n_tokens = cu_len[batch] >= 0 (0 does nothing)
+ *   page_table           [batch][table_stride] int32, pages of each sequence in order; entries past
+ *                        a sequence's last page are not read.  n_table <= table_stride entries a row.
+ *   cu_len               [batch + 1] int32, cu_len[0] = 0, not decreasing
+ *   first                NULL (0) or [batch] int32
+ *   out_dtype            SSM_BF16 or SSM_F32; k_out, v_out [n_tokens][Hk][D] contiguous, 16-byte
+ *                        aligned
+ * A token whose page is outside [0, n_pages) or past the table's row is not written and sets
+ * SSM_DEV_BAD_INDEX.
+ */
+int attn_cache_read(int batch, int64_t n_tokens, int n_kv_heads, int head_dim, ssm_dtype_t cache_dtype,
+                    const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                    int n_pages, int page_size, const int32_t* page_table, int64_t table_stride, int n_table,
+                    const int32_t* cu_len, const int32_t* first, ssm_dtype_t out_dtype,
+                    void* k_out, void* v_out, void* cuda_stream);
+
+/*
+ * attn_prefill -- causal attention over packed sequences.  Sequence b holds query rows
+ * cu_q[b] .. cu_q[b+1]-1 and key rows cu_k[b] .. cu_k[b+1]-1 (Lq and Lk of them).  Its last query
+ * sees its last key: query i sees keys j <= i + Lk - Lq, so Lk > Lq is a chunk of a prompt over
+ * its earlier tokens, and a query with no visible key gives zeros and lse -inf.
+ *   s_ij = scale * q_i . k_j;  out_i = sum_j softmax_j(s_ij) v_j;  lse_i = ln sum_j exp(s_ij)
+ * bf16 products with fp32 accumulation; the softmax weights are rounded to bf16 for the second
+ * product, their sum is not.  What lies in keys and values that a query does not see, NaN and
+ * infinities included, does not reach its output.
+ *
+ *   batch, total_q, total_k      1..65535; rows of q/out and of k/v (>= 0; total_q == 0 does nothing)
+ *   max_q                        an upper bound of the sequences' query rows (rows past it are not
+ *                                computed)
+ *   in_dtype                     SSM_BF16; SSM_F32 returns SSM_ERR_UNSUPPORTED
+ *   q, k, v                      views as above       cu_q, cu_k: [batch + 1] int32, not decreasing
+ *   scale                        finite, > 0
+ *   out                          view [total_q][H][D] in out_dtype, 16-byte aligned, strides
+ *                                multiples of 8 elements       lse: NULL or [total_q][H] float32
+ */
+int attn_prefill(int batch, int64_t total_q, int64_t total_k, int max_q, int n_q_heads, int n_kv_heads,
+                 int head_dim, ssm_dtype_t in_dtype, ssm_dtype_t out_dtype,
+                 const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                 const void* k, int64_t k_stride_t, int64_t k_stride_h,
+                 const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                 const int32_t* cu_q, const int32_t* cu_k, float scale,
+                 void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse, void* cuda_stream);
+
+/* Bytes of device workspace attn_decode_step needs for these sizes (0 on a bad size): the partial
+ * maxima, sums and outputs of the pieces into which the long axis is cut. */
+size_t attn_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim, int max_len);
+
+/*
+ * attn_decode_step -- one query token per request against its whole cached sequence (the token's
+ * own key and value appended before).  Equals the last row of attn_prefill over the cached rows.
+ *
+ *   batch                1..65535 requests
+ *   q                    view [batch][H][D] bf16       lens: [batch] int32, tokens cached for each;
+ *                        0 gives zeros and lse -inf.  A length below 0, above max_len or past the
+ *                        table's row is cut to the range and sets SSM_DEV_BAD_INDEX.
+ *   max_len              an upper bound of lens, >= 1
+ *   cache                as above; a page outside [0, n_pages) counts as not visible and sets
+ *                        SSM_DEV_BAD_INDEX
+ *   out                  view [batch][H][D] in out_dtype, 16-byte aligned, strides multiples of 8
+ *                        elements       lse: NULL or [batch][H] float32
+ *   workspace            at least attn_decode_workspace_bytes(...) bytes, 16-byte aligned (NULL
+ *                        allowed where that is 0); its contents on entry do not matter.  Calls that
+ *                        share a workspace must not overlap on the GPU.
+ */
+int attn_decode_step(int batch, int n_q_heads, int n_kv_heads, int head_dim, ssm_dtype_t in_dtype,
+                     ssm_dtype_t out_dtype, const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                     ssm_dtype_t cache_dtype, const void* k_cache, const void* v_cache,
+                     const float* k_scale, const float* v_scale, int n_pages, int page_size,
+                     const int32_t* page_table, int64_t table_stride, int n_table, const int32_t* lens,
+                     int max_len, float scale, void* out, int64_t out_stride_t, int64_t out_stride_h,
+                     float* lse, void* workspace, size_t workspace_bytes, void* cuda_stream);
 
 /*
  * ssm_selftest_expire_wait -- a diagnostic with no counterpart in the pages: launches one

@@ -716,3 +716,332 @@ int ssm_device_status(uint32_t* status, int clear) {
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------ attention
+namespace {
+
+// The parts of an attention call that several entry points share; each returns SSM_OK or fails.
+int check_heads(const char* fn, int n_q, int n_kv, int dim) {
+    if (n_kv < 1 || n_kv > 4096 || n_q < 1 || n_q > 65535 || n_q % n_kv != 0)
+        return fail(SSM_ERR_INVALID_ARG, "%s: %d query heads over %d kv heads", fn, n_q, n_kv);
+    if (dim < 16 || dim > 128 || dim % 16 != 0)
+        return fail(SSM_ERR_UNSUPPORTED, "%s: head_dim %d unsupported (multiples of 16 up to 128)", fn, dim);
+    return SSM_OK;
+}
+
+int check_view(const char* fn, const char* name, const void* p, int64_t st, int64_t sh, int dim) {
+    if (!p) return fail(SSM_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+    if (st < dim || sh < dim) return fail(SSM_ERR_INVALID_ARG, "%s: a stride of %s is below head_dim", fn, name);
+    if (!aligned(p, 16) || st % 8 != 0 || sh % 8 != 0)
+        return fail(SSM_ERR_MISALIGNED, "%s: %s must be 16-byte aligned with strides that are multiples of 8", fn, name);
+    return SSM_OK;
+}
+
+// An output's heads may not overlap inside a token, nor its tokens.
+int check_out_view(const char* fn, const char* name, const void* p, int64_t n, int64_t st, int64_t sh, int heads, int dim) {
+    const int rc = check_view(fn, name, p, st, sh, dim);
+    if (rc != SSM_OK) return rc;
+    const bool rows_apart = n <= 1 || st >= (int64_t)(heads - 1) * sh + dim;        // [token][head]
+    const bool heads_apart = heads <= 1 || sh >= (n - 1) * st + dim;                // [head][token]
+    if (!rows_apart && !heads_apart)
+        return fail(SSM_ERR_INVALID_ARG, "%s: the strides of %s let rows overlap", fn, name);
+    return SSM_OK;
+}
+
+int check_cache(const char* fn, int cache_dtype, const void* k, const void* v, const float* ks, const float* vs,
+                int n_pages, int page_size) {
+    if (cache_dtype != SSM_BF16 && cache_dtype != SSM_I8)
+        return fail(cache_dtype == SSM_F32 ? SSM_ERR_UNSUPPORTED : SSM_ERR_INVALID_ARG,
+                    "%s: the cache holds SSM_BF16 or SSM_I8 rows", fn);
+    if (n_pages < 1 || page_size < 1) return fail(SSM_ERR_INVALID_ARG, "%s: n_pages %d, page_size %d", fn, n_pages, page_size);
+    if (page_size % 16 != 0 || page_size > 4096)
+        return fail(SSM_ERR_UNSUPPORTED, "%s: page_size %d unsupported (multiples of 16 up to 4096)", fn, page_size);
+    if ((int64_t)n_pages * page_size >= (1LL << 31))
+        return fail(SSM_ERR_UNSUPPORTED, "%s: %d pages of %d tokens pass 2^31 slots", fn, n_pages, page_size);
+    if (!k || !v) return fail(SSM_ERR_INVALID_ARG, "%s: a cache pointer is NULL", fn);
+    if (cache_dtype == SSM_I8 && (!ks || !vs)) return fail(SSM_ERR_INVALID_ARG, "%s: an int8 cache needs k_scale and v_scale", fn);
+    if (cache_dtype == SSM_BF16 && (ks || vs)) return fail(SSM_ERR_INVALID_ARG, "%s: a bf16 cache has no scales", fn);
+    if (!aligned(k, 16) || !aligned(v, 16) || (ks && !aligned(ks, 16)) || (vs && !aligned(vs, 16)))
+        return fail(SSM_ERR_MISALIGNED, "%s: the caches and their scales must be 16-byte aligned", fn);
+    return SSM_OK;
+}
+
+int check_table(const char* fn, const int32_t* table, int64_t stride, int n_table) {
+    if (!table) return fail(SSM_ERR_INVALID_ARG, "%s: page_table is NULL", fn);
+    if (n_table < 1 || stride < n_table)
+        return fail(SSM_ERR_INVALID_ARG, "%s: page_table rows of %d entries with stride %lld", fn, n_table, (long long)stride);
+    if (!aligned(table, 4)) return fail(SSM_ERR_MISALIGNED, "%s: page_table is not element aligned", fn);
+    return SSM_OK;
+}
+
+ssm::AttnCache make_cache(const void* k, const void* v, const float* ks, const float* vs, int n_pages, int page_size,
+                          int n_kv, int dim) {
+    return ssm::AttnCache{k, v, ks, vs, n_pages, page_size, n_kv, dim};
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_rope_table(int64_t n_pos, int half, const double* inv_freq, double scale, float* cos_out, float* sin_out,
+                    void* cuda_stream) {
+    static const char* fn = "attn_rope_table";
+    g_err[0] = 0;
+    if (n_pos < 1 || n_pos > (1LL << 26)) return fail(SSM_ERR_INVALID_ARG, "%s: n_pos %lld not in [1, 2^26]", fn, (long long)n_pos);
+    if (half < 1 || half > 64) return fail(SSM_ERR_INVALID_ARG, "%s: half %d not in [1, 64]", fn, half);
+    if (!inv_freq || !cos_out || !sin_out) return fail(SSM_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+    if (!(scale - scale == 0)) return fail(SSM_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+    if (!aligned(cos_out, 4) || !aligned(sin_out, 4)) return fail(SSM_ERR_MISALIGNED, "%s: a table is not element aligned", fn);
+    ssm::AttnRopeArgs a{};
+    for (int i = 0; i < half; ++i) {
+        if (!(inv_freq[i] - inv_freq[i] == 0)) return fail(SSM_ERR_INVALID_ARG, "%s: inv_freq[%d] is not finite", fn, i);
+        a.inv_freq[i] = inv_freq[i];
+    }
+    a.n_pos = n_pos;
+    a.half = half;
+    a.scale = scale;
+    a.cos = cos_out;
+    a.sin = sin_out;
+    const char* why = "";
+    if (ssm::launch_attn_rope_table(a, static_cast<cudaStream_t>(cuda_stream), &why) != 0)
+        return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
+    return SSM_OK;
+}
+
+int attn_append(int64_t n_tokens, int n_q_heads, int n_kv_heads, int head_dim, int rot_dim, int interleaved,
+                const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                const void* k, int64_t k_stride_t, int64_t k_stride_h,
+                const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                const int32_t* positions, const float* cos, const float* sin, int64_t n_pos,
+                const int32_t* slots, ssm_dtype_t cache_dtype, void* k_cache, void* v_cache,
+                float* k_scale, float* v_scale, int n_pages, int page_size,
+                void* q_out, int64_t qo_stride_t, int64_t qo_stride_h,
+                void* k_out, int64_t ko_stride_t, int64_t ko_stride_h, void* cuda_stream) {
+    static const char* fn = "attn_append";
+    g_err[0] = 0;
+    int rc;
+    if (n_tokens < 0 || n_tokens >= (1LL << 31)) return fail(SSM_ERR_INVALID_ARG, "%s: n_tokens %lld not in [0, 2^31)", fn, (long long)n_tokens);
+    if ((rc = check_heads(fn, n_q_heads, n_kv_heads, head_dim)) != SSM_OK) return rc;
+    if (rot_dim < 0 || rot_dim > head_dim) return fail(SSM_ERR_INVALID_ARG, "%s: rot_dim %d not in [0, head_dim]", fn, rot_dim);
+    if (rot_dim % 8 != 0) return fail(SSM_ERR_UNSUPPORTED, "%s: rot_dim %d is not a multiple of 8", fn, rot_dim);
+    if ((rc = check_cache(fn, cache_dtype, k_cache, v_cache, k_scale, v_scale, n_pages, page_size)) != SSM_OK) return rc;
+    if (n_tokens == 0) return SSM_OK;
+    if ((rc = check_view(fn, "k", k, k_stride_t, k_stride_h, head_dim)) != SSM_OK) return rc;
+    if ((rc = check_view(fn, "v", v, v_stride_t, v_stride_h, head_dim)) != SSM_OK) return rc;
+    if ((q == nullptr) != (q_out == nullptr)) return fail(SSM_ERR_INVALID_ARG, "%s: q and q_out go together", fn);
+    if (q && (rc = check_view(fn, "q", q, q_stride_t, q_stride_h, head_dim)) != SSM_OK) return rc;
+    if (q && (rc = check_out_view(fn, "q_out", q_out, n_tokens, qo_stride_t, qo_stride_h, n_q_heads, head_dim)) != SSM_OK) return rc;
+    if (k_out && (rc = check_out_view(fn, "k_out", k_out, n_tokens, ko_stride_t, ko_stride_h, n_kv_heads, head_dim)) != SSM_OK) return rc;
+    if (q && q_out == q && (qo_stride_t != q_stride_t || qo_stride_h != q_stride_h))
+        return fail(SSM_ERR_INVALID_ARG, "%s: q_out is q with other strides", fn);
+    if (k_out && k_out == k && (ko_stride_t != k_stride_t || ko_stride_h != k_stride_h))
+        return fail(SSM_ERR_INVALID_ARG, "%s: k_out is k with other strides", fn);
+    if (!slots) return fail(SSM_ERR_INVALID_ARG, "%s: slots is NULL", fn);
+    if (rot_dim > 0 && (!positions || !cos || !sin || n_pos < 1))
+        return fail(SSM_ERR_INVALID_ARG, "%s: a rotation needs positions, cos, sin and n_pos", fn);
+    if (!aligned(slots, 4) || (positions && !aligned(positions, 4)) || (rot_dim > 0 && (!aligned(cos, 16) || !aligned(sin, 16))))
+        return fail(SSM_ERR_MISALIGNED, "%s: cos and sin must be 16-byte aligned, positions and slots element aligned", fn);
+    int serr = 0;
+    unsigned int* status = status_ptr(&serr);
+    if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
+    ssm::AttnAppendArgs a{};
+    a.n_tokens = n_tokens;
+    a.n_q = q ? n_q_heads : 0;
+    a.rot = rot_dim;
+    a.interleaved = interleaved != 0;
+    a.q = q;
+    a.q_st = q_stride_t;
+    a.q_sh = q_stride_h;
+    a.k = k;
+    a.k_st = k_stride_t;
+    a.k_sh = k_stride_h;
+    a.v = v;
+    a.v_st = v_stride_t;
+    a.v_sh = v_stride_h;
+    a.positions = positions;
+    a.cos = cos;
+    a.sin = sin;
+    a.n_pos = n_pos;
+    a.slots = slots;
+    a.c = make_cache(k_cache, v_cache, k_scale, v_scale, n_pages, page_size, n_kv_heads, head_dim);
+    a.q_out = q_out;
+    a.qo_st = qo_stride_t;
+    a.qo_sh = qo_stride_h;
+    a.k_out = k_out;
+    a.ko_st = ko_stride_t;
+    a.ko_sh = ko_stride_h;
+    a.status = status;
+    const char* why = "";
+    if (ssm::launch_attn_append(a, cache_dtype == SSM_I8, static_cast<cudaStream_t>(cuda_stream), &why) != 0)
+        return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
+    return SSM_OK;
+}
+
+int attn_cache_read(int batch, int64_t n_tokens, int n_kv_heads, int head_dim, ssm_dtype_t cache_dtype,
+                    const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                    int n_pages, int page_size, const int32_t* page_table, int64_t table_stride, int n_table,
+                    const int32_t* cu_len, const int32_t* first, ssm_dtype_t out_dtype,
+                    void* k_out, void* v_out, void* cuda_stream) {
+    static const char* fn = "attn_cache_read";
+    g_err[0] = 0;
+    int rc;
+    if (batch < 1 || batch > 65535) return fail(SSM_ERR_INVALID_ARG, "%s: batch %d not in [1, 65535]", fn, batch);
+    if (n_tokens < 0 || n_tokens >= (1LL << 31)) return fail(SSM_ERR_INVALID_ARG, "%s: n_tokens %lld not in [0, 2^31)", fn, (long long)n_tokens);
+    if ((rc = check_heads(fn, n_kv_heads, n_kv_heads, head_dim)) != SSM_OK) return rc;
+    if (!dtype_ok(out_dtype)) return fail(SSM_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+    if ((rc = check_cache(fn, cache_dtype, k_cache, v_cache, k_scale, v_scale, n_pages, page_size)) != SSM_OK) return rc;
+    if ((rc = check_table(fn, page_table, table_stride, n_table)) != SSM_OK) return rc;
+    if (!cu_len) return fail(SSM_ERR_INVALID_ARG, "%s: cu_len is NULL", fn);
+    if (n_tokens == 0) return SSM_OK;
+    if (!k_out || !v_out) return fail(SSM_ERR_INVALID_ARG, "%s: an output is NULL", fn);
+    if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(cu_len, 4) || (first && !aligned(first, 4)))
+        return fail(SSM_ERR_MISALIGNED, "%s: the outputs must be 16-byte aligned, cu_len and first element aligned", fn);
+    int serr = 0;
+    unsigned int* status = status_ptr(&serr);
+    if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
+    ssm::AttnReadArgs a{};
+    a.batch = batch;
+    a.n_table = n_table;
+    a.n_tokens = n_tokens;
+    a.table_stride = table_stride;
+    a.c = make_cache(k_cache, v_cache, k_scale, v_scale, n_pages, page_size, n_kv_heads, head_dim);
+    a.page_table = page_table;
+    a.cu_len = cu_len;
+    a.first = first;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.status = status;
+    const char* why = "";
+    if (ssm::launch_attn_read(a, cache_dtype == SSM_I8, out_dtype == SSM_BF16, static_cast<cudaStream_t>(cuda_stream),
+                              &why) != 0)
+        return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
+    return SSM_OK;
+}
+
+int attn_prefill(int batch, int64_t total_q, int64_t total_k, int max_q, int n_q_heads, int n_kv_heads,
+                 int head_dim, ssm_dtype_t in_dtype, ssm_dtype_t out_dtype,
+                 const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                 const void* k, int64_t k_stride_t, int64_t k_stride_h,
+                 const void* v, int64_t v_stride_t, int64_t v_stride_h,
+                 const int32_t* cu_q, const int32_t* cu_k, float scale,
+                 void* out, int64_t out_stride_t, int64_t out_stride_h, float* lse, void* cuda_stream) {
+    static const char* fn = "attn_prefill";
+    g_err[0] = 0;
+    int rc;
+    if (batch < 1 || batch > 65535) return fail(SSM_ERR_INVALID_ARG, "%s: batch %d not in [1, 65535]", fn, batch);
+    if (total_q < 0 || total_q > (1LL << 30) || total_k < 0 || total_k > (1LL << 30))
+        return fail(SSM_ERR_INVALID_ARG, "%s: total_q %lld, total_k %lld not in [0, 2^30]", fn, (long long)total_q, (long long)total_k);
+    if (max_q < 0) return fail(SSM_ERR_INVALID_ARG, "%s: max_q %d < 0", fn, max_q);
+    if ((rc = check_heads(fn, n_q_heads, n_kv_heads, head_dim)) != SSM_OK) return rc;
+    if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return fail(SSM_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+    if (in_dtype != SSM_BF16) return fail(SSM_ERR_UNSUPPORTED, "%s: q, k and v must be bf16", fn);
+    if (!(scale > 0.0f) || !(scale - scale == 0.0f)) return fail(SSM_ERR_INVALID_ARG, "%s: scale must be finite and > 0", fn);
+    if (!cu_q || !cu_k) return fail(SSM_ERR_INVALID_ARG, "%s: cu_q or cu_k is NULL", fn);
+    if (total_q == 0 || max_q == 0) return SSM_OK;
+    if ((rc = check_view(fn, "q", q, q_stride_t, q_stride_h, head_dim)) != SSM_OK) return rc;
+    if (total_k > 0) {
+        if ((rc = check_view(fn, "k", k, k_stride_t, k_stride_h, head_dim)) != SSM_OK) return rc;
+        if ((rc = check_view(fn, "v", v, v_stride_t, v_stride_h, head_dim)) != SSM_OK) return rc;
+    }
+    if ((rc = check_out_view(fn, "out", out, total_q, out_stride_t, out_stride_h, n_q_heads, head_dim)) != SSM_OK) return rc;
+    if (!aligned(cu_q, 4) || !aligned(cu_k, 4) || (lse && !aligned(lse, 4)))
+        return fail(SSM_ERR_MISALIGNED, "%s: cu_q, cu_k or lse is not element aligned", fn);
+    int serr = 0;
+    unsigned int* status = status_ptr(&serr);
+    if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
+    ssm::AttnPrefillArgs a{};
+    a.batch = batch;
+    a.max_q = max_q < total_q ? max_q : (int)total_q;
+    a.n_q = n_q_heads;
+    a.n_kv = n_kv_heads;
+    a.dim = head_dim;
+    a.total_q = total_q;
+    a.total_k = total_k;
+    a.q = q;
+    a.q_st = q_stride_t;
+    a.q_sh = q_stride_h;
+    a.k = k;
+    a.k_st = k_stride_t;
+    a.k_sh = k_stride_h;
+    a.v = v;
+    a.v_st = v_stride_t;
+    a.v_sh = v_stride_h;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.scale = scale;
+    a.out = out;
+    a.o_st = out_stride_t;
+    a.o_sh = out_stride_h;
+    a.lse = lse;
+    a.status = status;
+    const char* why = "";
+    if (ssm::launch_attn_prefill(a, out_dtype == SSM_BF16, static_cast<cudaStream_t>(cuda_stream), &why) != 0)
+        return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
+    return SSM_OK;
+}
+
+size_t attn_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim, int max_len) {
+    if (batch < 1 || batch > 65535 || n_kv_heads < 1 || n_kv_heads > 4096 || n_q_heads < 1 || n_q_heads > 65535 ||
+        n_q_heads % n_kv_heads != 0 || head_dim < 16 || head_dim > 128 || head_dim % 16 != 0 || max_len < 1)
+        return 0;
+    return ssm::attn_decode_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_len);
+}
+
+int attn_decode_step(int batch, int n_q_heads, int n_kv_heads, int head_dim, ssm_dtype_t in_dtype,
+                     ssm_dtype_t out_dtype, const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                     ssm_dtype_t cache_dtype, const void* k_cache, const void* v_cache,
+                     const float* k_scale, const float* v_scale, int n_pages, int page_size,
+                     const int32_t* page_table, int64_t table_stride, int n_table, const int32_t* lens,
+                     int max_len, float scale, void* out, int64_t out_stride_t, int64_t out_stride_h,
+                     float* lse, void* workspace, size_t workspace_bytes, void* cuda_stream) {
+    static const char* fn = "attn_decode_step";
+    g_err[0] = 0;
+    int rc;
+    if (batch < 1 || batch > 65535) return fail(SSM_ERR_INVALID_ARG, "%s: batch %d not in [1, 65535]", fn, batch);
+    if (max_len < 1) return fail(SSM_ERR_INVALID_ARG, "%s: max_len %d < 1", fn, max_len);
+    if ((rc = check_heads(fn, n_q_heads, n_kv_heads, head_dim)) != SSM_OK) return rc;
+    if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return fail(SSM_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+    if (in_dtype != SSM_BF16) return fail(SSM_ERR_UNSUPPORTED, "%s: q must be bf16", fn);
+    if (!(scale > 0.0f) || !(scale - scale == 0.0f)) return fail(SSM_ERR_INVALID_ARG, "%s: scale must be finite and > 0", fn);
+    if ((rc = check_view(fn, "q", q, q_stride_t, q_stride_h, head_dim)) != SSM_OK) return rc;
+    if ((rc = check_cache(fn, cache_dtype, k_cache, v_cache, k_scale, v_scale, n_pages, page_size)) != SSM_OK) return rc;
+    if ((rc = check_table(fn, page_table, table_stride, n_table)) != SSM_OK) return rc;
+    if (!lens) return fail(SSM_ERR_INVALID_ARG, "%s: lens is NULL", fn);
+    if ((rc = check_out_view(fn, "out", out, batch, out_stride_t, out_stride_h, n_q_heads, head_dim)) != SSM_OK) return rc;
+    if (!aligned(lens, 4) || (lse && !aligned(lse, 4)))
+        return fail(SSM_ERR_MISALIGNED, "%s: lens or lse is not element aligned", fn);
+    const size_t need = ssm::attn_decode_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_len);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(SSM_ERR_INVALID_ARG, "%s: workspace of %zu bytes given, %zu needed", fn,
+                    workspace ? workspace_bytes : (size_t)0, need);
+    if (need > 0 && !aligned(workspace, 16)) return fail(SSM_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", fn);
+    int serr = 0;
+    unsigned int* status = status_ptr(&serr);
+    if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
+    ssm::AttnDecodeArgs a{};
+    a.batch = batch;
+    a.n_q = n_q_heads;
+    a.n_table = n_table;
+    a.max_len = max_len;
+    a.q = q;
+    a.q_st = q_stride_t;
+    a.q_sh = q_stride_h;
+    a.table_stride = table_stride;
+    a.c = make_cache(k_cache, v_cache, k_scale, v_scale, n_pages, page_size, n_kv_heads, head_dim);
+    a.page_table = page_table;
+    a.lens = lens;
+    a.scale = scale;
+    a.out = out;
+    a.o_st = out_stride_t;
+    a.o_sh = out_stride_h;
+    a.lse = lse;
+    a.workspace = workspace;
+    a.status = status;
+    const char* why = "";
+    if (ssm::launch_attn_decode(a, cache_dtype == SSM_I8, out_dtype == SSM_BF16, static_cast<cudaStream_t>(cuda_stream),
+                                &why) != 0)
+        return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
+    return SSM_OK;
+}
+
+}  // extern "C"

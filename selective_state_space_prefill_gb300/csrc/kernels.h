@@ -188,6 +188,80 @@ struct SsdDecodeArgs {
     unsigned int* status;
 };
 
+// ------------------------------------------------------------------ attention
+// Paged cache [n_pages][n_kv][page_size][dim]; scales [n_pages][n_kv][page_size] (int8 rows only).
+struct AttnCache {
+    const void *k, *v;
+    const float *k_scale, *v_scale;
+    int n_pages, page_size, n_kv, dim;
+};
+
+struct AttnRopeArgs {
+    int64_t n_pos;
+    int half;
+    double scale;
+    float *cos, *sin;
+    double inv_freq[64];
+};
+
+struct AttnAppendArgs {
+    int64_t n_tokens;
+    int n_q, rot, interleaved;
+    const void *q, *k, *v;
+    int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
+    const int32_t* positions;
+    const float *cos, *sin;
+    int64_t n_pos;
+    const int32_t* slots;
+    AttnCache c;                    // written
+    void *q_out, *k_out;
+    int64_t qo_st, qo_sh, ko_st, ko_sh;
+    unsigned int* status;
+};
+
+struct AttnReadArgs {
+    int batch, n_table;
+    int64_t n_tokens, table_stride;
+    AttnCache c;
+    const int32_t *page_table, *cu_len, *first;
+    void *k_out, *v_out;
+    unsigned int* status;
+};
+
+struct AttnPrefillArgs {
+    int batch, max_q, n_q, n_kv, dim;
+    int64_t total_q, total_k;
+    const void *q, *k, *v;
+    int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh;
+    const int32_t *cu_q, *cu_k;
+    float scale;
+    void* out;
+    int64_t o_st, o_sh;
+    float* lse;
+    unsigned int* status;
+};
+
+struct AttnDecodeArgs {
+    int batch, n_q, n_table, max_len;
+    const void* q;
+    int64_t q_st, q_sh, table_stride;
+    AttnCache c;
+    const int32_t *page_table, *lens;
+    float scale;
+    void* out;
+    int64_t o_st, o_sh;
+    float* lse;
+    void* workspace;
+    unsigned int* status;
+};
+
+size_t attn_decode_workspace(int batch, int n_q, int n_kv, int dim, int max_len);
+int launch_attn_rope_table(const AttnRopeArgs& a, cudaStream_t stream, const char** why);
+int launch_attn_append(const AttnAppendArgs& a, bool cache_i8, cudaStream_t stream, const char** why);
+int launch_attn_read(const AttnReadArgs& a, bool cache_i8, bool out_bf16, cudaStream_t stream, const char** why);
+int launch_attn_prefill(const AttnPrefillArgs& a, bool out_bf16, cudaStream_t stream, const char** why);
+int launch_attn_decode(const AttnDecodeArgs& a, bool cache_i8, bool out_bf16, cudaStream_t stream, const char** why);
+
 // Each returns 0 on success, or -1 with *why set to a static message.
 int launch_ssd_prefill(const SsdArgs& a, bool out_bf16, cudaStream_t stream, const char** why);
 int launch_ssd_decode(const SsdDecodeArgs& a, bool in_bf16, bool out_bf16, cudaStream_t stream, const char** why);
