@@ -1,77 +1,498 @@
-// attn_prefill.cu -- causal attention over packed prompts with grouped heads (sm_103a).
+// attn_prefill.cu -- causal attention over packed prompts with grouped heads on the sm_103a
+// tensor cores (tcgen05).
 //
-// Row i of a sequence with Lq queries and Lk keys sees the keys j <= i + Lk - Lq.  One pass over
-// them carries the running maximum m and sum l of the softmax:
-//   m' = max(m, s_j); l = l e^(m-m') + e^(s_j-m'); o = o e^(m-m') + e^(s_j-m') v_j
-// and out = o / l, lse = m + ln l.
+// Row i of a sequence with Lq queries and Lk keys sees the keys j < see_i = min(Lk, i + Lk - Lq + 1).
+// One pass over the keys in blocks of 128 carries, per row, a reference m of the scores, the sum l
+// and the output o, all in fp32:
+//   p_j = 2^(c (s_j - m)), c = scale log2(e);   l += sum p_j;   o += sum p_j v_j
+// out = o / l, lse = ln 2 (c m + log2 l).  Any m gives the same quotient; it is raised to the
+// running maximum only when that has grown by more than 2^8 (kSlack, in units of c s), so that p
+// stays below 2^8 and o is seldom rescaled.  p is rounded to bf16 for the second product, as the
+// tensor cores take it with bf16 values; l sums it unrounded.
 //
-// A warp owns one (row, head) and its lanes the head's dimensions, so each key costs a warp sum.
+// Two dense products per block bound it: 2 x 128 x 128 x D multiply-adds on the tensor cores and
+// 128 x 128 exponentials.  The design keeps the tensor cores fed while the exponentials run:
+//   * a CTA owns 256 query rows of one head as two tiles of 128; while one tile's softmax runs, the
+//     tensor cores work on the other's products;
+//   * warps 0-3 and 4-7: the softmax of tile 0 and 1, a thread per row (TMEM lane), the row's 128
+//     scores in registers; they write p over their scores in TMEM, where tcgen05.mma takes it as
+//     its A operand, and rescale and store o;
+//   * warp 8: TMA loads of the two query tiles and a ring of key and value blocks;
+//   * warp 9: issues the MMAs: per block and tile o += P V, then the next block's S = Q K^T;
+//   * warps 10-11: make the value rows of blocks that some row does not wholly see harmless: the
+//     product multiplies an unseen value by 0, which a NaN or an infinity survives.  Rows past the
+//     sequence are zeroed; non-finite values are zeroed and noted (the first key of each column
+//     that holds +inf, -inf, NaN), and the rows that do see them get them back at the end.
+// TMEM: scores of tile t at column 128 t, output at 256 + 128 t; all 512 columns, one CTA per SM.
+// The grid runs the longest rows first (the last tiles of every head), so the tail is short.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "tcgen05.cuh"
 
 namespace ssm {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kM = 128;                 // query rows per tile
+constexpr int kN = 128;                 // keys per block
+constexpr int kThreads = 384;
+constexpr float kSlack = 8.0f;
 
-__device__ __forceinline__ float4 load4(const void* base, int64_t at, bool on) {
-    if (!on) return make_float4(0.f, 0.f, 0.f, 0.f);
-    const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(base) + at);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+template <int DP>                       // head_dim padded to 64 or 128
+struct Geo {
+    static constexpr int kTile = 128 * DP * 2;                  // bytes of 128 rows
+    static constexpr int kSlots = DP == 128 ? 4 : 8;            // ring of key and value blocks
+    static constexpr int kOffKV = 2 * kTile;
+    static constexpr int kOffBar = kOffKV + kSlots * kTile;
+    // q_full[2], s_full[2], p_full[2], o_full[2], v_raw[4], v_ok[4], kv_full[slots], kv_empty[slots],
+    // TMEM address
+    static constexpr int kBars = 16 + 2 * kSlots;
+    static constexpr int kOffBad = kOffBar + kBars * 8 + 16;    // first bad key per column: [3][DP]
+    static constexpr int kSmem = kOffBad + 3 * DP * 4 + 1024;   // + slack to align to 1024
+    // tcgen05.mma kind::f16 instruction descriptors: fp32 accumulator, bf16 operands, M = 128;
+    // scores: N = 128, both K-major; output: N = DP, B (values) MN-major
+    static constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kN >> 3) << 17) | (8u << 24);
+    static constexpr uint32_t kIdescO =
+        (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(DP >> 3) << 17) | (8u << 24);
+};
+
+// o += P V with P (bf16 pairs) in TMEM.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
-template <typename Tout>
-__global__ void __launch_bounds__(kThreads)
-k_attn_prefill(const AttnPrefillArgs a) {
-    const int b = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31;
-    const int i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
-    const int64_t lq = min((int64_t)a.cu_q[b + 1], a.total_q) - q0, lk = min((int64_t)a.cu_k[b + 1], a.total_k) - k0;
-    if (i >= lq || i >= a.max_q || q0 < 0 || k0 < 0) return;
-    const int d = 4 * lane, hk = h / (a.n_q / a.n_kv);
-    const bool on = d < a.dim;
-    float4 q = load4(a.q, (q0 + i) * a.q_st + h * a.q_sh + d, on);
-    const float s2 = a.scale * kLog2e;
-    const int64_t see = min(lk, i + lk - lq + 1);
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t j = 0; j < see; ++j) {
-        const float4 k = load4(a.k, (k0 + j) * a.k_st + hk * a.k_sh + d, on);
-        const float4 v = load4(a.v, (k0 + j) * a.v_st + hk * a.v_sh + d, on);
-        float s = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+// Descriptor of an MN-major tile with 128-byte swizzling (rows of 128 bytes run along K, groups of 8
+// rows 1024 bytes apart, the second 64 columns 16 KB on).
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(16384u >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
+}
+
+// 32 columns of this thread's TMEM lane, not waited for.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// Orders the uses of 32 loaded registers after the wait before it.
+__device__ __forceinline__ void pin32(uint32_t* r) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int DP, typename Tout>
+__global__ void __launch_bounds__(kThreads, 1)
+k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+               const __grid_constant__ CUtensorMap tm_v, const AttnPrefillArgs a) {
+    using G = Geo<DP>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ int s_err, s_bad;
+    const int h = (int)(blockIdx.x % (unsigned)a.n_q), b = blockIdx.y;
+    const int row0 = (int)((gridDim.x - 1 - blockIdx.x) / (unsigned)a.n_q) * 2 * kM;
+    // the sequence's rows, kept inside the tensors whatever cu_q and cu_k hold
+    const int q0 = min(max(a.cu_q[b], 0), (int)a.total_q), k0 = min(max(a.cu_k[b], 0), (int)a.total_k);
+    const int lq = min(min(a.cu_q[b + 1], (int)a.total_q) - q0, a.max_q);
+    const int lq_all = min(a.cu_q[b + 1], (int)a.total_q) - q0;
+    const int lk = max(min(a.cu_k[b + 1], (int)a.total_k) - k0, 0);
+    if (row0 >= lq) return;                              // the same for the whole block
+    const int off = lk - lq_all;                         // row i sees keys < min(lk, i + off + 1)
+    // blocks of keys that tile t's rows see
+    auto blocks = [&](int t) -> int {
+        const int r = row0 + t * kM;
+        if (r >= lq) return 0;
+        const int see = min(lk, min(lq - 1, r + kM - 1) + off + 1);
+        return see <= 0 ? 0 : (see + kN - 1) / kN;
+    };
+    const int n0 = blocks(0), n1 = blocks(1), nb = max(n0, n1);
+    // the first block that some row of the CTA's tiles does not wholly see; as 256 neighbouring rows'
+    // limits span at most 255 keys, at most three blocks are left from it on
+    const int whole = min(lk, row0 + off + 1);
+    const int mask_from = whole <= 0 ? 0 : whole / kN;
+
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
+    uint64_t* s_full = q_full + 2;
+    uint64_t* p_full = s_full + 2;
+    uint64_t* o_full = p_full + 2;
+    uint64_t* v_raw = o_full + 2;       // [4], one use each: a value block to be cleaned has landed
+    uint64_t* v_ok = v_raw + 4;         // [4], one use each: it is clean
+    uint64_t* kv_full = v_ok + 4;
+    uint64_t* kv_empty = kv_full + G::kSlots;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + G::kSlots);
+    int* bad = reinterpret_cast<int*>(smem + G::kOffBad);       // [3][DP]: +inf, -inf, NaN
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        s_err = 0;
+        s_bad = 0;
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_full[t], 1);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 4);           // one arrival per softmax warp
+            mbar_init(&o_full[t], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&v_raw[i], 1);
+            mbar_init(&v_ok[i], 2);             // one arrival per cleaning warp
+        }
+        for (int s = 0; s < G::kSlots; ++s) {
+            mbar_init(&kv_full[s], 1);
+            mbar_init(&kv_empty[s], 1);
+        }
+        fence_barrier_init();
+    }
+    for (int i = threadIdx.x; i < 3 * DP; i += kThreads) bad[i] = 0x7fffffff;
+    if (warp == 9) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto expired = [&]() {
+        s_err = 1;
+        atomicOr(a.status, 1u);
+    };
+
+    if (warp == 8 && lane == 0 && nb > 0) {
+        // ---- TMA producer: the query tiles, then K_0, V_0, K_1, V_1, ... through the ring
+        const int hk = h / (a.n_q / a.n_kv);
+        for (int t = 0; t < 2; ++t) {
+            if ((t ? n1 : n0) == 0) continue;
+            mbar_arrive_expect_tx(&q_full[t], G::kTile);
+            for (int c = 0; c < DP / 64; ++c)
+                tma_load_3d(smem + t * G::kTile + c * 16384, &tm_q, &q_full[t], 64 * c, h, q0 + row0 + t * kM);
+        }
+        int it = 0;
+        for (; it < 2 * nb; ++it) {
+            const int s = it % G::kSlots;
+            if (it >= G::kSlots && !mbar_wait_bounded(&kv_empty[s], (uint32_t)((it / G::kSlots + 1) & 1))) {
+                expired();
+                break;
+            }
+            unsigned char* dst = smem + G::kOffKV + s * G::kTile;
+            uint64_t* full = &kv_full[s];
+            if ((it & 1) && (it >> 1) >= mask_from) {     // by way of the cleaning warps
+                mbar_arrive(full);
+                full = &v_raw[(it >> 1) - mask_from];
+            }
+            mbar_arrive_expect_tx(full, G::kTile);
+            for (int c = 0; c < DP / 64; ++c)
+                tma_load_3d(dst + c * 16384, it & 1 ? &tm_v : &tm_k, full, 64 * c, hk, k0 + (it >> 1) * kN);
+        }
+        // tail: every load has landed and the MMAs' last releases have arrived before the CTA ends
+        for (int u = max(0, it - G::kSlots); u < it; ++u) {
+            const bool raw = (u & 1) && (u >> 1) >= mask_from;
+            if (!mbar_wait_bounded(raw ? &v_raw[(u >> 1) - mask_from] : &kv_full[u % G::kSlots],
+                                   raw ? 0u : (uint32_t)((u / G::kSlots) & 1)))
+                expired();
+            if (!s_err && !mbar_wait_bounded(&kv_empty[u % G::kSlots], (uint32_t)((u / G::kSlots) & 1))) expired();
+        }
+        for (int t = 0; t < 2; ++t)
+            if ((t ? n1 : n0) > 0 && !mbar_wait_bounded(&q_full[t], 0)) expired();
+    } else if (warp == 9 && lane == 0 && nb > 0) {
+        // ---- MMA issuer
+        const int dsteps = a.dim / 16;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok && !mbar_wait_bounded(bar, parity)) {
+                ok = false;
+                expired();
+            }
+        };
+        auto scores = [&](int t, int j) {                // S_t = Q_t K_j^T
+            const uint32_t qa = smem_u32(smem + t * G::kTile);
+            const uint32_t ka = smem_u32(smem + G::kOffKV + ((2 * j) % G::kSlots) * G::kTile);
+            for (int k = 0; k < dsteps; ++k)
+                mma_bf16(tmem + (uint32_t)(128 * t), smem_desc_sw128(qa + (k >> 2) * 16384 + 32 * (k & 3)),
+                         smem_desc_sw128(ka + (k >> 2) * 16384 + 32 * (k & 3)), G::kIdescS, k != 0);
+            mma_commit(&s_full[t]);
+        };
+        wait(&kv_full[0], 0);
+        for (int t = 0; t < 2 && ok; ++t) {
+            if ((t ? n1 : n0) == 0) continue;
+            wait(&q_full[t], 0);
+            tc_fence_after();
+            if (ok) scores(t, 0);
+        }
+        if (ok) mma_commit(&kv_empty[0]);
+        for (int j = 0; j < nb && ok; ++j) {
+            const int vi = 2 * j + 1, ki = 2 * j + 2;
+            wait(&kv_full[vi % G::kSlots], (uint32_t)((vi / G::kSlots) & 1));
+            if (j >= mask_from) wait(&v_ok[j - mask_from], 0);
+            if (j + 1 < nb) wait(&kv_full[ki % G::kSlots], (uint32_t)((ki / G::kSlots) & 1));
+            const uint64_t vd = smem_desc_mn(smem_u32(smem + G::kOffKV + (vi % G::kSlots) * G::kTile));
+            for (int t = 0; t < 2 && ok; ++t) {
+                const int n = t ? n1 : n0;
+                if (j >= n) continue;
+                wait(&p_full[t], (uint32_t)(j & 1));
+                if (!ok) break;
+                tc_fence_after();
+                for (int k = 0; k < kN / 16; ++k)        // 16 keys: 8 columns of P, 2048 bytes of V
+                    mma_bf16_ts(tmem + 256u + (uint32_t)(128 * t), tmem + (uint32_t)(128 * t + 8 * k),
+                                vd + (uint64_t)(2048 >> 4) * k, G::kIdescO, (j | k) != 0);
+                mma_commit(&o_full[t]);
+                if (j + 1 < n) scores(t, j + 1);
+            }
+            if (ok) mma_commit(&kv_empty[vi % G::kSlots]);
+            if (ok && j + 1 < nb) mma_commit(&kv_empty[ki % G::kSlots]);
+        }
+    } else if (warp >= 10) {
+        // ---- value blocks that some row does not wholly see
+        for (int j = mask_from; j < nb; ++j) {
+            const int vi = 2 * j + 1;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&v_raw[j - mask_from], 0))) {
+                expired();
+                break;
+            }
+            unsigned char* v = smem + G::kOffKV + (vi % G::kSlots) * G::kTile;
+            const int rows = lk - j * kN;                // of this sequence; later ones are zeroed
+            for (int i = threadIdx.x - 320; i < G::kTile / 16; i += 64) {
+                const int r = (i >> 3) & 127;
+                uint4* p = reinterpret_cast<uint4*>(v) + i;
+                if (r >= rows) {
+                    *p = make_uint4(0u, 0u, 0u, 0u);
+                    continue;
+                }
+                const uint4 w = *p;
+                uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                bool fine = true;
 #pragma unroll
-        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-        s *= s2;                                     // in units of log 2
-        const float m2 = fmaxf(m, s), r = ex2(m - m2), p = ex2(s - m2);
-        m = m2;
-        l = l * r + p;
-        o.x = o.x * r + p * v.x;
-        o.y = o.y * r + p * v.y;
-        o.z = o.z * r + p * v.z;
-        o.w = o.w * r + p * v.w;
+                for (int e = 0; e < 4; ++e)
+                    fine = fine && (ws[e] & 0x7f80u) != 0x7f80u && (ws[e] & 0x7f800000u) != 0x7f800000u;
+                if (fine) continue;
+                const int col = (i >> 10) * 64 + ((i & 7) ^ (r & 7)) * 8;       // the swizzle undone
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t x = (ws[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                    if ((x & 0x7f80u) != 0x7f80u) continue;
+                    const int kind = x == 0x7f80u ? 0 : (x == 0xff80u ? 1 : 2);
+                    atomicMin(&bad[kind * DP + col + e], j * kN + r);
+                    ws[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                }
+                *p = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+                s_bad = 1;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_ok[j - mask_from]);
+        }
+    } else if (warp < 8) {
+        // ---- softmax of tile t: thread = row
+        const int t = warp >> 2, quarter = warp & 3;
+        const int n = t ? n1 : n0;
+        const int row = row0 + t * kM + 32 * quarter + lane;
+        const int see = row < lq ? min(lk, row + off + 1) : 0;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const uint32_t ts = tmem + lanes + (uint32_t)(128 * t), to = tmem + lanes + 256u + (uint32_t)(128 * t);
+        const float c = a.scale * kLog2e;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s_full[t], (uint32_t)(j & 1)))) {
+                expired();
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t r[128];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32_async(ts + 32u * q, r + 32 * q);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) pin32(r + 32 * q);
+            if (j >= mask_from) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (j * kN + i >= see) r[i] = 0xff800000u;          // -inf
+            }
+            float mx = __uint_as_float(r[0]);
+#pragma unroll
+            for (int i = 1; i < 128; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
+            if (j == 0) {
+                m = mx;
+            } else {
+                const bool up = (mx - m) * c > kSlack;
+                if (__any_sync(0xffffffffu, up)) {
+                    // o belongs to this thread between the previous product's end and the next one's start
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&o_full[t], (uint32_t)((j - 1) & 1)))) {
+                        expired();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const float f = up ? ex2((m - mx) * c) : 1.f;
+                    if (up) m = mx;
+                    l *= f;
+#pragma unroll 1
+                    for (int q = 0; q < DP / 32; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32_async(to + 32u * q, o);
+                        tmem_wait_ld();
+                        pin32(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(to + 32u * q, o);
+                    }
+                }
+            }
+            const float mc = m == -INFINITY ? 0.f : m * c;       // nothing but -inf so far: p = 0
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float p0 = ex2(fmaf(__uint_as_float(r[64 * q + 2 * i]), c, -mc));
+                    const float p1 = ex2(fmaf(__uint_as_float(r[64 * q + 2 * i + 1]), c, -mc));
+                    sum0 += p0;
+                    sum1 += p1;
+                    p[i] = pack_bf16(p0, p1);
+                }
+                tmem_st32(ts + 32u * q, p);
+            }
+            l += sum0 + sum1;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[t]);
+        }
+        if (ok && n > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(&o_full[t], (uint32_t)((n - 1) & 1)))) {
+            expired();
+            ok = false;
+        }
+        tc_fence_after();
+        const bool store = ok && s_err == 0 && row < lq;
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        if (store && a.lse) a.lse[(int64_t)(q0 + row) * a.n_q + h] = l == 0.f ? -INFINITY : kLn2 * (m * c + log2f(l));
+        Tout* out = reinterpret_cast<Tout*>(a.out) + (int64_t)(q0 + row) * a.o_st + (int64_t)h * a.o_sh;
+        const bool any_bad = *(volatile int*)&s_bad != 0;
+#pragma unroll 1
+        for (int q = 0; q < DP / 32; ++q) {
+            uint32_t o[32];
+            __syncwarp();
+            if (n > 0) {
+                tmem_ld32_async(to + 32u * q, o);
+                tmem_wait_ld();
+                pin32(o);
+            }
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * inv;
+            if (any_bad) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int col = 32 * q + i;
+                    if (bad[col] < see) v[i] += INFINITY;
+                    if (bad[DP + col] < see) v[i] -= INFINITY;
+                    if (bad[2 * DP + col] < see) v[i] = NAN;
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {                // eight columns at a time, whole or not at all
+                if (!store || 32 * q + 8 * g >= a.dim) continue;
+                if constexpr (sizeof(Tout) == 2) {
+                    *reinterpret_cast<uint4*>(out + 32 * q + 8 * g) =
+                        make_uint4(pack_bf16(v[8 * g], v[8 * g + 1]), pack_bf16(v[8 * g + 2], v[8 * g + 3]),
+                                   pack_bf16(v[8 * g + 4], v[8 * g + 5]), pack_bf16(v[8 * g + 6], v[8 * g + 7]));
+                } else {
+                    reinterpret_cast<float4*>(out + 32 * q + 8 * g)[0] =
+                        make_float4(v[8 * g], v[8 * g + 1], v[8 * g + 2], v[8 * g + 3]);
+                    reinterpret_cast<float4*>(out + 32 * q + 8 * g)[1] =
+                        make_float4(v[8 * g + 4], v[8 * g + 5], v[8 * g + 6], v[8 * g + 7]);
+                }
+            }
+        }
     }
-    const float inv = see > 0 ? 1.f / l : 0.f;
-    if (on) {
-        Tout* out = reinterpret_cast<Tout*>(a.out) + (q0 + i) * a.o_st + h * a.o_sh + d;
-        out[0] = from_f32<Tout>(o.x * inv);
-        out[1] = from_f32<Tout>(o.y * inv);
-        out[2] = from_f32<Tout>(o.z * inv);
-        out[3] = from_f32<Tout>(o.w * inv);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
-    if (a.lse && lane == 0) a.lse[(q0 + i) * a.n_q + h] = see > 0 ? m * kLn2 + logf(l) : -INFINITY;
+}
+
+// Map over [tokens][heads][dim] bf16 with the given strides: boxes of 128 tokens x one head x 64
+// elements, 128-byte swizzle; elements past dim and rows past the tensor read as zero.
+bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int dim, int64_t st, int64_t sh) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
+    cuuint32_t box[3] = {64, 1, 128};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DP, typename Tout>
+int launch_dp(const AttnPrefillArgs& a, cudaStream_t stream, const char** why) {
+    CUtensorMap mq, mk, mv;
+    // without keys nothing is loaded; the maps then stand over q
+    const bool keys = a.total_k > 0;
+    if (!make_map(&mq, a.q, a.total_q, a.n_q, a.dim, a.q_st, a.q_sh) ||
+        !make_map(&mk, keys ? a.k : a.q, keys ? a.total_k : a.total_q, keys ? a.n_kv : a.n_q, a.dim,
+                  keys ? a.k_st : a.q_st, keys ? a.k_sh : a.q_sh) ||
+        !make_map(&mv, keys ? a.v : a.q, keys ? a.total_k : a.total_q, keys ? a.n_kv : a.n_q, a.dim,
+                  keys ? a.v_st : a.q_st, keys ? a.v_sh : a.q_sh)) {
+        *why = "cuTensorMapEncodeTiled failed (driver entry point missing or layout rejected)";
+        return -1;
+    }
+    auto kern = k_attn_prefill<DP, Tout>;
+    static ContextMemo attr;
+    if (!opt_in_dynamic_smem(attr, kern, Geo<DP>::kSmem, why)) return -1;
+    const int64_t tiles = ((int64_t)a.max_q + 2 * kM - 1) / (2 * kM);
+    if (tiles * a.n_q >= (1LL << 31)) {
+        *why = "heads times query tiles pass the grid";
+        return -1;
+    }
+    const dim3 grid((unsigned)(tiles * a.n_q), (unsigned)a.batch);
+    kern<<<grid, kThreads, Geo<DP>::kSmem, stream>>>(mq, mk, mv, a);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) return 0;
+    *why = cudaGetErrorString(e);
+    return -1;
 }
 
 }  // namespace
 
 int launch_attn_prefill(const AttnPrefillArgs& a, bool out_bf16, cudaStream_t stream, const char** why) {
-    const dim3 grid((unsigned)((a.max_q + 3) / 4), (unsigned)a.n_q, (unsigned)a.batch);
-    if (out_bf16) k_attn_prefill<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-    else k_attn_prefill<float><<<grid, kThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) return 0;
-    *why = cudaGetErrorString(e);
-    return -1;
+    if (a.dim <= 64)
+        return out_bf16 ? launch_dp<64, __nv_bfloat16>(a, stream, why) : launch_dp<64, float>(a, stream, why);
+    return out_bf16 ? launch_dp<128, __nv_bfloat16>(a, stream, why) : launch_dp<128, float>(a, stream, why);
 }
 
 }  // namespace ssm

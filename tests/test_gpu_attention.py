@@ -1,13 +1,13 @@
 """attn_prefill and attn_decode_step against the 64-bit softmax.
 
 The bounds (tests/_attn.py) are those of the documented arithmetic: scores from fp32 sums, weights
-rounded to bf16 for the second product, fp32 accumulation, one rounding of the output.
+rounded for the second product, fp32 accumulation, one rounding of the output.
 """
 import numpy as np
 import pytest
 import torch
 
-from _attn import attend64, check_attention, cu, heads, paged, to64
+from _attn import W_DECODE, W_PREFILL, attend64, check_attention, cu, heads, out_bound, paged, to64
 from selective_state_space_prefill_gb300 import binding as ssm
 
 pytestmark = pytest.mark.gpu
@@ -42,7 +42,7 @@ def test_prefill(ql, kl, H, Hk, D, out_dtype):
                                 max(ql), out_dtype=out_dtype, lse=True)
     torch.cuda.synchronize()
     ref = _prefill_ref(q, k, v, ql, kl, D ** -0.5)
-    check_attention(out, lse, ref, D, out_dtype, f"prefill {ql} {kl}")
+    check_attention(out, lse, ref, D, out_dtype, W_PREFILL, f"prefill {ql} {kl}")
     empty = np.isneginf(ref[1])
     assert (to64(out)[empty] == 0).all()
     assert ssm.device_status() == 0
@@ -57,7 +57,7 @@ def test_prefill_score_ranges(scale, gain):
     k *= torch.linspace(0.2, 1.5, n)[:, None, None].to(torch.bfloat16)      # later keys score higher
     out, lse = ssm.attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), cu([n]).to(DEV), cu([n]).to(DEV), n, scale=scale,
                                 out_dtype=torch.float32, lse=True)
-    check_attention(out, lse, _prefill_ref(q, k, v, [n], [n], scale), D, torch.float32)
+    check_attention(out, lse, _prefill_ref(q, k, v, [n], [n], scale), D, torch.float32, W_PREFILL)
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -133,7 +133,7 @@ def test_prefill_chunks_equal_the_whole_prompt():
                                 e - a, lse=True)
         outs.append(o)
         lses.append(l)
-    check_attention(torch.cat(outs), torch.cat(lses), ref, D, torch.bfloat16)
+    check_attention(torch.cat(outs), torch.cat(lses), ref, D, torch.bfloat16, W_PREFILL)
 
 
 # ------------------------------------------------------------------------------ decode
@@ -165,11 +165,11 @@ def test_decode(lens, H, Hk, D, page, i8, out_dtype):
     q = heads(g, len(lens), H, D, 1.5)
     out, lse = _decode(q, c, lens, out_dtype=out_dtype, lse=True)
     ref = _decode_ref(q, c, lens, D ** -0.5)
-    check_attention(out, lse, ref, D, out_dtype, f"decode {lens}")
+    check_attention(out, lse, ref, D, out_dtype, W_DECODE, f"decode {lens}")
     assert (to64(out)[np.isneginf(ref[1])] == 0).all()
     # a loose bound of the lengths only changes how the work is cut
     loose, _ = _decode(q, c, lens, max_len=(max(lens) + 1) * 9, out_dtype=out_dtype)
-    check_attention(loose, None, ref, D, out_dtype, f"decode {lens}, loose bound")
+    check_attention(loose, None, ref, D, out_dtype, W_DECODE, f"decode {lens}, loose bound")
     assert ssm.device_status() == 0
 
 
@@ -187,7 +187,7 @@ def test_decode_long_and_sharp(i8):
     c = paged(k, v, [n], 64, i8)
     q = heads(g, 1, H, D, 2.0)
     out, lse = _decode(q, c, [n], out_dtype=torch.float32, lse=True)
-    check_attention(out, lse, _decode_ref(q, c, [n], D ** -0.5), D, torch.float32)
+    check_attention(out, lse, _decode_ref(q, c, [n], D ** -0.5), D, torch.float32, W_DECODE)
 
 
 @pytest.mark.parametrize("i8", [True, False])
@@ -199,7 +199,7 @@ def test_decode_query_and_value_ranges(i8, gain):
     c = paged(torch.randn(n, 1, D, generator=g) / gain, torch.randn(n, 1, D, generator=g) * gain, [n], 16, i8)
     q = heads(g, 1, 4, D, gain)
     out, lse = _decode(q, c, [n], out_dtype=torch.float32, lse=True)
-    check_attention(out, lse, _decode_ref(q, c, [n], D ** -0.5), D, torch.float32)
+    check_attention(out, lse, _decode_ref(q, c, [n], D ** -0.5), D, torch.float32, W_DECODE)
 
 
 @pytest.mark.parametrize("i8", [True, False])
@@ -215,12 +215,12 @@ def test_decode_reports_bad_pages_and_lengths(i8):
     out, lse = _decode(q, c, lens, out_dtype=torch.float32, lse=True)
     assert ssm.device_status(clear=True) == ssm.DEV_BAD_INDEX
     ref = attend64(to64(q[:1]), c["k64"][:32], c["v64"][:32], 64 ** -0.5, 31)
-    check_attention(out[:1], lse[:1], ref, 64, torch.float32)
+    check_attention(out[:1], lse[:1], ref, 64, torch.float32, W_DECODE)
     assert torch.equal(out[1], good[1])
     cut, _ = _decode(q, c, [-3, 4000], max_len=40, out_dtype=torch.float32)
     assert ssm.device_status(clear=True) == ssm.DEV_BAD_INDEX
     assert bool((cut[0] == 0).all())
-    check_attention(cut[1:], None, attend64(to64(q[1:]), c["k64"][40:], c["v64"][40:], 64 ** -0.5, 39), 64, torch.float32)
+    check_attention(cut[1:], None, attend64(to64(q[1:]), c["k64"][40:], c["v64"][40:], 64 ** -0.5, 39), 64, torch.float32, W_DECODE)
 
 
 @pytest.mark.parametrize("i8", [True, False])
@@ -260,9 +260,8 @@ def test_append_read_prefill_decode_agree(i8):
     ref = attend64(to64(torch.cat(q)), to64(k), to64(v), D ** -0.5, 0)
     out, _ = torch.cat(outs), None
     # the prompt's rows attend over keys and values rounded to bf16 on reading an int8 cache
-    extra_v = 2.0 ** -9 * ref[2] + 2.0 ** -9 * 2.1 * ref[3][..., None] * ref[2]
-    from _attn import out_bound
-    bound = out_bound(ref[0], ref[2], ref[3], D, torch.bfloat16) + 1.1 * extra_v
+    extra_v = W_PREFILL * ref[2] + W_PREFILL * 2.1 * ref[3][..., None] * ref[2]
+    bound = out_bound(ref[0], ref[2], ref[3], D, torch.bfloat16, W_PREFILL) + 1.1 * extra_v
     assert (np.abs(to64(out) - ref[0]) <= bound).all()
     # the decode step captured in a graph: replays give the same bits
     lens = torch.tensor([N], dtype=torch.int32, device=DEV)
@@ -291,4 +290,4 @@ def test_decode_workspace_is_kept_inside():
     torch.cuda.synchronize()
     assert bool((buf[:256] == 0xA5).all()) and bool((buf[256 + need:] == 0xA5).all())
     assert bool((obuf[:, 0] == 7.0).all()) and bool((obuf[:, -1] == 7.0).all())
-    check_attention(out, None, _decode_ref(q, c, lens, D ** -0.5), D, torch.bfloat16)
+    check_attention(out, None, _decode_ref(q, c, lens, D ** -0.5), D, torch.bfloat16, W_DECODE)
