@@ -580,7 +580,7 @@ size_t attn_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int
  *   q                    view [batch][H][D] bf16       lens: [batch] int32, tokens cached for each;
  *                        0 gives zeros and lse -inf.  A length below 0, above max_len or past the
  *                        table's row is cut to the range and sets SSM_DEV_BAD_INDEX.
- *   max_len              an upper bound of lens, >= 1
+ *   max_len              an upper bound of lens, 1 .. 2^30
  *   cache                as above; a page outside [0, n_pages) counts as not visible and sets
  *                        SSM_DEV_BAD_INDEX
  *   out                  view [batch][H][D] in out_dtype, 16-byte aligned, strides multiples of 8

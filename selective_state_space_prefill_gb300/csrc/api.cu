@@ -982,7 +982,7 @@ int attn_prefill(int batch, int64_t total_q, int64_t total_k, int max_q, int n_q
 
 size_t attn_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int head_dim, int max_len) {
     if (batch < 1 || batch > 65535 || n_kv_heads < 1 || n_kv_heads > 4096 || n_q_heads < 1 || n_q_heads > 65535 ||
-        n_q_heads % n_kv_heads != 0 || head_dim < 16 || head_dim > 128 || head_dim % 16 != 0 || max_len < 1)
+        n_q_heads % n_kv_heads != 0 || head_dim < 16 || head_dim > 128 || head_dim % 16 != 0 || max_len < 1 || max_len > (1 << 30))
         return 0;
     return ssm::attn_decode_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_len);
 }
@@ -998,7 +998,7 @@ int attn_decode_step(int batch, int n_q_heads, int n_kv_heads, int head_dim, ssm
     g_err[0] = 0;
     int rc;
     if (batch < 1 || batch > 65535) return fail(SSM_ERR_INVALID_ARG, "%s: batch %d not in [1, 65535]", fn, batch);
-    if (max_len < 1) return fail(SSM_ERR_INVALID_ARG, "%s: max_len %d < 1", fn, max_len);
+    if (max_len < 1 || max_len > (1 << 30)) return fail(SSM_ERR_INVALID_ARG, "%s: max_len %d not in [1, 2^30]", fn, max_len);
     if ((rc = check_heads(fn, n_q_heads, n_kv_heads, head_dim)) != SSM_OK) return rc;
     if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return fail(SSM_ERR_INVALID_ARG, "%s: unknown dtype", fn);
     if (in_dtype != SSM_BF16) return fail(SSM_ERR_UNSUPPORTED, "%s: q must be bf16", fn);
