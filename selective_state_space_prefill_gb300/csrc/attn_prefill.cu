@@ -115,6 +115,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Pairs of fp32 in one 64-bit register: one instruction for two sums or multiply-adds.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 template <int DP, typename Tout>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -187,130 +207,10 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         atomicOr(a.status, 1u);
     };
 
-    if (warp == 8 && lane == 0 && nb > 0) {
-        // ---- TMA producer: the query tiles, then K_0, V_0, K_1, V_1, ... through the ring
-        const int hk = h / (a.n_q / a.n_kv);
-        for (int t = 0; t < 2; ++t) {
-            if ((t ? n1 : n0) == 0) continue;
-            mbar_arrive_expect_tx(&q_full[t], G::kTile);
-            for (int c = 0; c < DP / 64; ++c)
-                tma_load_3d(smem + t * G::kTile + c * 16384, &tm_q, &q_full[t], 64 * c, h, q0 + row0 + t * kM);
-        }
-        int it = 0;
-        for (; it < 2 * nb; ++it) {
-            const int s = it % G::kSlots;
-            if (it >= G::kSlots && !mbar_wait_bounded(&kv_empty[s], (uint32_t)((it / G::kSlots + 1) & 1))) {
-                expired();
-                break;
-            }
-            unsigned char* dst = smem + G::kOffKV + s * G::kTile;
-            uint64_t* full = &kv_full[s];
-            if ((it & 1) && (it >> 1) >= mask_from) {     // by way of the cleaning warps
-                mbar_arrive(full);
-                full = &v_raw[(it >> 1) - mask_from];
-            }
-            mbar_arrive_expect_tx(full, G::kTile);
-            for (int c = 0; c < DP / 64; ++c)
-                tma_load_3d(dst + c * 16384, it & 1 ? &tm_v : &tm_k, full, 64 * c, hk, k0 + (it >> 1) * kN);
-        }
-        // tail: every load has landed and the MMAs' last releases have arrived before the CTA ends
-        for (int u = max(0, it - G::kSlots); u < it; ++u) {
-            const bool raw = (u & 1) && (u >> 1) >= mask_from;
-            if (!mbar_wait_bounded(raw ? &v_raw[(u >> 1) - mask_from] : &kv_full[u % G::kSlots],
-                                   raw ? 0u : (uint32_t)((u / G::kSlots) & 1)))
-                expired();
-            if (!s_err && !mbar_wait_bounded(&kv_empty[u % G::kSlots], (uint32_t)((u / G::kSlots) & 1))) expired();
-        }
-        for (int t = 0; t < 2; ++t)
-            if ((t ? n1 : n0) > 0 && !mbar_wait_bounded(&q_full[t], 0)) expired();
-    } else if (warp == 9 && lane == 0 && nb > 0) {
-        // ---- MMA issuer
-        const int dsteps = a.dim / 16;
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (ok && !mbar_wait_bounded(bar, parity)) {
-                ok = false;
-                expired();
-            }
-        };
-        auto scores = [&](int t, int j) {                // S_t = Q_t K_j^T
-            const uint32_t qa = smem_u32(smem + t * G::kTile);
-            const uint32_t ka = smem_u32(smem + G::kOffKV + ((2 * j) % G::kSlots) * G::kTile);
-            for (int k = 0; k < dsteps; ++k)
-                mma_bf16(tmem + (uint32_t)(128 * t), smem_desc_sw128(qa + (k >> 2) * 16384 + 32 * (k & 3)),
-                         smem_desc_sw128(ka + (k >> 2) * 16384 + 32 * (k & 3)), G::kIdescS, k != 0);
-            mma_commit(&s_full[t]);
-        };
-        wait(&kv_full[0], 0);
-        for (int t = 0; t < 2 && ok; ++t) {
-            if ((t ? n1 : n0) == 0) continue;
-            wait(&q_full[t], 0);
-            tc_fence_after();
-            if (ok) scores(t, 0);
-        }
-        if (ok) mma_commit(&kv_empty[0]);
-        for (int j = 0; j < nb && ok; ++j) {
-            const int vi = 2 * j + 1, ki = 2 * j + 2;
-            wait(&kv_full[vi % G::kSlots], (uint32_t)((vi / G::kSlots) & 1));
-            if (j >= mask_from) wait(&v_ok[j - mask_from], 0);
-            if (j + 1 < nb) wait(&kv_full[ki % G::kSlots], (uint32_t)((ki / G::kSlots) & 1));
-            const uint64_t vd = smem_desc_mn(smem_u32(smem + G::kOffKV + (vi % G::kSlots) * G::kTile));
-            for (int t = 0; t < 2 && ok; ++t) {
-                const int n = t ? n1 : n0;
-                if (j >= n) continue;
-                wait(&p_full[t], (uint32_t)(j & 1));
-                if (!ok) break;
-                tc_fence_after();
-                for (int k = 0; k < kN / 16; ++k)        // 16 keys: 8 columns of P, 2048 bytes of V
-                    mma_bf16_ts(tmem + 256u + (uint32_t)(128 * t), tmem + (uint32_t)(128 * t + 8 * k),
-                                vd + (uint64_t)(2048 >> 4) * k, G::kIdescO, (j | k) != 0);
-                mma_commit(&o_full[t]);
-                if (j + 1 < n) scores(t, j + 1);
-            }
-            if (ok) mma_commit(&kv_empty[vi % G::kSlots]);
-            if (ok && j + 1 < nb) mma_commit(&kv_empty[ki % G::kSlots]);
-        }
-    } else if (warp >= 10) {
-        // ---- value blocks that some row does not wholly see
-        for (int j = mask_from; j < nb; ++j) {
-            const int vi = 2 * j + 1;
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&v_raw[j - mask_from], 0))) {
-                expired();
-                break;
-            }
-            unsigned char* v = smem + G::kOffKV + (vi % G::kSlots) * G::kTile;
-            const int rows = lk - j * kN;                // of this sequence; later ones are zeroed
-            for (int i = threadIdx.x - 320; i < G::kTile / 16; i += 64) {
-                const int r = (i >> 3) & 127;
-                uint4* p = reinterpret_cast<uint4*>(v) + i;
-                if (r >= rows) {
-                    *p = make_uint4(0u, 0u, 0u, 0u);
-                    continue;
-                }
-                const uint4 w = *p;
-                uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-                bool fine = true;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    fine = fine && (ws[e] & 0x7f80u) != 0x7f80u && (ws[e] & 0x7f800000u) != 0x7f800000u;
-                if (fine) continue;
-                const int col = (i >> 10) * 64 + ((i & 7) ^ (r & 7)) * 8;       // the swizzle undone
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t x = (ws[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-                    if ((x & 0x7f80u) != 0x7f80u) continue;
-                    const int kind = x == 0x7f80u ? 0 : (x == 0xff80u ? 1 : 2);
-                    atomicMin(&bad[kind * DP + col + e], j * kN + r);
-                    ws[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
-                }
-                *p = make_uint4(ws[0], ws[1], ws[2], ws[3]);
-                s_bad = 1;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&v_ok[j - mask_from]);
-        }
-    } else if (warp < 8) {
-        // ---- softmax of tile t: thread = row
+    if (warp < 8) {
+        // ---- softmax of tile t: thread = row.  The softmax warps take registers from the four service
+        // warps: 256 x 208 + 128 x 88 = 384 x 168, the launch's total.
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp >> 2, quarter = warp & 3;
         const int n = t ? n1 : n0;
         const int row = row0 + t * kM + 32 * quarter + lane;
@@ -338,9 +238,17 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 for (int i = 0; i < 128; ++i)
                     if (j * kN + i >= see) r[i] = 0xff800000u;          // -inf
             }
-            float mx = __uint_as_float(r[0]);
+            float mq[8];                                 // eight chains side by side
 #pragma unroll
-            for (int i = 1; i < 128; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
+            for (int i = 0; i < 8; ++i) mq[i] = __uint_as_float(r[i]);
+#pragma unroll
+            for (int i = 8; i < 128; i += 16)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    mq[e] = i + 8 < 128 ? fmaxf(fmaxf(mq[e], __uint_as_float(r[i + e])), __uint_as_float(r[i + 8 + e]))
+                                        : fmaxf(mq[e], __uint_as_float(r[i + e]));
+            const float mx = fmaxf(fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])),
+                                   fmaxf(fmaxf(mq[4], mq[5]), fmaxf(mq[6], mq[7])));
             if (j == 0) {
                 m = mx;
             } else {
@@ -369,21 +277,26 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
             }
             const float mc = m == -INFINITY ? 0.f : m * c;       // nothing but -inf so far: p = 0
-            float sum0 = 0.f, sum1 = 0.f;
+            const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+            uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 uint32_t p[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const float p0 = ex2(fmaf(__uint_as_float(r[64 * q + 2 * i]), c, -mc));
-                    const float p1 = ex2(fmaf(__uint_as_float(r[64 * q + 2 * i + 1]), c, -mc));
-                    sum0 += p0;
-                    sum1 += p1;
-                    p[i] = pack_bf16(p0, p1);
+                    float x0, x1;
+                    unpair(fma2(pair(__uint_as_float(r[64 * q + 2 * i]), __uint_as_float(r[64 * q + 2 * i + 1])), c2, mc2),
+                           x0, x1);
+                    x0 = ex2(x0);
+                    x1 = ex2(x1);
+                    sum[i & 3] = add2(sum[i & 3], pair(x0, x1));
+                    p[i] = pack_bf16(x0, x1);
                 }
                 tmem_st32(ts + 32u * q, p);
             }
-            l += sum0 + sum1;
+            float l0, l1;
+            unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
+            l += l0 + l1;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -433,6 +346,131 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     reinterpret_cast<float4*>(out + 32 * q + 8 * g)[1] =
                         make_float4(v[8 * g + 4], v[8 * g + 5], v[8 * g + 6], v[8 * g + 7]);
                 }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 8 && lane == 0 && nb > 0) {
+            // ---- TMA producer: the query tiles, then K_0, V_0, K_1, V_1, ... through the ring
+            const int hk = h / (a.n_q / a.n_kv);
+            for (int t = 0; t < 2; ++t) {
+                if ((t ? n1 : n0) == 0) continue;
+                mbar_arrive_expect_tx(&q_full[t], G::kTile);
+                for (int c = 0; c < DP / 64; ++c)
+                    tma_load_3d(smem + t * G::kTile + c * 16384, &tm_q, &q_full[t], 64 * c, h, q0 + row0 + t * kM);
+            }
+            int it = 0;
+            for (; it < 2 * nb; ++it) {
+                const int s = it % G::kSlots;
+                if (it >= G::kSlots && !mbar_wait_bounded(&kv_empty[s], (uint32_t)((it / G::kSlots + 1) & 1))) {
+                    expired();
+                    break;
+                }
+                unsigned char* dst = smem + G::kOffKV + s * G::kTile;
+                uint64_t* full = &kv_full[s];
+                if ((it & 1) && (it >> 1) >= mask_from) {     // by way of the cleaning warps
+                    mbar_arrive(full);
+                    full = &v_raw[(it >> 1) - mask_from];
+                }
+                mbar_arrive_expect_tx(full, G::kTile);
+                for (int c = 0; c < DP / 64; ++c)
+                    tma_load_3d(dst + c * 16384, it & 1 ? &tm_v : &tm_k, full, 64 * c, hk, k0 + (it >> 1) * kN);
+            }
+            // tail: every load has landed and the MMAs' last releases have arrived before the CTA ends
+            for (int u = max(0, it - G::kSlots); u < it; ++u) {
+                const bool raw = (u & 1) && (u >> 1) >= mask_from;
+                if (!mbar_wait_bounded(raw ? &v_raw[(u >> 1) - mask_from] : &kv_full[u % G::kSlots],
+                                       raw ? 0u : (uint32_t)((u / G::kSlots) & 1)))
+                    expired();
+                if (!s_err && !mbar_wait_bounded(&kv_empty[u % G::kSlots], (uint32_t)((u / G::kSlots) & 1))) expired();
+            }
+            for (int t = 0; t < 2; ++t)
+                if ((t ? n1 : n0) > 0 && !mbar_wait_bounded(&q_full[t], 0)) expired();
+        } else if (warp == 9 && lane == 0 && nb > 0) {
+            // ---- MMA issuer
+            const int dsteps = a.dim / 16;
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (ok && !mbar_wait_bounded(bar, parity)) {
+                    ok = false;
+                    expired();
+                }
+            };
+            auto scores = [&](int t, int j) {                // S_t = Q_t K_j^T
+                const uint32_t qa = smem_u32(smem + t * G::kTile);
+                const uint32_t ka = smem_u32(smem + G::kOffKV + ((2 * j) % G::kSlots) * G::kTile);
+                for (int k = 0; k < dsteps; ++k)
+                    mma_bf16(tmem + (uint32_t)(128 * t), smem_desc_sw128(qa + (k >> 2) * 16384 + 32 * (k & 3)),
+                             smem_desc_sw128(ka + (k >> 2) * 16384 + 32 * (k & 3)), G::kIdescS, k != 0);
+                mma_commit(&s_full[t]);
+            };
+            wait(&kv_full[0], 0);
+            for (int t = 0; t < 2 && ok; ++t) {
+                if ((t ? n1 : n0) == 0) continue;
+                wait(&q_full[t], 0);
+                tc_fence_after();
+                if (ok) scores(t, 0);
+            }
+            if (ok) mma_commit(&kv_empty[0]);
+            for (int j = 0; j < nb && ok; ++j) {
+                const int vi = 2 * j + 1, ki = 2 * j + 2;
+                wait(&kv_full[vi % G::kSlots], (uint32_t)((vi / G::kSlots) & 1));
+                if (j >= mask_from) wait(&v_ok[j - mask_from], 0);
+                if (j + 1 < nb) wait(&kv_full[ki % G::kSlots], (uint32_t)((ki / G::kSlots) & 1));
+                const uint64_t vd = smem_desc_mn(smem_u32(smem + G::kOffKV + (vi % G::kSlots) * G::kTile));
+                for (int t = 0; t < 2 && ok; ++t) {
+                    const int n = t ? n1 : n0;
+                    if (j >= n) continue;
+                    wait(&p_full[t], (uint32_t)(j & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int k = 0; k < kN / 16; ++k)        // 16 keys: 8 columns of P, 2048 bytes of V
+                        mma_bf16_ts(tmem + 256u + (uint32_t)(128 * t), tmem + (uint32_t)(128 * t + 8 * k),
+                                    vd + (uint64_t)(2048 >> 4) * k, G::kIdescO, (j | k) != 0);
+                    mma_commit(&o_full[t]);
+                    if (j + 1 < n) scores(t, j + 1);
+                }
+                if (ok) mma_commit(&kv_empty[vi % G::kSlots]);
+                if (ok && j + 1 < nb) mma_commit(&kv_empty[ki % G::kSlots]);
+            }
+        } else if (warp >= 10) {
+            // ---- value blocks that some row does not wholly see
+            for (int j = mask_from; j < nb; ++j) {
+                const int vi = 2 * j + 1;
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&v_raw[j - mask_from], 0))) {
+                    expired();
+                    break;
+                }
+                unsigned char* v = smem + G::kOffKV + (vi % G::kSlots) * G::kTile;
+                const int rows = lk - j * kN;                // of this sequence; later ones are zeroed
+                for (int i = threadIdx.x - 320; i < G::kTile / 16; i += 64) {
+                    const int r = (i >> 3) & 127;
+                    uint4* p = reinterpret_cast<uint4*>(v) + i;
+                    if (r >= rows) {
+                        *p = make_uint4(0u, 0u, 0u, 0u);
+                        continue;
+                    }
+                    const uint4 w = *p;
+                    uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                    bool fine = true;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        fine = fine && (ws[e] & 0x7f80u) != 0x7f80u && (ws[e] & 0x7f800000u) != 0x7f800000u;
+                    if (fine) continue;
+                    const int col = (i >> 10) * 64 + ((i & 7) ^ (r & 7)) * 8;       // the swizzle undone
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t x = (ws[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                        if ((x & 0x7f80u) != 0x7f80u) continue;
+                        const int kind = x == 0x7f80u ? 0 : (x == 0xff80u ? 1 : 2);
+                        atomicMin(&bad[kind * DP + col + e], j * kN + r);
+                        ws[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                    }
+                    *p = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+                    s_bad = 1;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_ok[j - mask_from]);
             }
         }
     }
