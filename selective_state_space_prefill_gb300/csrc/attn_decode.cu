@@ -5,24 +5,26 @@
 // Every cached byte is read once and used for the few query heads that share its kv head, so the
 // cache's bytes bound the step (and launch latency, when there are few of them).  What the design
 // has to do is keep enough of them in flight and the arithmetic out of their way:
-//   * a warp takes 16 keys at a time (a page holds a whole number of such units) straight from
-//     global memory into registers, 16 bytes a load, each byte by one lane; the values' loads are in
-//     flight under the scores, the next keys' under the softmax and the second product;
+//   * a warp takes 16 keys at a time (a page holds a whole number of such units); its lanes copy
+//     them to its own ring in shared memory with 16-byte asynchronous copies, several units ahead,
+//     and no warp waits for another.  The 16-byte chunks of a 128-byte line are permuted by the row
+//     (chunk ^ row % 8), so that the operand reads below meet no bank twice;
 //   * keys and values are the 16-row A operand of m16n8k16 tensor-core products and the (up to 8)
-//     query heads of the kv head their 8 columns: S^T = K q^T, O^T = V^T P^T.  The reduction index of
-//     each product may be permuted freely, so a lane's 16 loaded bytes are its operand elements as
-//     they lie; only P^T crosses lanes, as transposed 8 x 8 matrices;
-//   * int8 codes become fp16 exactly (bytes 0x64 and code + 128 are the half 1152 + code); the row
-//     scales multiply the scores after the first product and enter the softmax weights before the
-//     second;
+//     query heads of the kv head their 8 columns: S^T = K q^T, O^T = V^T P^T, the operands read as
+//     8 x 8 matrices (the values' transposed).  The order of the reduction index is free, so two
+//     int8 dimensions travel as one 16-bit element;
+//   * int8 codes become fp16 exactly, two at a time: code + 128 as the significand of 1024 + x for the
+//     values (1152 subtracted), as a subnormal, x 2^-24, for the keys, whose 128 is taken off the
+//     scores' starting value; the row scales multiply the scores after the first product and the
+//     softmax weights before the second;
 //   * the long axis is cut into pieces, one CTA each; a second kernel joins the pieces' (m, l, o).
 //
 // Precision: scores, m, l and o are fp32.  With int8 rows the query is held in fp16 after scaling
 // by a power of two (exact for bf16 queries within 2^-25 of their head's maximum) and the weights
-// w_j = 2^(s_j + log2 scale_j - mw) in fp16 (11 bits; mw, the running reference of the exponent with
-// the scale in it, keeps them in range whatever the rows' scales are).  With bf16 rows the weights
-// are a bf16 pair hi + lo.  Both references are raised only when the running maximum has grown by
-// more than 2^8, so rescaling o is rare.
+// w_j = 2^(s_j - mw) scale_j in fp16 (11 bits; mw is a running reference of the exponent with the
+// scale in it, so that they fit whatever the rows' scales are).  With bf16 rows the weights are a
+// bf16 pair hi + lo.  The references are raised only when a weight would pass them by more than 2^8,
+// so rescaling o is rare.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -35,7 +37,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 16;               // keys a warp takes at a time
 constexpr float kSlack = 8.0f;          // log2 of how far a weight may pass its reference
-constexpr float kLift = 6.0f;           // fp16 weights carry a factor 2^6: at most 2^14
+constexpr float kLift = 6.0f;           // fp16 weights carry a factor 2^6 ...
+constexpr float kMost = 16384.0f;       // ... and are at most 2^14
 constexpr unsigned kBadIndex = 8u;      // SSM_DEV_BAD_INDEX
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -55,10 +58,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// Two int8 codes (bytes i and j of w ^ 0x80808080, chosen by sel against 0x64 bytes) as exact halves.
-template <uint32_t sel>
-__device__ __forceinline__ uint32_t halves(uint32_t flipped) {
-    const uint32_t u = __byte_perm(flipped, 0x64646464u, sel);
+// Of the four codes in x, the bytes 0 and 2 (kHi false) or 1 and 3, exact in fp16: as (code + 128) 2^-24,
+// or as the code itself.
+template <bool kHi>
+__device__ __forceinline__ uint32_t raised(uint32_t x) {
+    return ((kHi ? x >> 8 : x) & 0x00ff00ffu) ^ 0x00800080u;
+}
+template <bool kHi>
+__device__ __forceinline__ uint32_t halves(uint32_t x) {
+    const uint32_t u = ((kHi ? x >> 8 : x) & 0x00ff00ffu) ^ 0x64806480u;
     const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));   // 1152
     return *reinterpret_cast<const uint32_t*>(&v);
 }
@@ -72,9 +80,48 @@ __device__ __forceinline__ uint32_t pack_b(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ uint4 ld16(const void* p, bool on) {
-    return on ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+// Asynchronous copies to shared memory; `on` false writes zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+// Four 8 x 8 matrices of 16-bit elements, lane 8 i + r giving the address of matrix i's row r.
+__device__ __forceinline__ void matrices(uint32_t (&x)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void matrices_t(uint32_t (&x)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ float lds4(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// A stage of a warp's ring: 16 key rows, 16 value rows, and (int8) their 16 + 16 scales.  A row of
+// ROW bytes is ROW / 128 lines of 128 bytes (line i of all 16 rows together), or half a line.
+template <bool I8, int DP>
+struct Ring {
+    static constexpr int kRow = DP * (I8 ? 1 : 2);
+    static constexpr int kLine = kRow < 128 ? kRow : 128;
+    static constexpr int kRows = kUnit * kRow;          // bytes of 16 rows
+    static constexpr int kStage = 2 * kRows + (I8 ? 128 : 0);
+    // so many that three or four CTAs share an SM with some 100 KB of copies in flight
+    static constexpr int kStages = kStage > 8000 ? 3 : (kStage > 4000 ? 3 : 4);
+    static constexpr int kPer = kLine / 16;             // chunks of a line
+    // byte offset of 16-byte chunk c of row r
+    static __device__ __forceinline__ uint32_t at(int r, int c) {
+        return (uint32_t)((c / kPer) * kUnit * kLine + r * kLine + ((c % kPer) ^ (kPer == 8 ? r & 7 : (r >> 1) & 3)) * 16);
+    }
+    // ... of chunk c + c0, c0 even, from that of chunk c < 2 (lines are 128-byte aligned)
+    static __device__ __forceinline__ uint32_t step(uint32_t a, int c0) {
+        return (a ^ (uint32_t)((c0 % kPer) * 16)) + (uint32_t)((c0 / kPer) * kUnit * kLine);
+    }
+};
 
 // Pieces of the long axis.
 struct Cut {
@@ -92,16 +139,34 @@ __device__ __forceinline__ int length_of(const AttnDecodeArgs& a, int b, bool re
     return len;
 }
 
+// The pieces' maxima and sums, after their outputs in the workspace.
+template <int DP>
+__device__ __forceinline__ float2* piece_sums(const AttnDecodeArgs& a, const Cut& cut, int64_t batch) {
+    return reinterpret_cast<float2*>(reinterpret_cast<float*>(a.workspace) + batch * a.n_q * cut.pieces * DP);
+}
+
+// A sum of 0 is that of no key: nothing seen, output zeros, lse -inf.
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : kLn2 * (m + log2f(l)); }
+__device__ __forceinline__ void store_out(float* p, float4 v, float l) {
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<float4*>(p) = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+}
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float4 v, float l) {
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2*>(p) = l == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_b(v.x * f, v.y * f), pack_b(v.z * f, v.w * f));
+}
+
 // DP: head_dim padded to 64 or 128.  NT: groups of 8 query heads a CTA serves.
 template <bool I8, int DP, int NT, typename Tout>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? (I8 ? 4 : 3) : 2)
 k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
     constexpr int kHeads = 8 * NT;
     constexpr int kSteps = DP / 16;                     // products over the head's dimensions
-    constexpr int kRowLoads = I8 ? DP / 64 : DP / 32;   // 16-byte loads a lane makes of a key row
-    constexpr int kVLoads = I8 ? 1 : DP / 64;           // ... of a value row (8 bytes for int8, DP 64)
+    using R = Ring<I8, DP>;
+    constexpr int kE = I8 ? 1 : 2;
+    extern __shared__ __align__(128) unsigned char smem[];      // the warps' rings, then their parts
     __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads], s_w[kWarps][kHeads];
-    __shared__ float s_o[kWarps][kHeads][DP];
+    float(*s_o)[kHeads][DP] = reinterpret_cast<float(*)[kHeads][DP]>(smem);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -115,46 +180,129 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
     const int dim = a.c.dim, psz = a.c.page_size;
     const float c = a.scale * kLog2e;
 
+    // the cache row of each of this warp's units in turn, or -1: past the end, or a page outside the cache
+    const int32_t* table = a.page_table + (int64_t)b * a.table_stride;
+    constexpr int kStep = kUnit * kWarps;
+    int at_j = begin + kUnit * warp, at_page = at_j / psz, at_row = at_j % psz;
+    const int skip_page = kStep / psz, skip_row = kStep % psz;
+    auto next_row = [&]() -> int64_t {
+        if (at_j >= end) return -1;
+        const int page = table[at_page], r = at_row;
+        at_j += kStep;
+        at_page += skip_page;
+        at_row += skip_row;
+        if (at_row >= psz) at_row -= psz, ++at_page;
+        if (page < 0 || page >= a.c.n_pages) {
+            if (lane == 0) atomicOr(a.status, kBadIndex);
+            return -1;
+        }
+        return ((int64_t)page * a.c.n_kv + hk) * psz + r;
+    };
+    // the copies of the unit whose first row is `row` into ring stage `st` (none for row < 0; the
+    // group is committed all the same, so that groups and units keep step)
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * R::kStages * R::kStage);
+    constexpr int kChunks = R::kRow / 16, kPerPass = 32 / kChunks;       // chunks of a row, rows a pass of the warp copies
+    const int ch16 = lane % kChunks, r0 = lane / kChunks;
+    const bool in = 16 * ch16 < dim * kE;               // chunks past the head's dimensions are zeros
+    const int64_t row_bytes = (int64_t)dim * kE, lane_off = in ? r0 * row_bytes + 16 * ch16 : 0, pass_bytes = kPerPass * row_bytes;
+    auto fetch = [&](int64_t row, int j, int st) {
+        if (row >= 0) {
+            const uint32_t dst = ring + (uint32_t)(st * R::kStage);
+            const char* kp = reinterpret_cast<const char*>(a.c.k) + row * row_bytes + lane_off;
+            const char* vp = reinterpret_cast<const char*>(a.c.v) + row * row_bytes + lane_off;
+            if (j + kUnit <= end) {
+#pragma unroll
+                for (int r = 0; r < kUnit; r += kPerPass) {
+                    copy16(dst + R::at(r0 + r, ch16), kp, in);
+                    copy16(dst + R::kRows + R::at(r0 + r, ch16), vp, in);
+                    if (in) kp += pass_bytes, vp += pass_bytes;
+                }
+            } else {
+#pragma unroll 1
+                for (int r = 0; r < kUnit; r += kPerPass) {
+                    // rows past the end are zeros: a value's weight is 0, but 0 x NaN is not
+                    const bool on = in && j + r0 + r < end;
+                    copy16(dst + R::at(r0 + r, ch16), on ? kp : reinterpret_cast<const char*>(a.c.k), on);
+                    copy16(dst + R::kRows + R::at(r0 + r, ch16), on ? vp : reinterpret_cast<const char*>(a.c.v), on);
+                    kp += pass_bytes, vp += pass_bytes;
+                }
+            }
+            if constexpr (I8) {
+                const int key = lane & 15;
+                copy4(dst + 2 * R::kRows + 4 * lane, (lane < 16 ? a.c.k_scale : a.c.v_scale) + row + key, j + key < end);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    int j = at_j, stage = 0;
+    int64_t rows[R::kStages];                           // of the units in the ring, the current one first
+#pragma unroll
+    for (int st = 0; st < R::kStages; ++st) {
+        rows[st] = next_row();
+        if (st + 1 < R::kStages) fetch(rows[st], j + st * kStep, st);
+    }
+    // this lane's rows of the operands' matrices: keys, matrix i = (key half i % 2, chunk i / 2); values
+    // the same for int8, (chunk i % 2, key half i / 2) for bf16
+    const uint32_t key_at = R::at((lane & 7) + (lane & 8), lane >> 4);
+    const uint32_t val_at = I8 ? key_at : R::at((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+
     // ---- the query heads as B operands: column n = lane / 4 is head h0 + 8 i + n
     uint32_t qb[NT][kSteps][2];
-    float ch[NT][2];                                    // c (and the query's scaling undone) of heads 2t, 2t + 1
+    float ch[NT][2];                                    // c (and the operands' scaling undone) of heads 2t, 2t + 1
+    float s0[NT][2];                                    // where their scores start: the keys' 128 taken off
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const bool on = 8 * i + g < nh;
         const __nv_bfloat16* qp = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)b * a.q_st +
                                   (int64_t)(h0 + 8 * i + (on ? g : 0)) * a.q_sh;
-        float qmax = 0.f;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            // the four dimensions this lane's operand elements stand for in step s
-            const int d = I8 ? 16 * (t + 4 * (s >> 2)) + 4 * (s & 3) : 8 * (t + 4 * (s >> 1)) + 4 * (s & 1);
-            const uint2 w = on && d < dim ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0u, 0u);
-            qb[i][s][0] = w.x;
-            qb[i][s][1] = w.y;
-            qmax = fmaxf(qmax, fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xffff0000u))));
-            qmax = fmaxf(qmax, fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xffff0000u))));
-        }
         ch[i][0] = ch[i][1] = c;
+        s0[i][0] = s0[i][1] = 0.f;
         if constexpr (I8) {
+            float qmax = 0.f;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const int d = 16 * s + 4 * t;           // elements d, d + 2 and d + 1, d + 3
+                const uint2 w = on && d < dim ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0u, 0u);
+                qb[i][s][0] = __byte_perm(w.x, w.y, 0x5410);
+                qb[i][s][1] = __byte_perm(w.x, w.y, 0x7632);
+                qmax = fmaxf(qmax, fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xffff0000u))));
+                qmax = fmaxf(qmax, fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xffff0000u))));
+            }
             qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, 1));
             qmax = fmaxf(qmax, __shfl_xor_sync(0xffffffffu, qmax, 2));
-            // 2^e with qmax 2^e in [2^10, 2^11); the exponent kept where 2^e and 2^-e are normal
-            const int e = qmax > 0.f ? max(-100, min(100, 137 - (int)(__float_as_uint(qmax) >> 23))) : 0;
-            const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
+            // 2^e with qmax 2^e in [2^10, 2^11); the exponent kept where 2^e and 2^(24-e) are normal
+            const int e = qmax > 0.f ? max(-90, min(90, 137 - (int)(__float_as_uint(qmax) >> 23))) : 0;
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 + 24 - e) << 23);
+            float sum = 0.f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t w = qb[i][s][k];
                     qb[i][s][k] = pack_h(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+                    const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&qb[i][s][k]));
+                    sum += r.x + r.y;
                 }
-            ch[i][0] *= __shfl_sync(0xffffffffu, down, 8 * t);          // lane 4 (2t) holds head 2t's
-            ch[i][1] *= __shfl_sync(0xffffffffu, down, 8 * t + 4);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {               // lane 4 n holds head n's
+                ch[i][x] *= __shfl_sync(0xffffffffu, down, 8 * t + 4 * x);
+                s0[i][x] = __shfl_sync(0xffffffffu, sum, 8 * t + 4 * x) * -7.62939453125e-6f;      // -128 x 2^-24
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const int d = 16 * s + 2 * t;
+                qb[i][s][0] = on && d < dim ? *reinterpret_cast<const uint32_t*>(qp + d) : 0u;
+                qb[i][s][1] = on && d < dim ? *reinterpret_cast<const uint32_t*>(qp + d + 8) : 0u;
+            }
         }
     }
 
     float o[NT][DP / 16][4];
-    float m[NT][2], mw[NT][2], l[NT][2];                // of heads 2t, 2t + 1
+    float m[NT][2], mw[NT][2], fw[NT][2], l[NT][2];     // of heads 2t, 2t + 1; fw = 2^(m - mw + kLift)
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -162,101 +310,65 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][k][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) m[i][e] = mw[i][e] = -INFINITY, l[i][e] = 0.f;
+        for (int e = 0; e < 2; ++e) m[i][e] = mw[i][e] = -INFINITY, fw[i][e] = INFINITY, l[i][e] = 0.f;
     }
 
-    // the cache row of a unit's first key, or -1
-    const int32_t* table = a.page_table + (int64_t)b * a.table_stride;
-    auto row_of = [&](int j) -> int64_t {
-        if (j >= end) return -1;
-        const int page = table[j / psz];
-        if (page < 0 || page >= a.c.n_pages) {
-            if (lane == 0) atomicOr(a.status, kBadIndex);
-            return -1;
+    for (; j < end; j += kStep) {
+        // the unit kStages - 1 ahead goes into the stage that the last unit left
+        int ahead = stage + R::kStages - 1;
+        if (ahead >= R::kStages) ahead -= R::kStages;
+        fetch(rows[R::kStages - 1], j + (R::kStages - 1) * kStep, ahead);
+        asm volatile("cp.async.wait_group %0;" ::"n"(R::kStages - 1) : "memory");
+        __syncwarp();
+        const int64_t row = rows[0];
+#pragma unroll
+        for (int st = 0; st + 1 < R::kStages; ++st) rows[st] = rows[st + 1];
+        rows[R::kStages - 1] = next_row();
+        const uint32_t base = ring + (uint32_t)(stage * R::kStage);
+        stage = stage + 1 == R::kStages ? 0 : stage + 1;
+        if (row < 0) {                                  // a page outside the cache: nothing to see
+            __syncwarp();
+            continue;
         }
-        return ((int64_t)page * a.c.n_kv + hk) * psz + j % psz;
-    };
-    constexpr int kE = I8 ? 1 : 2;
-    const char* kbase = reinterpret_cast<const char*>(a.c.k);
-    const char* vbase = reinterpret_cast<const char*>(a.c.v);
-    uint4 kr[2][kRowLoads];                             // rows g and g + 8
-    float ks[2] = {0.f, 0.f};
-    auto load_keys = [&](int64_t row) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const char* p = kbase + (row + g + 8 * r) * dim * kE;
-#pragma unroll
-            for (int i = 0; i < kRowLoads; ++i) {
-                const int at = 16 * (t + 4 * i);
-                kr[r][i] = ld16(p + at, row >= 0 && at < dim * kE);
-            }
-            if constexpr (I8) ks[r] = row >= 0 ? __ldg(a.c.k_scale + row + g + 8 * r) : 0.f;
-        }
-    };
-
-    int j = begin + kUnit * warp;
-    int64_t row = row_of(j);
-    load_keys(row);
-    for (; j < end; j += kUnit * kWarps) {
-        // ---- values of this unit, in flight: keys 2t, 2t + 1, 2t + 8, 2t + 9
-        uint4 vr[4][kVLoads];
-        float vs[2] = {0.f, 0.f};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int key = 2 * t + (r & 1) + 8 * (r >> 1);
-            const bool on = row >= 0 && j + key < end;
-            const char* p = vbase + (row + key) * dim * kE;
-            if constexpr (I8 && DP == 64) {
-                const uint2 w = on && 8 * g < dim ? __ldcs(reinterpret_cast<const uint2*>(p + 8 * g)) : make_uint2(0u, 0u);
-                vr[r][0] = make_uint4(w.x, w.y, 0u, 0u);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kVLoads; ++i) vr[r][i] = ld16(p + 16 * (g + 8 * i), on && 16 * (g + 8 * i) < dim * kE);
-            }
-        }
+        float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
         if constexpr (I8) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) vs[r] = row >= 0 && j + g + 8 * r < end ? __ldg(a.c.v_scale + row + g + 8 * r) : 0.f;
+            for (int r = 0; r < 2; ++r) {
+                ks[r] = lds4(base + 2 * R::kRows + 4 * (g + 8 * r));
+                ks[r] = fmaf(0.f, ks[r], ks[r]);        // +inf stands for a row that reads as NaN
+                vs[r] = lds4(base + 2 * R::kRows + 64 + 4 * (g + 8 * r));
+            }
         }
-        const int64_t next = row_of(j + kUnit * kWarps);
-
-        // ---- scores: S^T = K q^T
-        float s[NT][4];
+        // ---- scores: S^T = K q^T, in two chains of products
+        float s[NT][4], s1[NT][4];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[i][e] = s0[i][e & 1], s1[i][e] = 0.f;
+        if constexpr (I8) {
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-            uint32_t af[4];
-            if constexpr (I8) {
-                const uint4 w0 = kr[0][st >> 2], w1 = kr[1][st >> 2];
-                const uint32_t x0 = ((st & 3) == 0 ? w0.x : (st & 3) == 1 ? w0.y : (st & 3) == 2 ? w0.z : w0.w) ^ 0x80808080u;
-                const uint32_t x1 = ((st & 3) == 0 ? w1.x : (st & 3) == 1 ? w1.y : (st & 3) == 2 ? w1.z : w1.w) ^ 0x80808080u;
-                af[0] = halves<0x4140>(x0);
-                af[1] = halves<0x4140>(x1);
-                af[2] = halves<0x4342>(x0);
-                af[3] = halves<0x4342>(x1);
+            for (int ld = 0; ld < DP / 32; ++ld) {      // 32 dimensions: two chunks of 16
+                uint32_t x[4];
+                matrices(x, base + R::step(key_at, 2 * ld));
 #pragma unroll
-                for (int i = 0; i < NT; ++i) mma_f16(s[i], af, qb[i][st][0], qb[i][st][1]);
-            } else {
-                const uint4 w0 = kr[0][st >> 1], w1 = kr[1][st >> 1];
-                af[0] = st & 1 ? w0.z : w0.x;
-                af[1] = st & 1 ? w1.z : w1.x;
-                af[2] = st & 1 ? w0.w : w0.y;
-                af[3] = st & 1 ? w1.w : w1.y;
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t af[4] = {raised<false>(x[2 * u]), raised<false>(x[2 * u + 1]),
+                                            raised<true>(x[2 * u]), raised<true>(x[2 * u + 1])};
 #pragma unroll
-                for (int i = 0; i < NT; ++i) mma_b16(s[i], af, qb[i][st][0], qb[i][st][1]);
+                    for (int i = 0; i < NT; ++i)
+                        mma_f16(u ? s1[i] : s[i], af, qb[i][2 * ld + u][0], qb[i][2 * ld + u][1]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int st = 0; st < kSteps; ++st) {       // 16 dimensions: two chunks of 8
+                uint32_t x[4];
+                matrices(x, base + R::step(key_at, 2 * st));
+#pragma unroll
+                for (int i = 0; i < NT; ++i) mma_b16(st & 1 ? s1[i] : s[i], x, qb[i][st][0], qb[i][st][1]);
             }
         }
         // ---- softmax weights; s[i][2 r + e]: key g + 8 r, head 2t + e
-        bool see[2];
-        float lv[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            see[r] = row >= 0 && j + g + 8 * r < end;
-            lv[r] = I8 ? lg2(vs[r]) : 0.f;              // log2 of 0 is -inf: a row of zeros weighs nothing
-        }
         bool grow = false;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
@@ -265,97 +377,117 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float& x = s[i][2 * r + e];
-                    x = see[r] ? x * (I8 ? ch[i][e] * ks[r] : ch[i][e]) : -INFINITY;
-                    grow = grow || x > m[i][e] + kSlack || (I8 && x + lv[r] > mw[i][e] + kSlack);
+                    x = (x + s1[i][2 * r + e]) * (I8 ? ch[i][e] * ks[r] : ch[i][e]);
+                    if (j + kUnit > end) x = j + g + 8 * r < end ? x : -INFINITY;
+                    grow = grow || x > m[i][e] + kSlack;
                 }
-        load_keys(next);
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float x = fmaxf(s[i][e], s[i][2 + e]);
-                    float y = I8 ? fmaxf(s[i][e] + lv[0], s[i][2 + e] + lv[1]) : x;
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) {
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                        if constexpr (I8) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
-                    }
-                    if constexpr (!I8) y = x;
-                    const float mn = fmaxf(m[i][e], x), wn = fmaxf(mw[i][e], y);
-                    // nothing yet: 2^(-inf - m) = 0 scales a zero
-                    if (mn > -INFINITY) l[i][e] *= ex2(m[i][e] - mn);
-                    const float f = wn > -INFINITY ? ex2(mw[i][e] - wn) : 1.f;
-                    m[i][e] = mn;
-                    mw[i][e] = wn;
+                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    x = fmaxf(m[i][e], x);
+                    const float f = x > -INFINITY ? ex2(m[i][e] - x) : 1.f;     // nothing yet: 2^-inf scales a zero
+                    l[i][e] *= f;
+                    m[i][e] = x;
+                    if constexpr (I8) {
+                        fw[i][e] = ex2(x - mw[i][e] + kLift);
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        o[i][k][e] *= f;
-                        o[i][k][2 + e] *= f;
+                        for (int k = 0; k < DP / 16; ++k) {
+                            o[i][k][e] *= f;
+                            o[i][k][2 + e] *= f;
+                        }
                     }
                 }
+        }
+        float w[NT][4];
+        grow = false;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {           // a reference of -inf: nothing but -inf so far, weights 0
+                    const float p = ex2(s[i][2 * r + e] - (m[i][e] == -INFINITY ? 0.f : m[i][e]));
+                    l[i][e] += p;
+                    w[i][2 * r + e] = I8 ? p * (fw[i][e] * vs[r]) : p;
+                    grow = grow || (I8 && !(w[i][2 * r + e] <= kMost));
+                }
+        if constexpr (I8) {
+            if (__any_sync(0xffffffffu, grow)) {        // too large for fp16: a new reference of the weights
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float y = fmaxf(s[i][e] + lg2(vs[0]), s[i][2 + e] + lg2(vs[1]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                        y = fmaxf(mw[i][e], y);
+                        const float f = y > -INFINITY ? ex2(mw[i][e] - y) : 1.f;
+                        mw[i][e] = y;
+                        fw[i][e] = ex2(m[i][e] - y + kLift);
+#pragma unroll
+                        for (int k = 0; k < DP / 16; ++k) {
+                            o[i][k][e] *= f;
+                            o[i][k][2 + e] *= f;
+                        }
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)     // a row of zeros, or none seen: weight 0
+                            w[i][2 * r + e] = s[i][2 * r + e] == -INFINITY || vs[r] == 0.f
+                                                  ? 0.f
+                                                  : ex2(s[i][2 * r + e] + lg2(vs[r]) - ((y == -INFINITY ? 0.f : y) - kLift));
+                    }
+            }
         }
         uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float p[2], w[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {           // a reference of -inf: nothing but -inf so far, weights 0
-                    p[e] = see[r] ? ex2(s[i][2 * r + e] - (m[i][e] == -INFINITY ? 0.f : m[i][e])) : 0.f;
-                    l[i][e] += p[e];
-                    w[e] = p[e];
-                    if constexpr (I8)
-                        w[e] = see[r] ? ex2(s[i][2 * r + e] + lv[r] - ((mw[i][e] == -INFINITY ? 0.f : mw[i][e]) - kLift)) : 0.f;
-                }
+                const float w0 = w[i][2 * r], w1 = w[i][2 * r + 1];
                 if constexpr (I8) {
-                    pb[i][r] = transpose8(pack_h(w[0], w[1]));
+                    pb[i][r] = transpose8(pack_h(w0, w1));
                     pl[i][r] = 0u;
                 } else {
-                    const uint32_t hi = pack_b(w[0], w[1]);
+                    const uint32_t hi = pack_b(w0, w1);
                     pb[i][r] = transpose8(hi);
-                    pl[i][r] = transpose8(pack_b(w[0] - __uint_as_float(hi << 16), w[1] - __uint_as_float(hi & 0xffff0000u)));
+                    pl[i][r] = transpose8(pack_b(w0 - __uint_as_float(hi << 16), w1 - __uint_as_float(hi & 0xffff0000u)));
                 }
             }
-        // ---- O^T += V^T P^T: product k's rows g and g + 8 are the dimensions d and d + 1 of the lane's bytes
+        // ---- O^T += V^T P^T
+        if constexpr (I8) {
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-            uint32_t af[4];
-            if constexpr (I8) {
-                uint32_t x[4];                          // the word of four dimensions in each of the four rows
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    x[r] = ((k >> 1) == 0 ? vr[r][0].x : (k >> 1) == 1 ? vr[r][0].y : (k >> 1) == 2 ? vr[r][0].z : vr[r][0].w) ^
-                           0x80808080u;
-                const uint32_t y0 = __byte_perm(x[0], x[1], k & 1 ? 0x7362 : 0x5140);   // d of both keys, d + 1 of both
-                const uint32_t y1 = __byte_perm(x[2], x[3], k & 1 ? 0x7362 : 0x5140);
-                af[0] = halves<0x4140>(y0);
-                af[1] = halves<0x4342>(y0);
-                af[2] = halves<0x4140>(y1);
-                af[3] = halves<0x4342>(y1);
-#pragma unroll
-                for (int i = 0; i < NT; ++i) mma_f16(o[i][k], af, pb[i][0], pb[i][1]);
-            } else {
+            for (int ld = 0; ld < DP / 32; ++ld) {
                 uint32_t x[4];
+                matrices_t(x, base + R::kRows + R::step(val_at, 2 * ld));
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint4 v = vr[r][k >> 2];
-                    x[r] = (k & 3) == 0 ? v.x : (k & 3) == 1 ? v.y : (k & 3) == 2 ? v.z : v.w;
+                for (int u = 0; u < 2; ++u) {           // rows g and g + 8: dimensions 2g and 2g + 1 of the chunk
+                    const uint32_t af[4] = {halves<false>(x[2 * u]), halves<true>(x[2 * u]),
+                                            halves<false>(x[2 * u + 1]), halves<true>(x[2 * u + 1])};
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) mma_f16(o[i][2 * ld + u], af, pb[i][0], pb[i][1]);
                 }
-                af[0] = __byte_perm(x[0], x[1], 0x5410);
-                af[1] = __byte_perm(x[0], x[1], 0x7632);
-                af[2] = __byte_perm(x[2], x[3], 0x5410);
-                af[3] = __byte_perm(x[2], x[3], 0x7632);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) {
+                uint32_t x[4];
+                matrices_t(x, base + R::kRows + R::step(val_at, 2 * k));
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    mma_b16(o[i][k], af, pb[i][0], pb[i][1]);
-                    mma_b16(o[i][k], af, pl[i][0], pl[i][1]);
+                    mma_b16(o[i][k], x, pb[i][0], pb[i][1]);
+                    mma_b16(o[i][k], x, pl[i][0], pl[i][1]);
                 }
             }
         }
-        row = next;
+        __syncwarp();                                   // every lane is done with the stage
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();                                    // the rings become the warps' parts
 
     // ---- the warps' parts joined
 #pragma unroll
@@ -372,66 +504,107 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
             }
 #pragma unroll
             for (int k = 0; k < DP / 16; ++k) {
-                const int d = I8 ? (DP == 64 ? 8 * g + 2 * k : 16 * g + 2 * k) : 8 * (g + 8 * (k >> 2)) + 2 * (k & 3);
-                *reinterpret_cast<float2*>(&s_o[warp][hd][d]) = make_float2(o[i][k][e], o[i][k][2 + e]);
+                if constexpr (I8) {
+                    *reinterpret_cast<float2*>(&s_o[warp][hd][16 * k + 2 * g]) = make_float2(o[i][k][e], o[i][k][2 + e]);
+                } else {
+                    s_o[warp][hd][16 * k + g] = o[i][k][e];
+                    s_o[warp][hd][16 * k + 8 + g] = o[i][k][2 + e];
+                }
             }
         }
     __syncthreads();
-    for (int x = threadIdx.x; x < nh * DP; x += kThreads) {
-        const int hd = x / DP, d = x % DP;
-        float M = -INFINITY;
+    if (threadIdx.x < kHeads) {
+        // one head's maximum and sum over the warps, and what its parts are multiplied by; a warp that saw
+        // no key has m = -inf and counts 0
+        const int hd = threadIdx.x;
+        float M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][hd]);
-        float L = 0.f, acc = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            if (s_m[w][hd] == -INFINITY) continue;      // no key of this warp was seen
-            L += s_l[w][hd] * ex2(s_m[w][hd] - M);
-            if (s_w[w][hd] > -INFINITY || s_w[w][hd] != s_w[w][hd]) acc += s_o[w][hd][d] * ex2(s_w[w][hd] - M);
+            const bool any = s_m[w][hd] > -INFINITY || s_m[w][hd] != s_m[w][hd] || s_l[w][hd] != s_l[w][hd];
+            L += any ? s_l[w][hd] * ex2(s_m[w][hd] - M) : 0.f;
+            s_w[w][hd] = any ? ex2(s_w[w][hd] - M) : 0.f;
         }
+        s_m[0][hd] = M;
+        s_l[0][hd] = L;
         const int64_t at = (int64_t)b * a.n_q + h0 + hd;
-        if (cut.pieces == 1) {
-            if (d < dim)
-                reinterpret_cast<Tout*>(a.out)[(int64_t)b * a.o_st + (int64_t)(h0 + hd) * a.o_sh + d] =
-                    from_f32<Tout>(M == -INFINITY ? 0.f : acc / L);
-            if (a.lse && d == 0) a.lse[at] = M == -INFINITY ? -INFINITY : kLn2 * (M + log2f(L));
-        } else {
-            float* ws = reinterpret_cast<float*>(a.workspace);
-            const int64_t piece = at * cut.pieces + blockIdx.x;
-            ws[piece * DP + d] = acc;
-            if (d == 0) {
-                float2* ml = reinterpret_cast<float2*>(ws + (int64_t)gridDim.z * a.n_q * cut.pieces * DP);
-                ml[piece] = make_float2(M, L);
-            }
+        if (hd < nh && cut.pieces > 1)
+            piece_sums<DP>(a, cut, gridDim.z)[at * cut.pieces + blockIdx.x] = make_float2(M, L);
+        if (hd < nh && cut.pieces == 1 && a.lse) a.lse[at] = lse_of(M, L);
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < nh * (DP / 4); x += kThreads) {
+        const int hd = x / (DP / 4), d = 4 * (x % (DP / 4));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(&s_o[w][hd][d]);
+            const float f = s_w[w][hd];
+            acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+        }
+        if (cut.pieces > 1) {
+            const int64_t piece = ((int64_t)b * a.n_q + h0 + hd) * cut.pieces + blockIdx.x;
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.workspace) + piece * DP + d) = acc;
+        } else if (d < dim) {
+            store_out(reinterpret_cast<Tout*>(a.out) + (int64_t)b * a.o_st + (int64_t)(h0 + hd) * a.o_sh + d, acc,
+                      s_l[0][hd]);
         }
     }
 }
 
-// Joins the pieces of one (request, head): out = sum_p o_p 2^(m_p - m) / sum_p l_p 2^(m_p - m).
+// Joins the pieces of one (request, head): out = sum_p o_p 2^(m_p - m) / sum_p l_p 2^(m_p - m).  Eight
+// warps take every eighth piece (every sixteenth pair, for 64 dimensions), four dimensions a lane, so that
+// a hundred pieces cost a few loads' latency.
+constexpr int kJoinWarps = 8;
 template <int DP, typename Tout>
-__global__ void __launch_bounds__(DP)
+__global__ void __launch_bounds__(32 * kJoinWarps)
 k_attn_decode_join(const AttnDecodeArgs a, const Cut cut) {
-    const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+    constexpr int kLanes = DP / 4, kRows = kJoinWarps * 32 / kLanes;     // lanes of a piece's row, rows side by side
+    __shared__ float s_max[kJoinWarps], s_sum[kRows];
+    __shared__ float4 s_acc[kRows][kLanes];
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const int sub = tid % kLanes, first = tid / kLanes;
     const int len = length_of(a, b, false);
     const int n = (len + cut.tokens - 1) / cut.tokens;
     const int64_t at = (int64_t)b * a.n_q + h;
-    const float* ws = reinterpret_cast<const float*>(a.workspace) + at * cut.pieces * DP + d;
-    const float2* ml = reinterpret_cast<const float2*>(reinterpret_cast<const float*>(a.workspace) +
-                                                       (int64_t)a.batch * a.n_q * cut.pieces * DP) + at * cut.pieces;
+    const float4* rows = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.workspace) + at * cut.pieces * DP) + sub;
+    const float2* ml = piece_sums<DP>(a, cut, a.batch) + at * cut.pieces;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    float M = -INFINITY, L = 0.f, acc = 0.f;
-    for (int p = 0; p < n; ++p) M = fmaxf(M, ml[p].x);
-#pragma unroll 8
-    for (int p = 0; p < n; ++p) {
+    float M = -INFINITY;
+    for (int p = tid; p < n; p += 32 * kJoinWarps) M = fmaxf(M, ml[p].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    if ((tid & 31) == 0) s_max[tid >> 5] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_max[w]);
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = first; p < n; p += kRows) {
         const float2 x = ml[p];
-        const float f = x.x == -INFINITY ? 0.f : ex2(x.x - M);
+        const float4 v = rows[(int64_t)p * kLanes];
+        const float f = x.x == -INFINITY && x.y == 0.f ? 0.f : ex2(x.x - M);      // a piece that saw no key
         L += x.y * f;
-        acc += f == 0.f ? 0.f : ws[(int64_t)p * DP] * f;
+        acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
     }
-    if (d < a.c.dim)
-        reinterpret_cast<Tout*>(a.out)[(int64_t)b * a.o_st + (int64_t)h * a.o_sh + d] =
-            from_f32<Tout>(M == -INFINITY ? 0.f : acc / L);
-    if (a.lse && d == 0) a.lse[at] = M == -INFINITY ? -INFINITY : kLn2 * (M + log2f(L));
+    s_acc[first][sub] = acc;
+    if (sub == 0) s_sum[first] = L;
+    __syncthreads();
+    if (tid < kLanes) {
+        L = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const float4 v = s_acc[r][tid];
+            L += s_sum[r];
+            acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
+        if (4 * tid < a.c.dim)
+            store_out(reinterpret_cast<Tout*>(a.out) + (int64_t)b * a.o_st + (int64_t)h * a.o_sh + 4 * tid, acc, L);
+        if (a.lse && tid == 0) a.lse[at] = lse_of(M, L);
+    }
 }
 
 // CTAs side by side for one request's long axis: one per kv head and group of 16 (or 8) query heads.
@@ -462,14 +635,18 @@ Cut cut_of(int batch, int n_q, int n_kv, int64_t max_len) {
 template <bool I8, int DP, int NT, typename Tout>
 int launch(const AttnDecodeArgs& a, cudaStream_t stream, const char** why) {
     const Cut cut = cut_of(a.batch, a.n_q, a.c.n_kv, a.max_len);
+    constexpr int kRing = kWarps * Ring<I8, DP>::kStages * Ring<I8, DP>::kStage, kParts = kWarps * 8 * NT * DP * 4;
+    constexpr int kSmem = kRing > kParts ? kRing : kParts;
+    static ContextMemo attr_memo;
+    if (!opt_in_dynamic_smem(attr_memo, k_attn_decode<I8, DP, NT, Tout>, kSmem, why)) return -1;
     const dim3 grid((unsigned)cut.pieces, (unsigned)lanes_of(a.n_q, a.c.n_kv), (unsigned)a.batch);
-    k_attn_decode<I8, DP, NT, Tout><<<grid, kThreads, 0, stream>>>(a, cut);
+    k_attn_decode<I8, DP, NT, Tout><<<grid, kThreads, kSmem, stream>>>(a, cut);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && cut.pieces > 1) {
         // launched while the pieces still run; it waits for them before it reads
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)a.n_q, (unsigned)a.batch);
-        cfg.blockDim = dim3(DP);
+        cfg.blockDim = dim3(32 * kJoinWarps);
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
