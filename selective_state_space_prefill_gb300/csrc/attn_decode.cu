@@ -84,6 +84,9 @@ __device__ __forceinline__ uint32_t pack_b(float lo, float hi) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool on) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
 }
@@ -166,7 +169,7 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
     constexpr int kE = I8 ? 1 : 2;
     extern __shared__ __align__(128) unsigned char smem[];      // the warps' rings, then their parts
     __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads], s_w[kWarps][kHeads];
-    float(*s_o)[kHeads][DP] = reinterpret_cast<float(*)[kHeads][DP]>(smem);
+    float(*s_o)[kHeads][DP + 4] = reinterpret_cast<float(*)[kHeads][DP + 4]>(smem);     // + 4: no bank twice
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -210,12 +213,11 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
             const uint32_t dst = ring + (uint32_t)(st * R::kStage);
             const char* kp = reinterpret_cast<const char*>(a.c.k) + row * row_bytes + lane_off;
             const char* vp = reinterpret_cast<const char*>(a.c.v) + row * row_bytes + lane_off;
-            if (j + kUnit <= end) {
+            if (j + kUnit <= end && dim == DP) {        // whole rows, their places known to the compiler
 #pragma unroll
                 for (int r = 0; r < kUnit; r += kPerPass) {
-                    copy16(dst + R::at(r0 + r, ch16), kp, in);
-                    copy16(dst + R::kRows + R::at(r0 + r, ch16), vp, in);
-                    if (in) kp += pass_bytes, vp += pass_bytes;
+                    copy16(dst + R::at(r0 + r, ch16), kp + r * R::kRow);
+                    copy16(dst + R::kRows + R::at(r0 + r, ch16), vp + r * R::kRow);
                 }
             } else {
 #pragma unroll 1
@@ -274,22 +276,22 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
             // 2^e with qmax 2^e in [2^10, 2^11); the exponent kept where 2^e and 2^(24-e) are normal
             const int e = qmax > 0.f ? max(-90, min(90, 137 - (int)(__float_as_uint(qmax) >> 23))) : 0;
             const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 + 24 - e) << 23);
-            float sum = 0.f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t w = qb[i][s][k];
                     qb[i][s][k] = pack_h(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
-                    const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&qb[i][s][k]));
-                    sum += r.x + r.y;
                 }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            // the product with a key of codes 0
+            float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t key0[4] = {0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) mma_f16(zero, key0, qb[i][s][0], qb[i][s][1]);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {               // lane 4 n holds head n's
                 ch[i][x] *= __shfl_sync(0xffffffffu, down, 8 * t + 4 * x);
-                s0[i][x] = __shfl_sync(0xffffffffu, sum, 8 * t + 4 * x) * -7.62939453125e-6f;      // -128 x 2^-24
+                s0[i][x] = -zero[x];
             }
         } else {
 #pragma unroll
@@ -302,7 +304,8 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
     }
 
     float o[NT][DP / 16][4];
-    float m[NT][2], mw[NT][2], fw[NT][2], l[NT][2];     // of heads 2t, 2t + 1; fw = 2^(m - mw + kLift)
+    // of heads 2t, 2t + 1: references (mz: m, or 0 while m is -inf), fw = 2^(m - mw + kLift), sum
+    float m[NT][2], mz[NT][2], mw[NT][2], fw[NT][2], l[NT][2];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -310,7 +313,7 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][k][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) m[i][e] = mw[i][e] = -INFINITY, fw[i][e] = INFINITY, l[i][e] = 0.f;
+        for (int e = 0; e < 2; ++e) m[i][e] = mw[i][e] = -INFINITY, mz[i][e] = 0.f, fw[i][e] = INFINITY, l[i][e] = 0.f;
     }
 
     for (; j < end; j += kStep) {
@@ -393,6 +396,7 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
                     const float f = x > -INFINITY ? ex2(m[i][e] - x) : 1.f;     // nothing yet: 2^-inf scales a zero
                     l[i][e] *= f;
                     m[i][e] = x;
+                    mz[i][e] = x > -INFINITY ? x : 0.f;         // nothing but -inf so far: weights 0
                     if constexpr (I8) {
                         fw[i][e] = ex2(x - mw[i][e] + kLift);
                     } else {
@@ -411,8 +415,8 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {           // a reference of -inf: nothing but -inf so far, weights 0
-                    const float p = ex2(s[i][2 * r + e] - (m[i][e] == -INFINITY ? 0.f : m[i][e]));
+                for (int e = 0; e < 2; ++e) {
+                    const float p = ex2(s[i][2 * r + e] - mz[i][e]);
                     l[i][e] += p;
                     w[i][2 * r + e] = I8 ? p * (fw[i][e] * vs[r]) : p;
                     grow = grow || (I8 && !(w[i][2 * r + e] <= kMost));
@@ -553,32 +557,35 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
     }
 }
 
-// Joins the pieces of one (request, head): out = sum_p o_p 2^(m_p - m) / sum_p l_p 2^(m_p - m).  Eight
-// warps take every eighth piece (every sixteenth pair, for 64 dimensions), four dimensions a lane, so that
-// a hundred pieces cost a few loads' latency.
+// Joins the pieces of each (request, head): out = sum_p o_p 2^(m_p - m) / sum_p l_p 2^(m_p - m).  W warps
+// of a block of eight share one head's pieces, four dimensions a lane, so that a hundred pieces cost a
+// few loads' latency and a few pieces no idle warps.
 constexpr int kJoinWarps = 8;
-template <int DP, typename Tout>
+template <int DP, int W, typename Tout>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 k_attn_decode_join(const AttnDecodeArgs a, const Cut cut) {
-    constexpr int kLanes = DP / 4, kRows = kJoinWarps * 32 / kLanes;     // lanes of a piece's row, rows side by side
-    __shared__ float s_max[kJoinWarps], s_sum[kRows];
-    __shared__ float4 s_acc[kRows][kLanes];
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    constexpr int kLanes = DP / 4, kRows = W * 32 / kLanes;     // lanes of a piece's row, rows side by side
+    constexpr int kSides = kJoinWarps / W;                      // heads of a block
+    __shared__ float s_max[kJoinWarps], s_sum[kSides][kRows];
+    __shared__ float4 s_acc[kSides][kRows][kLanes];
+    const int side = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W);
+    const int h = blockIdx.x * kSides + side, b = blockIdx.y;
     const int sub = tid % kLanes, first = tid / kLanes;
-    const int len = length_of(a, b, false);
-    const int n = (len + cut.tokens - 1) / cut.tokens;
+    const int n = h < a.n_q ? (length_of(a, b, false) + cut.tokens - 1) / cut.tokens : 0;
     const int64_t at = (int64_t)b * a.n_q + h;
     const float4* rows = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.workspace) + at * cut.pieces * DP) + sub;
     const float2* ml = piece_sums<DP>(a, cut, a.batch) + at * cut.pieces;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float M = -INFINITY;
-    for (int p = tid; p < n; p += 32 * kJoinWarps) M = fmaxf(M, ml[p].x);
+    for (int p = tid; p < n; p += 32 * W) M = fmaxf(M, ml[p].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    if ((tid & 31) == 0) s_max[tid >> 5] = M;
-    __syncthreads();
+    if constexpr (W > 1) {
+        if ((tid & 31) == 0) s_max[tid >> 5] = M;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, s_max[w]);
+        for (int w = 0; w < W; ++w) M = fmaxf(M, s_max[w]);
+    }
     float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -589,16 +596,16 @@ k_attn_decode_join(const AttnDecodeArgs a, const Cut cut) {
         L += x.y * f;
         acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
     }
-    s_acc[first][sub] = acc;
-    if (sub == 0) s_sum[first] = L;
+    s_acc[side][first][sub] = acc;
+    if (sub == 0) s_sum[side][first] = L;
     __syncthreads();
-    if (tid < kLanes) {
+    if (tid < kLanes && h < a.n_q) {
         L = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
-            const float4 v = s_acc[r][tid];
-            L += s_sum[r];
+            const float4 v = s_acc[side][r][tid];
+            L += s_sum[side][r];
             acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
         }
         if (4 * tid < a.c.dim)
@@ -635,7 +642,7 @@ Cut cut_of(int batch, int n_q, int n_kv, int64_t max_len) {
 template <bool I8, int DP, int NT, typename Tout>
 int launch(const AttnDecodeArgs& a, cudaStream_t stream, const char** why) {
     const Cut cut = cut_of(a.batch, a.n_q, a.c.n_kv, a.max_len);
-    constexpr int kRing = kWarps * Ring<I8, DP>::kStages * Ring<I8, DP>::kStage, kParts = kWarps * 8 * NT * DP * 4;
+    constexpr int kRing = kWarps * Ring<I8, DP>::kStages * Ring<I8, DP>::kStage, kParts = kWarps * 8 * NT * (DP + 4) * 4;
     constexpr int kSmem = kRing > kParts ? kRing : kParts;
     static ContextMemo attr_memo;
     if (!opt_in_dynamic_smem(attr_memo, k_attn_decode<I8, DP, NT, Tout>, kSmem, why)) return -1;
@@ -645,7 +652,8 @@ int launch(const AttnDecodeArgs& a, cudaStream_t stream, const char** why) {
     if (e == cudaSuccess && cut.pieces > 1) {
         // launched while the pieces still run; it waits for them before it reads
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)a.n_q, (unsigned)a.batch);
+        const bool many = cut.pieces > 16;              // a warp joins up to 16 pieces in two rounds of loads
+        cfg.gridDim = dim3((unsigned)(many ? a.n_q : (a.n_q + kJoinWarps - 1) / kJoinWarps), (unsigned)a.batch);
         cfg.blockDim = dim3(32 * kJoinWarps);
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
@@ -653,7 +661,8 @@ int launch(const AttnDecodeArgs& a, cudaStream_t stream, const char** why) {
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, k_attn_decode_join<DP, Tout>, a, cut);
+        e = many ? cudaLaunchKernelEx(&cfg, k_attn_decode_join<DP, kJoinWarps, Tout>, a, cut)
+                 : cudaLaunchKernelEx(&cfg, k_attn_decode_join<DP, 1, Tout>, a, cut);
         if (e == cudaSuccess) e = cudaGetLastError();
     }
     if (e == cudaSuccess) return 0;
