@@ -24,7 +24,7 @@
 //     sequence are zeroed; non-finite values are zeroed and noted (the first key of each column
 //     that holds +inf, -inf, NaN), and the rows that do see them get them back at the end.
 // TMEM: scores of tile t at column 128 t, output at 256 + 128 t; all 512 columns, one CTA per SM.
-// The grid runs the longest rows first (the last tiles of every head), so the tail is short.
+// The grid runs the longest rows first (the last tiles of every head and sequence), so the tail is short.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -39,6 +39,12 @@ constexpr int kM = 128;                 // query rows per tile
 constexpr int kN = 128;                 // keys per block
 constexpr int kThreads = 384;
 constexpr float kSlack = 8.0f;
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
 
 template <int DP>                       // head_dim padded to 64 or 128
 struct Geo {
@@ -142,8 +148,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     using G = Geo<DP>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_err, s_bad;
-    const int h = (int)(blockIdx.x % (unsigned)a.n_q), b = blockIdx.y;
-    const int row0 = (int)((gridDim.x - 1 - blockIdx.x) / (unsigned)a.n_q) * 2 * kM;
+    const int h = (int)(blockIdx.x % (unsigned)a.n_q), b = (int)(blockIdx.x / (unsigned)a.n_q % (unsigned)a.batch);
+    const int row0 = (int)((gridDim.x - 1 - blockIdx.x) / ((unsigned)a.n_q * (unsigned)a.batch)) * 2 * kM;
     // the sequence's rows, kept inside the tensors whatever cu_q and cu_k hold
     const int q0 = min(max(a.cu_q[b], 0), (int)a.total_q), k0 = min(max(a.cu_k[b], 0), (int)a.total_k);
     const int lq = min(min(a.cu_q[b + 1], (int)a.total_q) - q0, a.max_q);
@@ -386,52 +392,70 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             for (int t = 0; t < 2; ++t)
                 if ((t ? n1 : n0) > 0 && !mbar_wait_bounded(&q_full[t], 0)) expired();
-        } else if (warp == 9 && lane == 0 && nb > 0) {
-            // ---- MMA issuer
-            const int dsteps = a.dim / 16;
+        } else if (warp == 9 && nb > 0) {
+            // ---- MMA issuer: the whole warp walks the loop, so that descriptors stay in uniform registers
+            // (32 products a block leave 64 cycles for each), one elected lane issues
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                if (ok && !mbar_wait_bounded(bar, parity)) {
+                if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity))) {
                     ok = false;
                     expired();
                 }
             };
-            auto scores = [&](int t, int j) {                // S_t = Q_t K_j^T
-                const uint32_t qa = smem_u32(smem + t * G::kTile);
-                const uint32_t ka = smem_u32(smem + G::kOffKV + ((2 * j) % G::kSlots) * G::kTile);
-                for (int k = 0; k < dsteps; ++k)
-                    mma_bf16(tmem + (uint32_t)(128 * t), smem_desc_sw128(qa + (k >> 2) * 16384 + 32 * (k & 3)),
-                             smem_desc_sw128(ka + (k >> 2) * 16384 + 32 * (k & 3)), G::kIdescS, k != 0);
-                mma_commit(&s_full[t]);
+            const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0), tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t qd = smem_desc_sw128(base), kd = smem_desc_sw128(base + G::kOffKV), vd = smem_desc_mn(base + G::kOffKV);
+            auto scores = [&](int t, int slot) {             // S_t = Q_t K^T
+                if (elect_one()) {
+                    const uint64_t q = qd + (uint64_t)(t * (G::kTile >> 4)), k = kd + (uint64_t)(slot * (G::kTile >> 4));
+#pragma unroll
+                    for (int s = 0; s < DP / 16; ++s) {      // dimensions past head_dim are zeros
+                        const uint64_t at = (uint64_t)((s >> 2) * (16384 >> 4) + 2 * (s & 3));
+                        mma_bf16(tm + (uint32_t)(128 * t), q + at, k + at, G::kIdescS, s != 0);
+                    }
+                    mma_commit(&s_full[t]);
+                }
+                __syncwarp();
+            };
+            auto output = [&](int t, int slot, bool first) { // O_t += P_t V
+                if (elect_one()) {
+                    const uint64_t v = vd + (uint64_t)(slot * (G::kTile >> 4));
+#pragma unroll
+                    for (int s = 0; s < kN / 16; ++s)        // 16 keys: 8 columns of P, 2048 bytes of V
+                        mma_bf16_ts(tm + (uint32_t)(256 + 128 * t), tm + (uint32_t)(128 * t + 8 * s),
+                                    v + (uint64_t)(s * (2048 >> 4)), G::kIdescO, s != 0 || !first);
+                    mma_commit(&o_full[t]);
+                }
+                __syncwarp();
+            };
+            auto release = [&](int slot) {
+                if (elect_one()) mma_commit(&kv_empty[slot]);
+                __syncwarp();
             };
             wait(&kv_full[0], 0);
-            for (int t = 0; t < 2 && ok; ++t) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
                 if ((t ? n1 : n0) == 0) continue;
                 wait(&q_full[t], 0);
                 tc_fence_after();
                 if (ok) scores(t, 0);
             }
-            if (ok) mma_commit(&kv_empty[0]);
+            if (ok) release(0);
             for (int j = 0; j < nb && ok; ++j) {
-                const int vi = 2 * j + 1, ki = 2 * j + 2;
-                wait(&kv_full[vi % G::kSlots], (uint32_t)((vi / G::kSlots) & 1));
+                const int vi = 2 * j + 1, ki = 2 * j + 2, vslot = vi % G::kSlots, kslot = ki % G::kSlots;
+                wait(&kv_full[vslot], (uint32_t)((vi / G::kSlots) & 1));
                 if (j >= mask_from) wait(&v_ok[j - mask_from], 0);
-                if (j + 1 < nb) wait(&kv_full[ki % G::kSlots], (uint32_t)((ki / G::kSlots) & 1));
-                const uint64_t vd = smem_desc_mn(smem_u32(smem + G::kOffKV + (vi % G::kSlots) * G::kTile));
-                for (int t = 0; t < 2 && ok; ++t) {
+                if (j + 1 < nb) wait(&kv_full[kslot], (uint32_t)((ki / G::kSlots) & 1));
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
                     const int n = t ? n1 : n0;
                     if (j >= n) continue;
                     wait(&p_full[t], (uint32_t)(j & 1));
-                    if (!ok) break;
                     tc_fence_after();
-                    for (int k = 0; k < kN / 16; ++k)        // 16 keys: 8 columns of P, 2048 bytes of V
-                        mma_bf16_ts(tmem + 256u + (uint32_t)(128 * t), tmem + (uint32_t)(128 * t + 8 * k),
-                                    vd + (uint64_t)(2048 >> 4) * k, G::kIdescO, (j | k) != 0);
-                    mma_commit(&o_full[t]);
-                    if (j + 1 < n) scores(t, j + 1);
+                    if (ok) output(t, vslot, j == 0);
+                    if (ok && j + 1 < n) scores(t, kslot);
                 }
-                if (ok) mma_commit(&kv_empty[vi % G::kSlots]);
-                if (ok && j + 1 < nb) mma_commit(&kv_empty[ki % G::kSlots]);
+                if (ok) release(vslot);
+                if (ok && j + 1 < nb) release(kslot);
             }
         } else if (warp >= 10) {
             // ---- value blocks that some row does not wholly see
@@ -513,11 +537,11 @@ int launch_dp(const AttnPrefillArgs& a, cudaStream_t stream, const char** why) {
     static ContextMemo attr;
     if (!opt_in_dynamic_smem(attr, kern, Geo<DP>::kSmem, why)) return -1;
     const int64_t tiles = ((int64_t)a.max_q + 2 * kM - 1) / (2 * kM);
-    if (tiles * a.n_q >= (1LL << 31)) {
-        *why = "heads times query tiles pass the grid";
+    if (tiles * a.n_q * a.batch >= (1LL << 31)) {
+        *why = "sequences times heads times query tiles pass the grid";
         return -1;
     }
-    const dim3 grid((unsigned)(tiles * a.n_q), (unsigned)a.batch);
+    const dim3 grid((unsigned)(tiles * a.n_q * a.batch));
     kern<<<grid, kThreads, Geo<DP>::kSmem, stream>>>(mq, mk, mv, a);
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) return 0;
