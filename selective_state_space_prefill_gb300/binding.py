@@ -13,7 +13,7 @@ from pathlib import Path
 
 import torch
 
-from .build import LIB
+from .build import CALLS, LIB
 
 SSM_F32, SSM_BF16, SSM_I8 = 0, 1, 2
 _STATUS = {0: "SSM_OK", -1: "SSM_ERR_INVALID_ARG", -2: "SSM_ERR_UNSUPPORTED", -3: "SSM_ERR_MISALIGNED",
@@ -570,57 +570,40 @@ def ssd_decode_step(xBC, z, dt, conv_w, conv_b, A, D, dt_bias, n_heads, n_groups
 
 
 # ------------------------------------------------------------------ attention (hybrid layers)
-_CACHE_CODE = {torch.int8: SSM_I8, torch.bfloat16: SSM_BF16}
+_calls = None
 
 
-def _stream_of(t, stream):
-    """The raw stream to launch on: the caller's, or torch's current one on t's device."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.device.index)
+def attn_calls():
+    """The extension that marshals the attention calls (csrc/attn_call.cpp): it checks the tensors,
+    allocates missing outputs and calls libssm, in the microsecond that a short step allows."""
+    global _calls
+    if _calls is None:
+        import importlib.machinery
+        import importlib.util
+
+        if not CALLS.exists():
+            raise ImportError(f"the attention calls are not built ({CALLS} missing): run "
+                              "`python -c 'import __graft_entry__ as g; g.build()'` first")
+        loader = importlib.machinery.ExtensionFileLoader("_attn_call", str(CALLS))
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_attn_call", loader))
+        loader.exec_module(mod)
+        lib = load()
+        mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.attn_append, lib.attn_cache_read, lib.attn_prefill, lib.attn_decode_workspace_bytes,
+            lib.attn_decode_step)))
+        _calls = mod
+    return _calls
 
 
-def _heads_view(t, name):
-    """(heads, dim, token stride, head stride) of a bf16 or fp32 [tokens, heads, dim] view.  A stride
-    along an extent of one moves nothing, so it is given as a value the library accepts."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    n, h, d = t.shape
-    st, sh, sd = t.stride()
-    if sd != 1 and d > 1:
-        raise ValueError(f"{name} must have channel stride 1")
-    if h == 1:
-        sh = d
-    if n <= 1:
-        st = h * sh
-    return h, d, st, sh
+def _outcome(r, fn):
+    """What an attention call returned: its outputs, or the status of its refusal."""
+    if type(r) is int:
+        raise SSMError(fn, r, load().ssm_last_error().decode())
+    return r
 
 
-def _int32(t, shape, name):
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int32 {tuple(shape)}")
-
-
-def _cache_args(k_cache, v_cache, k_scale, v_scale):
-    """(type code, n_pages, kv_heads, page_size, dim) of a paged cache."""
-    code = _CACHE_CODE.get(k_cache.dtype)
-    if code is None:
-        raise TypeError(f"unsupported cache dtype {k_cache.dtype} (int8 or bfloat16)")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype \
-            or not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_cache.is_cuda and v_cache.is_cuda):
-        raise ValueError("k_cache and v_cache must be contiguous CUDA tensors of one shape "
-                         "[n_pages, kv_heads, page_size, head_dim] and one dtype")
-    if code == SSM_I8:
-        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if t is None or t.dtype != torch.float32 or t.shape != k_cache.shape[:3] or not t.is_contiguous() \
-                    or not t.is_cuda:
-                raise ValueError(f"{n} must be a contiguous float32 CUDA tensor {tuple(k_cache.shape[:3])} "
-                                 "for an int8 cache")
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("a bfloat16 cache has no scales")
-    return (code, *k_cache.shape)
-
-
-def _dp(t):
-    return None if t is None else t.data_ptr()
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def attn_rope_table(inv_freq, n_pos, scale=1.0, device="cuda", stream=None):
@@ -632,8 +615,8 @@ def attn_rope_table(inv_freq, n_pos, scale=1.0, device="cuda", stream=None):
     cos = torch.empty(n_pos, len(freqs), device=device, dtype=torch.float32)
     sin = torch.empty_like(cos)
     _need_cuda(cos)
-    rc = lib.attn_rope_table(n_pos, len(freqs), ctypes.cast(arr, ctypes.c_void_p), float(scale), cos.data_ptr(),
-                             sin.data_ptr(), _stream_of(cos, stream))
+    rc = lib.attn_rope_table(n_pos, len(freqs), ctypes.cast(arr, ctypes.c_void_p), float(scale), _ptr(cos), _ptr(sin),
+                             _stream(stream))
     _check(lib, "attn_rope_table", rc)
     return cos, sin
 
@@ -647,63 +630,8 @@ def attn_append(q, k, v, positions, cos, sin, k_cache, v_cache, slots, k_scale=N
     float32) or bfloat16, updated in place.  cos, sin [n_pos, rot_dim / 2] float32; None leaves the heads
     unrotated.  q may be None.  q_out may be q and k_out may be k; ``k_out=True`` allocates the rotated
     keys.  Returns (q_out, k_out), None for what was not asked."""
-    lib = load()
-    code, n_pages, Hk, page, D = _cache_args(k_cache, v_cache, k_scale, v_scale)
-    T = k.shape[0]
-    hk, d, k_st, k_sh = _heads_view(k, "k")
-    hv, dv, v_st, v_sh = _heads_view(v, "v")
-    if hk != Hk or d != D or hv != Hk or dv != D or v.shape[0] != T:
-        raise ValueError("k and v must be [tokens, kv_heads, head_dim] of the cache")
-    bf = torch.bfloat16
-    if k.dtype != bf or v.dtype != bf or not (k.is_cuda and v.is_cuda and slots.is_cuda):
-        raise ValueError("k and v must be bfloat16 CUDA tensors, slots a CUDA tensor")
-    _int32(slots, (T,), "slots")
-    rot = n_pos = 0
-    if cos is not None:
-        n_pos, half = cos.shape
-        rot = 2 * half
-        if cos.dtype != torch.float32 or sin.dtype != torch.float32 or sin.shape != cos.shape \
-                or not (cos.is_contiguous() and sin.is_contiguous() and cos.is_cuda and sin.is_cuda):
-            raise ValueError("cos and sin must be contiguous float32 CUDA tensors [n_pos, half]")
-        _int32(positions, (T,), "positions")
-        if not positions.is_cuda:
-            raise ValueError("positions must be a CUDA tensor")
-    H, q_st, q_sh, qo_st, qo_sh = Hk, 0, 0, 0, 0
-    if q is not None:
-        H, dq, q_st, q_sh = _heads_view(q, "q")
-        if q.dtype != bf or not q.is_cuda or dq != D or q.shape[0] != T:
-            raise ValueError("q must be a bfloat16 CUDA tensor [tokens, heads, head_dim]")
-        if q_out is None:
-            q_out = torch.empty(q.shape, device=q.device, dtype=bf)
-        elif q_out.dtype != bf or q_out.shape != q.shape or not q_out.is_cuda:
-            raise ValueError("q_out must be shaped like q, bfloat16")
-        _, _, qo_st, qo_sh = _heads_view(q_out, "q_out")
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    ko_st = ko_sh = 0
-    if k_out is not None and k_out is not False:
-        if k_out is True:
-            k_out = torch.empty(k.shape, device=k.device, dtype=bf)
-        elif k_out.dtype != bf or k_out.shape != k.shape or not k_out.is_cuda:
-            raise ValueError("k_out must be shaped like k, bfloat16")
-        _, _, ko_st, ko_sh = _heads_view(k_out, "k_out")
-    else:
-        k_out = None
-    rc = lib.attn_append(T, H, Hk, D, rot, 1 if interleaved else 0, _dp(q), q_st, q_sh, k.data_ptr(), k_st, k_sh,
-                         v.data_ptr(), v_st, v_sh, _dp(positions) if rot else None, _dp(cos), _dp(sin), n_pos,
-                         slots.data_ptr(), code, k_cache.data_ptr(), v_cache.data_ptr(), _dp(k_scale), _dp(v_scale),
-                         n_pages, page, _dp(q_out), qo_st, qo_sh, _dp(k_out), ko_st, ko_sh, _stream_of(k, stream))
-    if rc:
-        _check(lib, "attn_append", rc)
-    return q_out, k_out
-
-
-def _table_args(page_table, batch):
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != batch \
-            or (page_table.stride(1) != 1 and page_table.shape[1] > 1) or not page_table.is_cuda:
-        raise ValueError("page_table must be an int32 CUDA tensor [batch, pages] with contiguous rows")
-    n = page_table.shape[1]
-    return page_table.stride(0) if batch > 1 else max(n, 1), n
+    return _outcome((_calls or attn_calls()).append(q, k, v, positions, cos, sin, k_cache, v_cache, slots, k_scale,
+                                                    v_scale, interleaved, q_out, k_out, _raw(stream)), "attn_append")
 
 
 def attn_cache_read(k_cache, v_cache, page_table, cu_len, n_tokens, k_scale=None, v_scale=None, first=None,
@@ -713,48 +641,8 @@ def attn_cache_read(k_cache, v_cache, page_table, cu_len, n_tokens, k_scale=None
     page_table [batch, pages] int32; cu_len [batch + 1] int32, cu_len[batch] = n_tokens; first [batch]
     int32 names each sequence's first token read (None: 0).  k_out and v_out are contiguous, bfloat16 or
     float32 (``out_dtype`` when allocated here)."""
-    lib = load()
-    code, n_pages, Hk, page, D = _cache_args(k_cache, v_cache, k_scale, v_scale)
-    batch = cu_len.shape[0] - 1
-    _int32(cu_len, (batch + 1,), "cu_len")
-    _need_cuda(cu_len, first, k_out, v_out)
-    if first is not None:
-        _int32(first, (batch,), "first")
-    ts, nt = _table_args(page_table, batch)
-    shape = (n_tokens, Hk, D)
-    if k_out is None:
-        k_out = torch.empty(shape, device=k_cache.device, dtype=out_dtype)
-    if v_out is None:
-        v_out = torch.empty(shape, device=k_cache.device, dtype=k_out.dtype)
-    if k_out.shape != shape or v_out.shape != shape or v_out.dtype != k_out.dtype \
-            or not (k_out.is_contiguous() and v_out.is_contiguous()):
-        raise ValueError(f"k_out and v_out must be contiguous {shape} of one dtype")
-    rc = lib.attn_cache_read(batch, n_tokens, Hk, D, code, k_cache.data_ptr(), v_cache.data_ptr(), _dp(k_scale),
-                             _dp(v_scale), n_pages, page, page_table.data_ptr(), ts, nt, cu_len.data_ptr(),
-                             _dp(first), _dtype_code(k_out.dtype), k_out.data_ptr(), v_out.data_ptr(),
-                             _stream_of(k_cache, stream))
-    if rc:
-        _check(lib, "attn_cache_read", rc)
-    return k_out, v_out
-
-
-def _attn_out(q, out, out_dtype):
-    if out is None:
-        out = torch.empty(q.shape, device=q.device, dtype=out_dtype)
-    elif out.shape != q.shape or not out.is_cuda:
-        raise ValueError("out must be a CUDA tensor shaped like q")
-    return out
-
-
-def _attn_lse(q, lse):
-    """The lse tensor to write: given, allocated for True, or None."""
-    if lse is None or lse is False:
-        return None
-    if lse is True:
-        return torch.empty(q.shape[:2], device=q.device, dtype=torch.float32)
-    if lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() or not lse.is_cuda:
-        raise ValueError("lse must be contiguous float32 [tokens, heads]")
-    return lse
+    return _outcome((_calls or attn_calls()).read(k_cache, v_cache, page_table, cu_len, n_tokens, k_scale, v_scale, first,
+                                                  k_out, v_out, out_dtype, _raw(stream)), "attn_cache_read")
 
 
 def attn_prefill(q, k, v, cu_q, cu_k, max_q, scale=None, out=None, out_dtype=torch.bfloat16, lse=None, stream=None):
@@ -762,29 +650,8 @@ def attn_prefill(q, k, v, cu_q, cu_k, max_q, scale=None, out=None, out_dtype=tor
     cu_q and cu_k [batch + 1] int32, max_q an upper bound of the sequences' query rows.  A sequence's last
     query sees its last key.  ``scale`` defaults to head_dim ** -0.5; ``lse=True`` also returns the log of
     each row's softmax sum [Tq, H] float32.  Returns (out, lse)."""
-    lib = load()
-    H, D, q_st, q_sh = _heads_view(q, "q")
-    Hk, dk, k_st, k_sh = _heads_view(k, "k")
-    hv, dv, v_st, v_sh = _heads_view(v, "v")
-    if dk != D or dv != D or hv != Hk or v.shape[0] != k.shape[0]:
-        raise ValueError("k and v must be [tokens, kv_heads, head_dim] of one shape, with q's head_dim")
-    if k.dtype != q.dtype or v.dtype != q.dtype or not (q.is_cuda and k.is_cuda and v.is_cuda):
-        raise ValueError("q, k and v must be CUDA tensors of one dtype")
-    batch = cu_q.shape[0] - 1
-    _int32(cu_q, (batch + 1,), "cu_q")
-    _int32(cu_k, (batch + 1,), "cu_k")
-    if not (cu_q.is_cuda and cu_k.is_cuda):
-        raise ValueError("cu_q and cu_k must be CUDA tensors")
-    out = _attn_out(q, out, out_dtype)
-    _, _, o_st, o_sh = _heads_view(out, "out")
-    lse = _attn_lse(q, lse)
-    rc = lib.attn_prefill(batch, q.shape[0], k.shape[0], max_q, H, Hk, D, _dtype_code(q.dtype),
-                          _dtype_code(out.dtype), q.data_ptr(), q_st, q_sh, k.data_ptr(), k_st, k_sh, v.data_ptr(),
-                          v_st, v_sh, cu_q.data_ptr(), cu_k.data_ptr(), D ** -0.5 if scale is None else scale,
-                          out.data_ptr(), o_st, o_sh, _dp(lse), _stream_of(q, stream))
-    if rc:
-        _check(lib, "attn_prefill", rc)
-    return out, lse
+    return _outcome((_calls or attn_calls()).prefill(q, k, v, cu_q, cu_k, max_q, scale, out, out_dtype, lse, _raw(stream)),
+                    "attn_prefill")
 
 
 def attn_decode_workspace_bytes(batch: int, n_heads: int, kv_heads: int, head_dim: int, max_len: int) -> int:
@@ -798,28 +665,5 @@ def attn_decode_step(q, k_cache, v_cache, page_table, lens, max_len, k_scale=Non
     (lens [batch] int32, at most max_len).  The cache and page_table are as for attn_cache_read.
     ``workspace`` (a CUDA uint8 tensor of at least attn_decode_workspace_bytes(...) bytes) is allocated
     here with torch when not given.  Returns (out, lse)."""
-    lib = load()
-    code, n_pages, Hk, page, D = _cache_args(k_cache, v_cache, k_scale, v_scale)
-    H, dq, q_st, q_sh = _heads_view(q, "q")
-    batch = q.shape[0]
-    if dq != D or not q.is_cuda or not lens.is_cuda:
-        raise ValueError("q must be a CUDA tensor [batch, heads, head_dim] with the cache's head_dim, lens on CUDA")
-    _int32(lens, (batch,), "lens")
-    ts, nt = _table_args(page_table, batch)
-    out = _attn_out(q, out, out_dtype)
-    _, _, o_st, o_sh = _heads_view(out, "out")
-    lse = _attn_lse(q, lse)
-    if workspace is None:
-        need = int(lib.attn_decode_workspace_bytes(batch, H, Hk, D, max_len))
-        workspace = torch.empty(max(need, 1), device=q.device, dtype=torch.uint8)
-    elif not workspace.is_contiguous() or not workspace.is_cuda:
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    rc = lib.attn_decode_step(batch, H, Hk, D, _dtype_code(q.dtype), _dtype_code(out.dtype), q.data_ptr(), q_st, q_sh,
-                              code, k_cache.data_ptr(), v_cache.data_ptr(), _dp(k_scale), _dp(v_scale), n_pages, page,
-                              page_table.data_ptr(), ts, nt, lens.data_ptr(), max_len,
-                              D ** -0.5 if scale is None else scale, out.data_ptr(), o_st, o_sh, _dp(lse),
-                              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                              _stream_of(q, stream))
-    if rc:
-        _check(lib, "attn_decode_step", rc)
-    return out, lse
+    return _outcome((_calls or attn_calls()).decode(q, k_cache, v_cache, page_table, lens, max_len, k_scale, v_scale, scale,
+                                                    out, out_dtype, lse, workspace, _raw(stream)), "attn_decode_step")

@@ -100,5 +100,57 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     return LIB
 
 
+# ------------------------------------------------------------------ the attention calls' marshalling
+CALLS_SRC = "attn_call.cpp"
+CALLS = BUILD / "_attn_call.so"
+CALLS_STAMP = BUILD / "_attn_call.sha256"
+
+
+def _calls_command(out: Path) -> list[str]:
+    """One g++ run against the torch and Python of this interpreter."""
+    import sysconfig
+
+    import torch
+
+    root = Path(torch.__file__).resolve().parent
+    cuda = Path(nvcc()).resolve().parents[1]
+    return [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+            "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", str(INCLUDE), "-I", sysconfig.get_paths()["include"], "-I", str(root / "include"),
+            "-I", str(root / "include/torch/csrc/api/include"), "-I", str(cuda / "include"),
+            str(CSRC / CALLS_SRC), "-o", str(out), "-L", str(root / "lib"), f"-Wl,-rpath,{root / 'lib'}",
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def build_calls(force: bool = False) -> Path:
+    """Compile the Python extension that marshals the attention calls; returns its path.
+
+    Reused only when its stamp holds the digest of its source, the ABI header, the command, and the
+    versions of Python and torch that it was compiled against."""
+    import sys
+
+    import torch
+
+    h = hashlib.sha256()
+    for p in (CSRC / CALLS_SRC, INCLUDE / "ssm.h"):
+        h.update(p.name.encode() + b"\0" + p.read_bytes() + b"\0")
+    h.update(" ".join(_calls_command(CALLS)).encode())
+    h.update(f"{sys.version} {torch.__version__}".encode())
+    digest = h.hexdigest()
+    if not force and CALLS.exists() and CALLS_STAMP.exists() and CALLS_STAMP.read_text().strip() == digest:
+        return CALLS
+    BUILD.mkdir(parents=True, exist_ok=True)
+    tmp = BUILD / f"_attn_call.{os.getpid()}.tmp"
+    r = subprocess.run(_calls_command(tmp), capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    stamp_tmp = BUILD / f"_attn_call.sha256.{os.getpid()}.tmp"
+    stamp_tmp.write_text(digest + "\n")
+    os.replace(stamp_tmp, CALLS_STAMP)
+    return CALLS
+
+
 if __name__ == "__main__":
     print(build(force=True, verbose=True))
+    print(build_calls(force=True))

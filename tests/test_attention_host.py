@@ -16,6 +16,7 @@ FAKE = 0x10000
 @pytest.fixture(scope="module")
 def lib():
     build.build()
+    build.build_calls()
     return binding.load()
 
 
@@ -113,7 +114,7 @@ def test_calls_without_tokens_do_nothing(lib):
     assert lib.attn_prefill(*dict(PREFILL, tq=0, q=None, out=None).values()) == 0
 
 
-def test_binding_checks_come_first():
+def test_binding_checks_come_first(lib):
     """CPU tensors, wrong shapes and types are refused by the binding itself."""
     bf = torch.bfloat16
     x = torch.zeros(4, 2, 64, dtype=bf)
