@@ -10,6 +10,8 @@
 //
 // All three are elementwise over rows: the bytes moved bound them (and launch latency, for a few
 // tokens).
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -76,46 +78,45 @@ struct Words<4> {
     }
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
+constexpr int kAppendAhead = 4;         // rows a lane group has in flight
+constexpr int kAppendBlocks = 7;        // on an SM
+
+// How a token's rows are shared out: a turn is 32 / LPR heads of one kind (q heads first, then k, then
+// v), a part is `turns` consecutive turns, taken by one warp.
+struct AppendShape {
+    int q_turns, kv_turns;              // turns of the q heads, of the k heads (and of the v heads)
+    int turns, parts;                   // of a part, of a token
+};
 
 // A row of up to EPL * LPR elements lies on LPR lanes, EPL consecutive ones each, in registers from
 // the load to the store; a pair's other element comes by a shuffle (half layout: from the lane half /
-// EPL away, so half must be a multiple of EPL) or lies beside it (interleaved).  grid.x: tokens;
-// grid.y: groups of rows_per_block of the token's n_q + 2 n_kv rows (q heads, then k heads, then v
-// heads).  The next row's load is in flight while a row is worked on.
+// EPL away, so half must be a multiple of EPL) or lies beside it (interleaved).  A warp reads a token's
+// slot, position, cosines and sines once and then only rows, several at a time in flight.
 template <bool I8, int EPL, int LPR>
-__global__ void __launch_bounds__(kAppendThreads)
-k_attn_append(const AttnAppendArgs a, int rows_per_block) {
-    constexpr int kRows = kAppendThreads / LPR, W = EPL / 2;
-    const int64_t t = blockIdx.x;
-    const int sub = threadIdx.x % LPR, e = EPL * sub;
+__global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
+k_attn_append(const AttnAppendArgs a, const AppendShape s) {
+    constexpr int W = EPL / 2, kHeads = 32 / LPR;
+    const int64_t id = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const int64_t t = id / s.parts;
+    if (t >= a.n_tokens) return;                     // whole warps leave: no barrier below
+    const int part = (int)(id - t * s.parts);
+    const int sub = threadIdx.x % LPR, e = EPL * sub, head0 = (threadIdx.x & 31) / LPR;
     const int D = a.c.dim, half = a.rot / 2, nkv = a.c.n_kv;
-    const int rows = a.n_q + 2 * nkv;
-    const int r_end = min(rows, ((int)blockIdx.y + 1) * rows_per_block);
-    int r = (int)blockIdx.y * rows_per_block + threadIdx.x / LPR;
-    const __nv_bfloat16* qp = reinterpret_cast<const __nv_bfloat16*>(a.q) + t * a.q_st + e;
-    const __nv_bfloat16* kp = reinterpret_cast<const __nv_bfloat16*>(a.k) + t * a.k_st + e;
-    const __nv_bfloat16* vp = reinterpret_cast<const __nv_bfloat16*>(a.v) + t * a.v_st + e;
     const bool mine = e < D;
-    auto load = [&](int r, uint32_t* w) {
-        const __nv_bfloat16* p = r < a.n_q ? qp + r * a.q_sh
-                                           : (r < a.n_q + nkv ? kp + (r - a.n_q) * a.k_sh : vp + (r - a.n_q - nkv) * a.v_sh);
-        if (mine && r < r_end) Words<W>::load(w, p);
-    };
-    uint32_t x[W] = {}, nx[W] = {};
     const int slot = a.slots[t];
-    const int pos = a.rot ? a.positions[t] : 0;
-    if (slot != -1) load(r, x);
     if (slot == -1) return;
+    const int pos = a.rot ? a.positions[t] : 0;
     if (slot < 0 || slot >= a.c.n_pages * a.c.page_size || (a.rot && (pos < 0 || pos >= a.n_pos))) {
-        if (threadIdx.x == 0) atomicOr(a.status, kBadIndex);
+        if ((threadIdx.x & 31) == 0) atomicOr(a.status, kBadIndex);
         return;
     }
-    // this lane's cosines and sines, the same for every head; half layout: one a element, interleaved: one a pair
+    const int begin = part * s.turns, end = begin + s.turns;
+    // this lane's cosines and sines, the same for every head; half layout: one an element, interleaved: one a pair
     const bool turned = e < a.rot;
     const bool first = e < half;                     // half layout: this lane holds the pairs' first elements
     float cs[EPL], sn[EPL];
-    if (turned) {
+    if (turned && begin < s.q_turns + s.kv_turns) {
         const float *cr = a.cos + (int64_t)pos * half, *sr = a.sin + (int64_t)pos * half;
         if (a.interleaved) {
 #pragma unroll
@@ -132,72 +133,91 @@ k_attn_append(const AttnAppendArgs a, int rows_per_block) {
     }
     const int other = turned ? (first ? sub + half / EPL : sub - half / EPL) : sub;
     const int64_t row0 = (int64_t)(slot / a.c.page_size) * nkv * a.c.page_size + slot % a.c.page_size;
-    __nv_bfloat16* qo = reinterpret_cast<__nv_bfloat16*>(a.q_out) + t * a.qo_st + e;
-    __nv_bfloat16* ko = reinterpret_cast<__nv_bfloat16*>(a.k_out) + t * a.ko_st + e;
 
-    // every lane of the block takes the same number of turns: the shuffles are the whole warp's
-    for (int r0 = (int)blockIdx.y * rows_per_block; r0 < r_end; r0 += kRows, r += kRows) {
-        load(r + kRows, nx);
-        const bool on = mine && r < r_end;
-        const int kind = r < a.n_q ? 0 : (r < a.n_q + nkv ? 1 : 2);         // q, k, v
-        const int h = kind == 0 ? r : (kind == 1 ? r - a.n_q : r - a.n_q - nkv);
-        float y[EPL];
+    // the heads of turns [lo, hi) of one kind: 0 q, 1 k, 2 v
+    auto run = [&](auto kind_of, const void* in, int64_t st, int64_t sh, int heads, int lo, int hi) {
+        constexpr int kind = decltype(kind_of)::value;
+        const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(in) + t * st + e;
+        for (int u0 = lo; u0 < hi; u0 += kAppendAhead) {
+            uint32_t x[kAppendAhead][W];
 #pragma unroll
-        for (int i = 0; i < W; ++i) y[2 * i] = lo_f32(x[i]), y[2 * i + 1] = hi_f32(x[i]);
-        if (a.rot) {                                  // the same branch for the whole block
-            if (a.interleaved) {
-                if (turned && kind < 2)
+            for (int u = 0; u < kAppendAhead; ++u) {
+                const int h = (u0 + u) * kHeads + head0;
 #pragma unroll
-                    for (int i = 0; i < W; ++i) {
-                        const float u = y[2 * i], v = y[2 * i + 1];
-                        y[2 * i] = rot_first(u, v, cs[i], sn[i]);
-                        y[2 * i + 1] = rot_second(u, v, cs[i], sn[i]);
+                for (int i = 0; i < W; ++i) x[u][i] = 0u;
+                if (mine && u0 + u < hi && h < heads) Words<W>::load(x[u], src + h * sh);
+            }
+#pragma unroll
+            for (int u = 0; u < kAppendAhead; ++u) {
+                if (u0 + u >= hi) break;             // the whole warp's: shuffles follow
+                const int h = (u0 + u) * kHeads + head0;
+                const bool on = mine && h < heads;
+                float y[EPL];
+#pragma unroll
+                for (int i = 0; i < W; ++i) y[2 * i] = lo_f32(x[u][i]), y[2 * i + 1] = hi_f32(x[u][i]);
+                if (kind < 2 && a.rot) {
+                    if (a.interleaved) {
+                        if (turned)
+#pragma unroll
+                            for (int i = 0; i < W; ++i) {
+                                const float p = y[2 * i], q = y[2 * i + 1];
+                                y[2 * i] = rot_first(p, q, cs[i], sn[i]);
+                                y[2 * i + 1] = rot_second(p, q, cs[i], sn[i]);
+                            }
+                    } else {
+                        uint32_t o[W];
+#pragma unroll
+                        for (int i = 0; i < W; ++i) o[i] = __shfl_sync(0xffffffffu, x[u][i], other, LPR);
+                        if (turned)
+#pragma unroll
+                            for (int i = 0; i < EPL; ++i) {
+                                const float z = i & 1 ? hi_f32(o[i / 2]) : lo_f32(o[i / 2]);
+                                y[i] = first ? rot_first(y[i], z, cs[i], sn[i]) : rot_second(z, y[i], cs[i], sn[i]);
+                            }
                     }
-            } else {
-                uint32_t o[W];
+                }
+                uint32_t out[W];
+                if (kind < 2 || !I8) {
 #pragma unroll
-                for (int i = 0; i < W; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], other, LPR);
-                if (turned && kind < 2)
+                    for (int i = 0; i < W; ++i) out[i] = pack2(y[2 * i], y[2 * i + 1]);
+                }
+                if (kind == 0 && on)
+                    Words<W>::store(reinterpret_cast<__nv_bfloat16*>(a.q_out) + t * a.qo_st + h * a.qo_sh + e, out);
+                if (kind == 1 && on && a.k_out)
+                    Words<W>::store(reinterpret_cast<__nv_bfloat16*>(a.k_out) + t * a.ko_st + h * a.ko_sh + e, out);
+                if constexpr (kind > 0) {
+                    const int64_t row = row0 + (int64_t)h * a.c.page_size;
+                    void* cache = const_cast<void*>(kind == 1 ? a.c.k : a.c.v);
+                    if constexpr (I8) {
+                        // fmaxf passes over a NaN; the leading zero stands for a row of nothing else
+                        float m = 0.f;
 #pragma unroll
-                    for (int i = 0; i < EPL; ++i) {
-                        const float z = i & 1 ? hi_f32(o[i / 2]) : lo_f32(o[i / 2]);
-                        y[i] = first ? rot_first(y[i], z, cs[i], sn[i]) : rot_second(z, y[i], cs[i], sn[i]);
+                        for (int i = 0; i < EPL; ++i) m = fmaxf(m, fabsf(y[i]));
+#pragma unroll
+                        for (int d = LPR / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                        if (on) {
+                            const float inv = m > 0.f ? __fdiv_rn(127.f, m) : 0.f;
+                            uint32_t codes[EPL / 4];
+#pragma unroll
+                            for (int i = 0; i < EPL / 4; ++i)
+                                codes[i] = code8(y[4 * i], inv) | code8(y[4 * i + 1], inv) << 8 |
+                                           code8(y[4 * i + 2], inv) << 16 | code8(y[4 * i + 3], inv) << 24;
+                            int8_t* p = reinterpret_cast<int8_t*>(cache) + row * D + e;
+                            if constexpr (EPL == 8) *reinterpret_cast<uint2*>(p) = make_uint2(codes[0], codes[1]);
+                            else *reinterpret_cast<uint32_t*>(p) = codes[0];
+                            if (sub == 0) const_cast<float*>(kind == 1 ? a.c.k_scale : a.c.v_scale)[row] = __fdiv_rn(m, 127.f);
+                        }
+                    } else {
+                        if (on) Words<W>::store(reinterpret_cast<__nv_bfloat16*>(cache) + row * D + e, out);
                     }
+                }
             }
         }
-        uint32_t out[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) out[i] = pack2(y[2 * i], y[2 * i + 1]);
-        if (on && kind == 0) Words<W>::store(qo + h * a.qo_sh, out);
-        if (on && kind == 1 && a.k_out) Words<W>::store(ko + h * a.ko_sh, out);
-        const int64_t row = row0 + (int64_t)h * a.c.page_size;
-        if constexpr (I8) {
-            // fmaxf passes over a NaN; the leading zero stands for a row of nothing else
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) m = fmaxf(m, fabsf(y[i]));
-            if (!on) m = 0.f;
-#pragma unroll
-            for (int d = LPR / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            if (on && kind > 0) {
-                const float inv = m > 0.f ? __fdiv_rn(127.f, m) : 0.f;
-                uint32_t codes[EPL / 4];
-#pragma unroll
-                for (int i = 0; i < EPL / 4; ++i)
-                    codes[i] = code8(y[4 * i], inv) | code8(y[4 * i + 1], inv) << 8 | code8(y[4 * i + 2], inv) << 16 |
-                               code8(y[4 * i + 3], inv) << 24;
-                int8_t* p = reinterpret_cast<int8_t*>(const_cast<void*>(kind == 1 ? a.c.k : a.c.v)) + row * D + e;
-                if constexpr (EPL == 8) *reinterpret_cast<uint2*>(p) = make_uint2(codes[0], codes[1]);
-                else *reinterpret_cast<uint32_t*>(p) = codes[0];
-                if (sub == 0) const_cast<float*>(kind == 1 ? a.c.k_scale : a.c.v_scale)[row] = __fdiv_rn(m, 127.f);
-            }
-        } else {
-            if (on && kind > 0)
-                Words<W>::store(reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(kind == 1 ? a.c.k : a.c.v)) + row * D + e, out);
-        }
-#pragma unroll
-        for (int i = 0; i < W; ++i) x[i] = nx[i];
-    }
+    };
+    const int k0 = s.q_turns, v0 = k0 + s.kv_turns;
+    run(std::integral_constant<int, 0>(), a.q, a.q_st, a.q_sh, a.n_q, begin, min(end, s.q_turns));
+    run(std::integral_constant<int, 1>(), a.k, a.k_st, a.k_sh, nkv, max(begin, k0) - k0, min(end, v0) - k0);
+    run(std::integral_constant<int, 2>(), a.v, a.v_st, a.v_sh, nkv, max(begin, v0) - v0, min(end - v0, s.kv_turns));
 }
 
 // ------------------------------------------------------------------ read
@@ -329,12 +349,20 @@ int launch_attn_rope_table(const AttnRopeArgs& a, cudaStream_t stream, const cha
 
 template <bool I8, int EPL, int LPR>
 static void append(const AttnAppendArgs& a, cudaStream_t stream) {
-    const int rows = a.n_q + 2 * a.c.n_kv, per_pass = kAppendThreads / LPR;
-    // few tokens: a row per lane group, so that the rows run side by side; many: a block per token, which
-    // reads the token's slot, position, cosines and sines once
-    const int rows_per_block = a.n_tokens < 1024 ? per_pass : (rows + per_pass - 1) / per_pass * per_pass;
-    const dim3 grid((unsigned)a.n_tokens, (unsigned)((rows + rows_per_block - 1) / rows_per_block));
-    k_attn_append<I8, EPL, LPR><<<grid, kAppendThreads, 0, stream>>>(a, rows_per_block);
+    constexpr int kHeads = 32 / LPR;
+    AppendShape s;
+    s.q_turns = (a.n_q + kHeads - 1) / kHeads;
+    s.kv_turns = (a.c.n_kv + kHeads - 1) / kHeads;
+    const int total = s.q_turns + 2 * s.kv_turns;
+    // few tokens: a token's rows spread over so many warps that some 4864 (152 SMs x 32) run side by side;
+    // many: a token a warp
+    const int64_t want = (4864 + a.n_tokens - 1) / a.n_tokens;
+    s.parts = (int)(want < 1 ? 1 : (want > total ? total : want));
+    s.turns = (total + s.parts - 1) / s.parts;
+    s.parts = (total + s.turns - 1) / s.turns;
+    const int64_t warps = a.n_tokens * s.parts;
+    constexpr int kPer = kAppendThreads / 32;
+    k_attn_append<I8, EPL, LPR><<<(unsigned)((warps + kPer - 1) / kPer), kAppendThreads, 0, stream>>>(a, s);
 }
 
 template <bool I8>
