@@ -201,6 +201,9 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_init(&kv_empty[s], 1);
         }
         fence_barrier_init();
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
     }
     for (int i = threadIdx.x; i < 3 * DP; i += kThreads) bad[i] = 0x7fffffff;
     if (warp == 9) tmem_alloc(tmem_slot, 512);
@@ -224,6 +227,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const uint32_t ts = tmem + lanes + (uint32_t)(128 * t), to = tmem + lanes + 256u + (uint32_t)(128 * t);
         const float c = a.scale * kLog2e;
+        // from this block on a row of this tile does not see all of it
+        const int whole_t = min(lk, row0 + t * kM + off + 1), mask_t = whole_t <= 0 ? 0 : whole_t / kN;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int j = 0; j < n; ++j) {
@@ -239,7 +244,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tmem_wait_ld();
 #pragma unroll
             for (int q = 0; q < 4; ++q) pin32(r + 32 * q);
-            if (j >= mask_from) {
+            if (j >= mask_t) {
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
                     if (j * kN + i >= see) r[i] = 0xff800000u;          // -inf
@@ -467,30 +472,55 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
                 unsigned char* v = smem + G::kOffKV + (vi % G::kSlots) * G::kTile;
                 const int rows = lk - j * kN;                // of this sequence; later ones are zeroed
-                for (int i = threadIdx.x - 320; i < G::kTile / 16; i += 64) {
-                    const int r = (i >> 3) & 127;
-                    uint4* p = reinterpret_cast<uint4*>(v) + i;
-                    if (r >= rows) {
-                        *p = make_uint4(0u, 0u, 0u, 0u);
-                        continue;
-                    }
-                    const uint4 w = *p;
-                    uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-                    bool fine = true;
+                // rows before `seen` are seen by every row of both tiles and stay as they are; eight chunks of
+                // 16 bytes are looked at together, as nearly all are fine
+                const int seen = max(whole - j * kN, 0);
+                constexpr int kAhead = 8;
+                for (int i0 = threadIdx.x - 320; i0 < G::kTile / 16; i0 += 64 * kAhead) {
+                    uint4 x[kAhead];
+                    __nv_bfloat162 z = __float2bfloat162_rn(0.f);
+                    bool past = false;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        fine = fine && (ws[e] & 0x7f80u) != 0x7f80u && (ws[e] & 0x7f800000u) != 0x7f800000u;
-                    if (fine) continue;
-                    const int col = (i >> 10) * 64 + ((i & 7) ^ (r & 7)) * 8;       // the swizzle undone
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t x = (ws[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-                        if ((x & 0x7f80u) != 0x7f80u) continue;
-                        const int kind = x == 0x7f80u ? 0 : (x == 0xff80u ? 1 : 2);
-                        atomicMin(&bad[kind * DP + col + e], j * kN + r);
-                        ws[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                    for (int u = 0; u < kAhead; ++u) {
+                        const int i = i0 + 64 * u, r = (i >> 3) & 127;
+                        x[u] = make_uint4(0u, 0u, 0u, 0u);
+                        if (r >= seen && r < rows) x[u] = reinterpret_cast<const uint4*>(v)[i];
+                        past = past || r >= rows;
                     }
-                    *p = make_uint4(ws[0], ws[1], ws[2], ws[3]);
-                    s_bad = 1;
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) {
+                        const uint32_t ws[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)      // x 0: a NaN for an infinity or a NaN, a zero otherwise
+                            z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&ws[e]), __float2bfloat162_rn(0.f), z);
+                    }
+                    if ((*reinterpret_cast<const uint32_t*>(&z) & 0x7fff7fffu) == 0u && !past) continue;
+                    for (int u = 0; u < kAhead; ++u) {
+                        const int i = i0 + 64 * u, r = (i >> 3) & 127;
+                        uint4* p = reinterpret_cast<uint4*>(v) + i;
+                        if (r >= rows) {
+                            *p = make_uint4(0u, 0u, 0u, 0u);
+                            continue;
+                        }
+                        if (r < seen) continue;
+                        const uint4 y = *p;
+                        uint32_t ws[4] = {y.x, y.y, y.z, y.w};
+                        bool fine = true;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            fine = fine && (ws[e] & 0x7f80u) != 0x7f80u && (ws[e] & 0x7f800000u) != 0x7f800000u;
+                        if (fine) continue;
+                        const int col = (i >> 10) * 64 + ((i & 7) ^ (r & 7)) * 8;       // the swizzle undone
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t b16 = (ws[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                            if ((b16 & 0x7f80u) != 0x7f80u) continue;
+                            const int kind = b16 == 0x7f80u ? 0 : (b16 == 0xff80u ? 1 : 2);
+                            atomicMin(&bad[kind * DP + col + e], j * kN + r);
+                            ws[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
+                        }
+                        *p = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+                        s_bad = 1;
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
