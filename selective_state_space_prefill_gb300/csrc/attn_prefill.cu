@@ -8,7 +8,7 @@
 // out = o / l, lse = ln 2 (c m + log2 l).  Any m gives the same quotient; it is raised to the
 // running maximum only when that has grown by more than 2^8 (kSlack, in units of c s), so that p
 // stays below 2^8 and o is seldom rescaled.  p is rounded to bf16 for the second product, as the
-// tensor cores take it with bf16 values; l sums it unrounded.
+// tensor cores take it with bf16 values; l sums it unrounded.  For few rows p is a bf16 pair.
 //
 // Two dense products per block bound it: 2 x 128 x 128 x D multiply-adds on the tensor cores and
 // 128 x 128 exponentials.  The design keeps the tensor cores fed while the exponentials run:
@@ -141,7 +141,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-template <int DP, typename Tout>
+// kPair: the weights as bf16 pairs hi + lo, both multiplied with the values.
+template <int DP, bool kPair, typename Tout>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const AttnPrefillArgs a) {
@@ -292,7 +293,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                uint32_t p[32];
+                uint32_t p[32], p_lo[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     float x0, x1;
@@ -302,8 +303,11 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     x1 = ex2(x1);
                     sum[i & 3] = add2(sum[i & 3], pair(x0, x1));
                     p[i] = pack_bf16(x0, x1);
+                    if constexpr (kPair)
+                        p_lo[i] = pack_bf16(x0 - __uint_as_float(p[i] << 16), x1 - __uint_as_float(p[i] & 0xffff0000u));
                 }
                 tmem_st32(ts + 32u * q, p);
+                if constexpr (kPair) tmem_st32(ts + 64u + 32u * q, p_lo);
             }
             float l0, l1;
             unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l0, l1);
@@ -428,6 +432,12 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     for (int s = 0; s < kN / 16; ++s)        // 16 keys: 8 columns of P, 2048 bytes of V
                         mma_bf16_ts(tm + (uint32_t)(256 + 128 * t), tm + (uint32_t)(128 * t + 8 * s),
                                     v + (uint64_t)(s * (2048 >> 4)), G::kIdescO, s != 0 || !first);
+                    if constexpr (kPair) {
+#pragma unroll
+                        for (int s = 0; s < kN / 16; ++s)    // the low parts, 64 columns on
+                            mma_bf16_ts(tm + (uint32_t)(256 + 128 * t), tm + (uint32_t)(128 * t + 64 + 8 * s),
+                                        v + (uint64_t)(s * (2048 >> 4)), G::kIdescO, 1);
+                    }
                     mma_commit(&o_full[t]);
                 }
                 __syncwarp();
@@ -550,7 +560,7 @@ bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int d
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DP, typename Tout>
+template <int DP, bool kPair, typename Tout>
 int launch_dp(const AttnPrefillArgs& a, cudaStream_t stream, const char** why) {
     CUtensorMap mq, mk, mv;
     // without keys nothing is loaded; the maps then stand over q
@@ -563,7 +573,7 @@ int launch_dp(const AttnPrefillArgs& a, cudaStream_t stream, const char** why) {
         *why = "cuTensorMapEncodeTiled failed (driver entry point missing or layout rejected)";
         return -1;
     }
-    auto kern = k_attn_prefill<DP, Tout>;
+    auto kern = k_attn_prefill<DP, kPair, Tout>;
     static ContextMemo attr;
     if (!opt_in_dynamic_smem(attr, kern, Geo<DP>::kSmem, why)) return -1;
     const int64_t tiles = ((int64_t)a.max_q + 2 * kM - 1) / (2 * kM);
@@ -579,12 +589,19 @@ int launch_dp(const AttnPrefillArgs& a, cudaStream_t stream, const char** why) {
     return -1;
 }
 
+template <typename Tout>
+int launch_shape(const AttnPrefillArgs& a, cudaStream_t stream, const char** why) {
+    // Few rows (a short chunk, some tokens to verify) take microseconds of latency whatever the weights
+    // are: there they keep 16 bits.  On whole prompts the second product would cost a third of the time.
+    const bool pair = a.total_q * a.n_q <= 256;
+    if (a.dim <= 64) return pair ? launch_dp<64, true, Tout>(a, stream, why) : launch_dp<64, false, Tout>(a, stream, why);
+    return pair ? launch_dp<128, true, Tout>(a, stream, why) : launch_dp<128, false, Tout>(a, stream, why);
+}
+
 }  // namespace
 
 int launch_attn_prefill(const AttnPrefillArgs& a, bool out_bf16, cudaStream_t stream, const char** why) {
-    if (a.dim <= 64)
-        return out_bf16 ? launch_dp<64, __nv_bfloat16>(a, stream, why) : launch_dp<64, float>(a, stream, why);
-    return out_bf16 ? launch_dp<128, __nv_bfloat16>(a, stream, why) : launch_dp<128, float>(a, stream, why);
+    return out_bf16 ? launch_shape<__nv_bfloat16>(a, stream, why) : launch_shape<float>(a, stream, why);
 }
 
 }  // namespace ssm
