@@ -25,6 +25,7 @@
 //     that holds +inf, -inf, NaN), and the rows that do see them get them back at the end.
 // TMEM: scores of tile t at column 128 t, output at 256 + 128 t; all 512 columns, one CTA per SM.
 // The grid runs the longest rows first (the last tiles of every head and sequence), so the tail is short.
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -34,6 +35,8 @@
 
 namespace ssm {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kM = 128;                 // query rows per tile
 constexpr int kN = 128;                 // keys per block
@@ -51,7 +54,10 @@ struct Geo {
     static constexpr int kTile = 128 * DP * 2;                  // bytes of 128 rows
     static constexpr int kSlots = DP == 128 ? 4 : 8;            // ring of key and value blocks
     static constexpr int kOffKV = 2 * kTile;
+    // a split item's part, over the operands: [256][DP + 4] outputs, then [256] (maximum, sum)
+    static constexpr int kOffSums = 256 * (DP + 4) * 4;
     static constexpr int kOffBar = kOffKV + kSlots * kTile;
+    static_assert(kOffSums + 256 * 8 <= kOffKV + kSlots * kTile, "a part fits over the operands");
     // q_full[2], s_full[2], p_full[2], o_full[2], v_raw[4], v_ok[4], kv_full[slots], kv_empty[slots],
     // TMEM address
     static constexpr int kBars = 16 + 2 * kSlots;
@@ -142,22 +148,27 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 // kPair: the weights as bf16 pairs hi + lo, both multiplied with the values.
-template <int DP, bool kPair, typename Tout>
+// kSplit: the CTAs of a cluster share the key blocks of an item and join their outputs through
+// distributed shared memory.
+template <int DP, bool kPair, bool kSplit, typename Tout>
 __global__ void __launch_bounds__(kThreads, 1)
 k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const AttnPrefillArgs a) {
     using G = Geo<DP>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ int s_err, s_bad;
-    const int h = (int)(blockIdx.x % (unsigned)a.n_q), b = (int)(blockIdx.x / (unsigned)a.n_q % (unsigned)a.batch);
-    const int row0 = (int)((gridDim.x - 1 - blockIdx.x) / ((unsigned)a.n_q * (unsigned)a.batch)) * 2 * kM;
+    const unsigned splits = kSplit ? cg::this_cluster().num_blocks() : 1u, rank = kSplit ? cg::this_cluster().block_rank() : 0u;
+    const unsigned item = blockIdx.x / splits, items = gridDim.x / splits;
+    const int h = (int)(item % (unsigned)a.n_q), b = (int)(item / (unsigned)a.n_q % (unsigned)a.batch);
+    const int row0 = (int)((items - 1 - item) / ((unsigned)a.n_q * (unsigned)a.batch)) * 2 * kM;
     // the sequence's rows, kept inside the tensors whatever cu_q and cu_k hold
-    const int q0 = min(max(a.cu_q[b], 0), (int)a.total_q), k0 = min(max(a.cu_k[b], 0), (int)a.total_k);
+    const int q0 = min(max(a.cu_q[b], 0), (int)a.total_q);
+    int k0 = min(max(a.cu_k[b], 0), (int)a.total_k);
     const int lq = min(min(a.cu_q[b + 1], (int)a.total_q) - q0, a.max_q);
     const int lq_all = min(a.cu_q[b + 1], (int)a.total_q) - q0;
-    const int lk = max(min(a.cu_k[b + 1], (int)a.total_k) - k0, 0);
-    if (row0 >= lq) return;                              // the same for the whole block
-    const int off = lk - lq_all;                         // row i sees keys < min(lk, i + off + 1)
+    int lk = max(min(a.cu_k[b + 1], (int)a.total_k) - k0, 0);
+    if (row0 >= lq) return;                              // the same for the whole block, and cluster
+    int off = lk - lq_all;                         // row i sees keys < min(lk, i + off + 1)
     // blocks of keys that tile t's rows see
     auto blocks = [&](int t) -> int {
         const int r = row0 + t * kM;
@@ -165,6 +176,12 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int see = min(lk, min(lq - 1, r + kM - 1) + off + 1);
         return see <= 0 ? 0 : (see + kN - 1) / kN;
     };
+    if constexpr (kSplit) {                              // this CTA's share: as if the keys began and ended there
+        const int all = max(blocks(0), blocks(1)), from = (int)((int64_t)all * rank / splits) * kN;
+        lk = min(lk, (int)((int64_t)all * (rank + 1) / splits) * kN) - from;
+        k0 += from;
+        off -= from;
+    }
     const int n0 = blocks(0), n1 = blocks(1), nb = max(n0, n1);
     // the first block that some row of the CTA's tiles does not wholly see; as 256 neighbouring rows'
     // limits span at most 255 keys, at most three blocks are left from it on
@@ -322,13 +339,9 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             ok = false;
         }
         tc_fence_after();
-        const bool store = ok && s_err == 0 && row < lq;
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        if (store && a.lse) a.lse[(int64_t)(q0 + row) * a.n_q + h] = l == 0.f ? -INFINITY : kLn2 * (m * c + log2f(l));
-        Tout* out = reinterpret_cast<Tout*>(a.out) + (int64_t)(q0 + row) * a.o_st + (int64_t)h * a.o_sh;
         const bool any_bad = *(volatile int*)&s_bad != 0;
-#pragma unroll 1
-        for (int q = 0; q < DP / 32; ++q) {
+        // 32 columns of this row's output, not yet divided, with the non-finite values that it sees
+        auto columns = [&](int q, float (&v)[32]) {
             uint32_t o[32];
             __syncwarp();
             if (n > 0) {
@@ -336,9 +349,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tmem_wait_ld();
                 pin32(o);
             }
-            float v[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = l == 0.f ? 0.f : __uint_as_float(o[i]) * inv;
+            for (int i = 0; i < 32; ++i) v[i] = l == 0.f ? 0.f : __uint_as_float(o[i]);
             if (any_bad) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
@@ -348,18 +360,45 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (bad[2 * DP + col] < see) v[i] = NAN;
                 }
             }
+        };
+        if constexpr (kSplit) {
+            // both tiles' products are done: the operands' shared memory becomes this CTA's part
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            const int r = t * kM + 32 * quarter + lane;
+            float* part = reinterpret_cast<float*>(smem) + r * (DP + 4);
+#pragma unroll 1
+            for (int q = 0; q < DP / 32; ++q) {
+                float v[32];
+                columns(q, v);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {                // eight columns at a time, whole or not at all
-                if (!store || 32 * q + 8 * g >= a.dim) continue;
-                if constexpr (sizeof(Tout) == 2) {
-                    *reinterpret_cast<uint4*>(out + 32 * q + 8 * g) =
-                        make_uint4(pack_bf16(v[8 * g], v[8 * g + 1]), pack_bf16(v[8 * g + 2], v[8 * g + 3]),
-                                   pack_bf16(v[8 * g + 4], v[8 * g + 5]), pack_bf16(v[8 * g + 6], v[8 * g + 7]));
-                } else {
-                    reinterpret_cast<float4*>(out + 32 * q + 8 * g)[0] =
-                        make_float4(v[8 * g], v[8 * g + 1], v[8 * g + 2], v[8 * g + 3]);
-                    reinterpret_cast<float4*>(out + 32 * q + 8 * g)[1] =
-                        make_float4(v[8 * g + 4], v[8 * g + 5], v[8 * g + 6], v[8 * g + 7]);
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<float4*>(part + 32 * q + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+            reinterpret_cast<float2*>(smem + G::kOffSums)[r] = make_float2(l == 0.f ? -INFINITY : m * c, l);
+        } else {
+            const bool store = ok && s_err == 0 && row < lq;
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            if (store && a.lse) a.lse[(int64_t)(q0 + row) * a.n_q + h] = l == 0.f ? -INFINITY : kLn2 * (m * c + log2f(l));
+            Tout* out = reinterpret_cast<Tout*>(a.out) + (int64_t)(q0 + row) * a.o_st + (int64_t)h * a.o_sh;
+#pragma unroll 1
+            for (int q = 0; q < DP / 32; ++q) {
+                float v[32];
+                columns(q, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= inv;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {                // eight columns at a time, whole or not at all
+                    if (!store || 32 * q + 8 * g >= a.dim) continue;
+                    if constexpr (sizeof(Tout) == 2) {
+                        *reinterpret_cast<uint4*>(out + 32 * q + 8 * g) =
+                            make_uint4(pack_bf16(v[8 * g], v[8 * g + 1]), pack_bf16(v[8 * g + 2], v[8 * g + 3]),
+                                       pack_bf16(v[8 * g + 4], v[8 * g + 5]), pack_bf16(v[8 * g + 6], v[8 * g + 7]));
+                    } else {
+                        reinterpret_cast<float4*>(out + 32 * q + 8 * g)[0] =
+                            make_float4(v[8 * g], v[8 * g + 1], v[8 * g + 2], v[8 * g + 3]);
+                        reinterpret_cast<float4*>(out + 32 * q + 8 * g)[1] =
+                            make_float4(v[8 * g + 4], v[8 * g + 5], v[8 * g + 6], v[8 * g + 7]);
+                    }
                 }
             }
         }
@@ -544,6 +583,41 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if constexpr (kSplit) {
+        // out = sum_p o_p 2^(m_p - m) / sum_p l_p 2^(m_p - m) over the cluster's parts; a warp per row, every
+        // splits-th row of the item
+        auto cluster = cg::this_cluster();
+        cluster.sync();
+        for (int r = (int)rank + (int)splits * warp; r < 2 * kM && row0 + r < lq; r += (int)splits * (kThreads / 32)) {
+            float M = -INFINITY, L = 0.f;
+            for (unsigned p = 0; p < splits; ++p)
+                M = fmaxf(M, cluster.map_shared_rank(reinterpret_cast<float2*>(smem + G::kOffSums), p)[r].x);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (unsigned p = 0; p < splits; ++p) {
+                const float2 ml = cluster.map_shared_rank(reinterpret_cast<float2*>(smem + G::kOffSums), p)[r];
+                if (ml.y == 0.f) continue;               // it holds no key that this row sees
+                const float f = ex2(ml.x - M);
+                L += ml.y * f;
+                if (4 * lane < DP) {
+                    const float4 v = *reinterpret_cast<const float4*>(
+                        cluster.map_shared_rank(reinterpret_cast<float*>(smem), p) + r * (DP + 4) + 4 * lane);
+                    acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+                }
+            }
+            if (s_err) continue;
+            const int64_t token = (int64_t)q0 + row0 + r;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            if (lane == 0 && a.lse) a.lse[token * a.n_q + h] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
+            if (4 * lane < a.dim) {
+                Tout* out = reinterpret_cast<Tout*>(a.out) + token * a.o_st + (int64_t)h * a.o_sh + 4 * lane;
+                if constexpr (sizeof(Tout) == 2)
+                    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+                else
+                    *reinterpret_cast<float4*>(out) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            }
+        }
+        cluster.sync();                                  // no CTA leaves while its part is read
+    }
 }
 
 // Map over [tokens][heads][dim] bf16 with the given strides: boxes of 128 tokens x one head x 64
@@ -560,8 +634,11 @@ bool make_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int d
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DP, bool kPair, typename Tout>
-int launch_dp(const AttnPrefillArgs& a, cudaStream_t stream, const char** why) {
+// Pairs of query tiles over all sequences.
+int64_t tile_pairs(const AttnPrefillArgs& a) { return ((int64_t)a.max_q + 2 * kM - 1) / (2 * kM) * a.batch; }
+
+template <int DP, bool kPair, bool kSplit, typename Tout>
+int launch_dp(const AttnPrefillArgs& a, unsigned splits, cudaStream_t stream, const char** why) {
     CUtensorMap mq, mk, mv;
     // without keys nothing is loaded; the maps then stand over q
     const bool keys = a.total_k > 0;
@@ -573,35 +650,58 @@ int launch_dp(const AttnPrefillArgs& a, cudaStream_t stream, const char** why) {
         *why = "cuTensorMapEncodeTiled failed (driver entry point missing or layout rejected)";
         return -1;
     }
-    auto kern = k_attn_prefill<DP, kPair, Tout>;
+    auto kern = k_attn_prefill<DP, kPair, kSplit, Tout>;
     static ContextMemo attr;
     if (!opt_in_dynamic_smem(attr, kern, Geo<DP>::kSmem, why)) return -1;
-    const int64_t tiles = ((int64_t)a.max_q + 2 * kM - 1) / (2 * kM);
-    if (tiles * a.n_q * a.batch >= (1LL << 31)) {
-        *why = "sequences times heads times query tiles pass the grid";
-        return -1;
-    }
-    const dim3 grid((unsigned)(tiles * a.n_q * a.batch));
-    kern<<<grid, kThreads, Geo<DP>::kSmem, stream>>>(mq, mk, mv, a);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tile_pairs(a) * a.n_q * splits));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Geo<DP>::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute cluster[1];
+    cluster[0].id = cudaLaunchAttributeClusterDimension;
+    cluster[0].val.clusterDim.x = splits;
+    cluster[0].val.clusterDim.y = cluster[0].val.clusterDim.z = 1;
+    cfg.attrs = cluster;
+    cfg.numAttrs = kSplit ? 1 : 0;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e == cudaSuccess) return 0;
     *why = cudaGetErrorString(e);
     return -1;
 }
 
-template <typename Tout>
+template <int DP, typename Tout>
 int launch_shape(const AttnPrefillArgs& a, cudaStream_t stream, const char** why) {
+    int dev = 0, n_sm = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n_sm < 1) {
+        *why = "cudaGetDevice / multiprocessor count failed";
+        return -1;
+    }
+    if (tile_pairs(a) * a.n_q * 8 >= (1LL << 31)) {
+        *why = "sequences times heads times query tiles pass the grid";
+        return -1;
+    }
+    // Where the items leave half of the SMs or more without work and have 2048 keys or more on average, up
+    // to eight CTAs share the keys of one, 512 or more each: 8 rows of 32 heads over 4008 keys 66 -> 27 us,
+    // 1024 rows of 16 heads over 9024 keys 115 -> 76; with 1024 keys the join's 6 us are not won back (19 -> 25).
+    const int64_t items = tile_pairs(a) * a.n_q, keys = a.total_k / a.batch;
+    unsigned splits = 1;
+    while (splits < 8 && 2 * splits * items <= n_sm && keys >= 2048 && keys >= 2 * splits * 512) splits *= 2;
     // Few rows (a short chunk, some tokens to verify) take microseconds of latency whatever the weights
     // are: there they keep 16 bits.  On whole prompts the second product would cost a third of the time.
-    const bool pair = a.total_q * a.n_q <= 256;
-    if (a.dim <= 64) return pair ? launch_dp<64, true, Tout>(a, stream, why) : launch_dp<64, false, Tout>(a, stream, why);
-    return pair ? launch_dp<128, true, Tout>(a, stream, why) : launch_dp<128, false, Tout>(a, stream, why);
+    if (a.total_q * a.n_q <= 256) return launch_dp<DP, true, true, Tout>(a, splits, stream, why);
+    if (splits > 1) return launch_dp<DP, false, true, Tout>(a, splits, stream, why);
+    return launch_dp<DP, false, false, Tout>(a, 1, stream, why);
 }
 
 }  // namespace
 
 int launch_attn_prefill(const AttnPrefillArgs& a, bool out_bf16, cudaStream_t stream, const char** why) {
-    return out_bf16 ? launch_shape<__nv_bfloat16>(a, stream, why) : launch_shape<float>(a, stream, why);
+    if (a.dim <= 64)
+        return out_bf16 ? launch_shape<64, __nv_bfloat16>(a, stream, why) : launch_shape<64, float>(a, stream, why);
+    return out_bf16 ? launch_shape<128, __nv_bfloat16>(a, stream, why) : launch_shape<128, float>(a, stream, why);
 }
 
 }  // namespace ssm

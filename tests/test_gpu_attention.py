@@ -80,7 +80,7 @@ def test_prefill_layouts(D):
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-@pytest.mark.parametrize("D,n", [(64, 300), (128, 300), (128, 90)])
+@pytest.mark.parametrize("D,n", [(64, 300), (128, 300), (128, 90), (128, 1500)])
 def test_prefill_unseen_values_do_not_leak(D, n, bad):
     """Non-finite keys and values at a token reach only the rows that see it; the neighbours in the
     packing are untouched."""
@@ -106,6 +106,22 @@ def test_prefill_unseen_values_do_not_leak(D, n, bad):
     k2[at], v2[at] = bad, bad
     out, _ = ssm.attn_prefill(q.to(DEV), k2.to(DEV), v2.to(DEV), c, c, n, out_dtype=torch.float32)
     assert torch.equal(out[~sees.to(DEV)], clean[~sees.to(DEV)])
+
+
+@pytest.mark.parametrize("ql,kl,H,Hk,D", [
+    ([1], [5000], 8, 2, 128), ([8, 3, 1], [2200, 0, 999], 4, 1, 64), ([257, 300], [2000, 1700], 3, 3, 80),
+    ([700], [900], 2, 1, 128), ([40], [3001], 12, 4, 64), ([1, 0, 2], [1, 4000, 130], 5, 5, 96),
+])
+def test_prefill_few_rows_over_many_keys(ql, kl, H, Hk, D):
+    """Items too few for the GPU: their keys are shared out between the CTAs of a cluster."""
+    g = torch.Generator().manual_seed(sum(kl) + H)
+    q = heads(g, sum(ql), H, D, 1.5)
+    k, v = heads(g, sum(kl), Hk, D), heads(g, sum(kl), Hk, D)
+    for out_dtype in (torch.bfloat16, torch.float32):
+        out, lse = ssm.attn_prefill(q.to(DEV), k.to(DEV), v.to(DEV), cu(ql).to(DEV), cu(kl).to(DEV), max(ql),
+                                    out_dtype=out_dtype, lse=True)
+        check_attention(out, lse, _prefill_ref(q, k, v, ql, kl, D ** -0.5), D, out_dtype, W_PREFILL, f"{ql} {kl}")
+    assert ssm.device_status() == 0
 
 
 def test_prefill_max_q_and_empty_calls():
