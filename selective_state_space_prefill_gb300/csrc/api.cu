@@ -938,6 +938,11 @@ int attn_prefill(int batch, int64_t total_q, int64_t total_k, int max_q, int n_q
     if (!(scale > 0.0f) || !(scale - scale == 0.0f)) return fail(SSM_ERR_INVALID_ARG, "%s: scale must be finite and > 0", fn);
     if (!cu_q || !cu_k) return fail(SSM_ERR_INVALID_ARG, "%s: cu_q or cu_k is NULL", fn);
     if (total_q == 0 || max_q == 0) return SSM_OK;
+    // the grid counts (256 query rows, sequence, head) items, up to eight CTAs each, in 31 bits
+    const int64_t rows = max_q < total_q ? max_q : total_q;
+    if ((rows + 255) / 256 * batch >= (1LL << 31) / 8 / n_q_heads)
+        return fail(SSM_ERR_UNSUPPORTED, "%s: %d sequences of up to %lld rows and %d heads pass the grid", fn, batch,
+                    (long long)rows, n_q_heads);
     if ((rc = check_view(fn, "q", q, q_stride_t, q_stride_h, head_dim)) != SSM_OK) return rc;
     if (total_k > 0) {
         if ((rc = check_view(fn, "k", k, k_stride_t, k_stride_h, head_dim)) != SSM_OK) return rc;

@@ -100,9 +100,16 @@ at::ScalarType scalar_type(PyObject* o) {
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType s, const at::Tensor& like) {
     return at::empty(shape, like.options().dtype(s).memory_format(c10::nullopt).requires_grad(false));
 }
+// The caller's stream, or torch's current one on t's device.
 void* stream_of(PyObject* o, const at::Tensor& t) {
     if (given(o)) return reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(o)));
     return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
+}
+// Memory made here belongs to the current stream; a caller's other stream is noted as its user, so that
+// it is not handed out again while the call still runs there.
+void used_on(PyObject* o, void* stream, const at::Tensor& t) {
+    if (given(o) && t.defined() && t.numel() > 0)
+        t.record_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), t.get_device()).unwrap());
 }
 
 struct Cache {
@@ -238,10 +245,12 @@ PyObject* do_append(PyObject* const* a) {
         ko = view(k_out, "k_out");
     }
     const int inter = PyObject_IsTrue(a[11]);
+    void* stream = stream_of(a[14], k);
+    if (!given(a[12])) used_on(a[14], stream, q_out);
+    if (a[13] == Py_True) used_on(a[14], stream, k_out);
     const int rc = f_append(kv.n, as_int(qv.p || given(a[0]) ? qv.h : c.h, "heads"), c.h, c.d, as_int(2 * half, "rot_dim"), inter > 0,
                             qv.p, qv.st, qv.sh, kv.p, kv.st, kv.sh, vv.p, vv.st, vv.sh, positions, cp, sp, n_pos, slots,
-                            c.code, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, qo.p, qo.st, qo.sh, ko.p, ko.st, ko.sh,
-                            stream_of(a[14], k));
+                            c.code, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, qo.p, qo.st, qo.sh, ko.p, ko.st, ko.sh, stream);
     return rc ? PyLong_FromLong(rc) : two(q_out, k_out);
 }
 
@@ -260,8 +269,11 @@ PyObject* do_read(PyObject* const* a) {
     if (k.sizes() != at::IntArrayRef(shape, 3) || v.sizes() != k.sizes() || v.scalar_type() != k.scalar_type() ||
         !k.is_contiguous() || !v.is_contiguous())
         value_error("k_out and v_out must be contiguous [n_tokens, kv_heads, head_dim] of one dtype");
+    void* stream = stream_of(a[11], kc);
+    if (!given(a[8])) used_on(a[11], stream, k);
+    if (!given(a[9])) used_on(a[11], stream, v);
     const int rc = f_read(as_int(batch, "batch"), n, c.h, c.d, c.code, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, tb.p, tb.stride,
-                          tb.n, cu, first, out_code(k.scalar_type()), k.data_ptr(), v.data_ptr(), stream_of(a[11], kc));
+                          tb.n, cu, first, out_code(k.scalar_type()), k.data_ptr(), v.data_ptr(), stream);
     return rc ? PyLong_FromLong(rc) : two(k, v);
 }
 
@@ -278,11 +290,14 @@ PyObject* do_prefill(PyObject* const* a) {
     const int32_t *cq = int32s(a[3], batch + 1, "cu_q"), *ck = int32s(a[4], batch + 1, "cu_k");
     const at::Tensor out = attn_out(a[7], a[8], q), lse = attn_lse(a[9], q);
     const View ov = view(out, "out");
+    void* stream = stream_of(a[10], q);
+    if (!given(a[7])) used_on(a[10], stream, out);
+    if (a[9] == Py_True) used_on(a[10], stream, lse);
     const int rc = f_prefill(as_int(batch, "batch"), qv.n, kv.n, as_int(integer(a[5], "max_q"), "max_q"), as_int(qv.h, "heads"),
                              as_int(kv.h, "kv_heads"), as_int(qv.d, "head_dim"), out_code(q.scalar_type()),
                              out_code(out.scalar_type()), qv.p, qv.st, qv.sh, kv.p, kv.st, kv.sh, vv.p, vv.st, vv.sh, cq, ck,
                              (float)scale_of(a[6], qv.d), ov.p, ov.st, ov.sh,
-                             lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, stream_of(a[10], q));
+                             lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, stream);
     return rc ? PyLong_FromLong(rc) : two(out, lse);
 }
 
@@ -305,11 +320,15 @@ PyObject* do_decode(PyObject* const* a) {
         const size_t need = f_decode_bytes(batch, heads, c.h, c.d, max_len);
         if (need) ws = fresh({(int64_t)need}, at::kByte, q);
     }
+    void* stream = stream_of(a[13], q);
+    if (!given(a[9])) used_on(a[13], stream, out);
+    if (a[11] == Py_True) used_on(a[13], stream, lse);
+    if (!given(a[12])) used_on(a[13], stream, ws);
     const int rc = f_decode(batch, heads, c.h, c.d, out_code(q.scalar_type()), out_code(out.scalar_type()), qv.p, qv.st, qv.sh,
                             c.code, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, tb.p, tb.stride, tb.n, lens, max_len,
                             (float)scale_of(a[8], c.d), ov.p, ov.st, ov.sh,
                             lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
-                            ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.nbytes() : 0, stream_of(a[13], q));
+                            ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.nbytes() : 0, stream);
     return rc ? PyLong_FromLong(rc) : two(out, lse);
 }
 

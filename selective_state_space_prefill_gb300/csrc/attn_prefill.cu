@@ -679,10 +679,6 @@ int launch_shape(const AttnPrefillArgs& a, cudaStream_t stream, const char** why
         *why = "cudaGetDevice / multiprocessor count failed";
         return -1;
     }
-    if (tile_pairs(a) * a.n_q * 8 >= (1LL << 31)) {
-        *why = "sequences times heads times query tiles pass the grid";
-        return -1;
-    }
     // Where the items leave half of the SMs or more without work and have 2048 keys or more on average, up
     // to eight CTAs share the keys of one, 512 or more each: 8 rows of 32 heads over 4008 keys 66 -> 27 us,
     // 1024 rows of 16 heads over 9024 keys 115 -> 76; with 1024 keys the join's 6 us are not won back (19 -> 25).

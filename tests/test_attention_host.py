@@ -78,6 +78,7 @@ PREFILL = dict(batch=1, tq=4, tk=4, max_q=4, H=8, Hk=2, D=64, idt=1, odt=1, q=FA
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID),
     (dict(cuq=None), INVALID), (dict(q=None), INVALID), (dict(kt=100), MISALIGNED), (dict(vh=16), INVALID),
     (dict(out=None), INVALID), (dict(ot=64), INVALID), (dict(out=FAKE + 2), MISALIGNED), (dict(lse=FAKE + 2), MISALIGNED),
+    (dict(batch=65535, tq=1 << 26, max_q=1 << 20), UNSUPPORTED),
 ])
 def test_prefill_refusals(lib, kw, code):
     _refused(lib, "attn_prefill", PREFILL, kw, code)

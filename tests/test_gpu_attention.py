@@ -111,6 +111,7 @@ def test_prefill_unseen_values_do_not_leak(D, n, bad):
 @pytest.mark.parametrize("ql,kl,H,Hk,D", [
     ([1], [5000], 8, 2, 128), ([8, 3, 1], [2200, 0, 999], 4, 1, 64), ([257, 300], [2000, 1700], 3, 3, 80),
     ([700], [900], 2, 1, 128), ([40], [3001], 12, 4, 64), ([1, 0, 2], [1, 4000, 130], 5, 5, 96),
+    ([70, 0, 129], [2500, 2600, 2049], 3, 1, 128), ([2, 2], [4200, 4097], 6, 2, 64),
 ])
 def test_prefill_few_rows_over_many_keys(ql, kl, H, Hk, D):
     """Items too few for the GPU: their keys are shared out between the CTAs of a cluster."""
@@ -122,6 +123,24 @@ def test_prefill_few_rows_over_many_keys(ql, kl, H, Hk, D):
                                     out_dtype=out_dtype, lse=True)
         check_attention(out, lse, _prefill_ref(q, k, v, ql, kl, D ** -0.5), D, out_dtype, W_PREFILL, f"{ql} {kl}")
     assert ssm.device_status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prefill_split_keys_do_not_leak(bad):
+    """The same where a cluster shares the keys: a bad value in the last CTA's share reaches only the
+    rows that see it."""
+    g = torch.Generator().manual_seed(6)
+    lq, lk, D = 300, 5000, 64
+    q, k, v = heads(g, lq, 3, D).to(DEV), heads(g, lk, 1, D).to(DEV), heads(g, lk, 1, D).to(DEV)
+    cq, ck = cu([lq]).to(DEV), cu([lk]).to(DEV)
+    clean, cl = ssm.attn_prefill(q, k, v, cq, ck, lq, lse=True, out_dtype=torch.float32)
+    v2 = v.clone()
+    v2[4850, 0, 7] = bad                        # row i sees keys up to i + 4700
+    out, lse = ssm.attn_prefill(q, k, v2, cq, ck, lq, lse=True, out_dtype=torch.float32)
+    hit = out[150:, :, 7]
+    assert bool(hit.isnan().all()) if bad != bad else bool((hit == bad).all())
+    out[150:, :, 7] = clean[150:, :, 7]
+    assert torch.equal(out, clean) and torch.equal(lse, cl)
 
 
 def test_prefill_max_q_and_empty_calls():
