@@ -342,6 +342,9 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
                 vs[r] = lds4(base + 2 * R::kRows + 64 + 4 * (g + 8 * r));
             }
         }
+        uint32_t at[DP / 32];                           // int8 keys' places, and values' behind them
+#pragma unroll
+        for (int ld = 0; ld < DP / 32; ++ld) at[ld] = base + R::step(key_at, 2 * ld);
         // ---- scores: S^T = K q^T, in two chains of products
         float s[NT][4], s1[NT][4];
 #pragma unroll
@@ -352,7 +355,7 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
 #pragma unroll
             for (int ld = 0; ld < DP / 32; ++ld) {      // 32 dimensions: two chunks of 16
                 uint32_t x[4];
-                matrices(x, base + R::step(key_at, 2 * ld));
+                matrices(x, at[ld]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const uint32_t af[4] = {raised<false>(x[2 * u]), raised<false>(x[2 * u + 1]),
@@ -467,7 +470,7 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
 #pragma unroll
             for (int ld = 0; ld < DP / 32; ++ld) {
                 uint32_t x[4];
-                matrices_t(x, base + R::kRows + R::step(val_at, 2 * ld));
+                matrices_t(x, at[ld] + R::kRows);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {           // rows g and g + 8: dimensions 2g and 2g + 1 of the chunk
                     const uint32_t af[4] = {halves<false>(x[2 * u]), halves<true>(x[2 * u]),
