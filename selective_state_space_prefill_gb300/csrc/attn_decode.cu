@@ -25,6 +25,7 @@
 // scale in it, so that they fit whatever the rows' scales are).  With bf16 rows the weights are a
 // bf16 pair hi + lo.  The references are raised only when a weight would pass them by more than 2^8,
 // so rescaling o is rare.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -32,6 +33,8 @@
 
 namespace ssm {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
@@ -126,9 +129,10 @@ struct Ring {
     }
 };
 
-// Pieces of the long axis.
+// Pieces of the long axis; `cluster`: the pieces are the CTAs of a cluster and join there.
 struct Cut {
     int tokens, pieces;
+    bool cluster;
 };
 
 // A request's length, kept inside the bound and the table.
@@ -160,7 +164,7 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* p, float4 v, float l) {
 }
 
 // DP: head_dim padded to 64 or 128.  NT: groups of 8 query heads a CTA serves.
-template <bool I8, int DP, int NT, typename Tout>
+template <bool I8, int DP, int NT, bool kCluster, typename Tout>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? (I8 ? 4 : 3) : 2)
 k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
     constexpr int kHeads = 8 * NT;
@@ -171,7 +175,7 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
     __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads], s_w[kWarps][kHeads];
     float(*s_o)[kHeads][DP + 4] = reinterpret_cast<float(*)[kHeads][DP + 4]>(smem);     // + 4: no bank twice
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (!kCluster) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int group = a.n_q / a.c.n_kv, per_kv = (group + kHeads - 1) / kHeads;
@@ -179,7 +183,7 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
     const int nh = min(kHeads, (hk + 1) * group - h0);  // heads of this CTA
     const int len = length_of(a, b, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0);
     const int begin = (int)blockIdx.x * cut.tokens, end = min(len, begin + cut.tokens);
-    if (begin >= end && !(blockIdx.x == 0 && cut.pieces == 1)) return;
+    if (!kCluster && begin >= end && !(blockIdx.x == 0 && cut.pieces == 1)) return;
     const int dim = a.c.dim, psz = a.c.page_size;
     const float c = a.scale * kLog2e;
 
@@ -536,9 +540,9 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
         s_m[0][hd] = M;
         s_l[0][hd] = L;
         const int64_t at = (int64_t)b * a.n_q + h0 + hd;
-        if (hd < nh && cut.pieces > 1)
+        if (!kCluster && hd < nh && cut.pieces > 1)
             piece_sums<DP>(a, cut, gridDim.z)[at * cut.pieces + blockIdx.x] = make_float2(M, L);
-        if (hd < nh && cut.pieces == 1 && a.lse) a.lse[at] = lse_of(M, L);
+        if (!kCluster && hd < nh && cut.pieces == 1 && a.lse) a.lse[at] = lse_of(M, L);
     }
     __syncthreads();
     for (int x = threadIdx.x; x < nh * (DP / 4); x += kThreads) {
@@ -550,13 +554,38 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
             const float f = s_w[w][hd];
             acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
         }
-        if (cut.pieces > 1) {
+        if constexpr (kCluster) {
+            *reinterpret_cast<float4*>(&s_o[0][hd][d]) = acc;        // read above by this thread alone
+        } else if (cut.pieces > 1) {
             const int64_t piece = ((int64_t)b * a.n_q + h0 + hd) * cut.pieces + blockIdx.x;
             *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.workspace) + piece * DP + d) = acc;
         } else if (d < dim) {
             store_out(reinterpret_cast<Tout*>(a.out) + (int64_t)b * a.o_st + (int64_t)(h0 + hd) * a.o_sh + d, acc,
                       s_l[0][hd]);
         }
+    }
+    if constexpr (kCluster) {
+        // the pieces' parts, read from the cluster's CTAs, which share the elements out
+        auto cluster = cg::this_cluster();
+        cluster.sync();
+        for (int x = (int)cluster.block_rank() * kThreads + threadIdx.x; x < nh * (DP / 4); x += cut.pieces * kThreads) {
+            const int hd = x / (DP / 4), d = 4 * (x % (DP / 4));
+            float M = -INFINITY, L = 0.f;
+            for (int p = 0; p < cut.pieces; ++p) M = fmaxf(M, *cluster.map_shared_rank(&s_m[0][hd], p));
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p = 0; p < cut.pieces; ++p) {
+                const float mp = *cluster.map_shared_rank(&s_m[0][hd], p), lp = *cluster.map_shared_rank(&s_l[0][hd], p);
+                const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&s_o[0][hd][d], p));
+                const float f = mp == -INFINITY && lp == 0.f ? 0.f : ex2(mp - M);      // a piece that saw no key
+                L += lp * f;
+                acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+            }
+            const int64_t at = (int64_t)b * a.n_q + h0 + hd;
+            if (d < dim)
+                store_out(reinterpret_cast<Tout*>(a.out) + (int64_t)b * a.o_st + (int64_t)(h0 + hd) * a.o_sh + d, acc, L);
+            if (a.lse && d == 0) a.lse[at] = lse_of(M, L);
+        }
+        cluster.sync();                                 // no CTA leaves while its part is read
     }
 }
 
@@ -624,10 +653,25 @@ int lanes_of(int n_q, int n_kv) {
 }
 
 Cut cut_of(int batch, int n_q, int n_kv, int64_t max_len) {
+    const int64_t side = (int64_t)batch * lanes_of(n_q, n_kv);
+    Cut c;
+    auto even = [&](int64_t p) {
+        c.tokens = (int)(((max_len + p - 1) / p + 63) / 64 * 64);
+        c.pieces = (int)((max_len + c.tokens - 1) / c.tokens);
+    };
+    // A short call: at most eight pieces of 64 keys or more, all on the GPU at once and joined by their
+    // cluster without a second launch: one request of 1024 keys 12.9 -> 10.9 us, nine of 4096 31 -> 27.  A
+    // request or two of 4096 keys on 8 kv heads want more than 64 CTAs: there 17 us against 13.
+    if (max_len > 64 && side * 8 <= 608 && (max_len <= 2048 || (max_len <= 4096 && side * 8 >= 152))) {
+        const int64_t p = (max_len + 63) / 64;
+        even(p < 8 ? p : 8);
+        c.cluster = true;
+        return c;
+    }
+    c.cluster = false;
     // Many CTAs of at least 512 keys, so that requests of different lengths fill the GPU evenly and the
     // join reads little; where that leaves fewer than two per resident slot (152 SMs x 3), pieces
     // down to 128 keys.
-    const int64_t side = (int64_t)batch * lanes_of(n_q, n_kv);
     int64_t p = (3648 + side - 1) / side;
     const int64_t most = (max_len + 511) / 512;
     if (p > most) p = most;
@@ -636,33 +680,40 @@ Cut cut_of(int batch, int n_q, int n_kv, int64_t max_len) {
         const int64_t fine = (max_len + 127) / 128;
         if (p > fine) p = fine;
     }
-    Cut c;
-    c.tokens = (int)(((max_len + p - 1) / p + 63) / 64 * 64);
-    c.pieces = (int)((max_len + c.tokens - 1) / c.tokens);
+    even(p);
     return c;
 }
 
-template <bool I8, int DP, int NT, typename Tout>
-int launch(const AttnDecodeArgs& a, cudaStream_t stream, const char** why) {
-    const Cut cut = cut_of(a.batch, a.n_q, a.c.n_kv, a.max_len);
+template <bool I8, int DP, int NT, bool kCluster, typename Tout>
+int launch(const AttnDecodeArgs& a, const Cut& cut, cudaStream_t stream, const char** why) {
     constexpr int kRing = kWarps * Ring<I8, DP>::kStages * Ring<I8, DP>::kStage, kParts = kWarps * 8 * NT * (DP + 4) * 4;
     constexpr int kSmem = kRing > kParts ? kRing : kParts;
+    auto kern = k_attn_decode<I8, DP, NT, kCluster, Tout>;
     static ContextMemo attr_memo;
-    if (!opt_in_dynamic_smem(attr_memo, k_attn_decode<I8, DP, NT, Tout>, kSmem, why)) return -1;
-    const dim3 grid((unsigned)cut.pieces, (unsigned)lanes_of(a.n_q, a.c.n_kv), (unsigned)a.batch);
-    k_attn_decode<I8, DP, NT, Tout><<<grid, kThreads, kSmem, stream>>>(a, cut);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && cut.pieces > 1) {
+    if (!opt_in_dynamic_smem(attr_memo, kern, kSmem, why)) return -1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)cut.pieces, (unsigned)lanes_of(a.n_q, a.c.n_kv), (unsigned)a.batch);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    if (kCluster) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)cut.pieces;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+    }
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, cut);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e == cudaSuccess && !kCluster && cut.pieces > 1) {
         // launched while the pieces still run; it waits for them before it reads
-        cudaLaunchConfig_t cfg = {};
         const bool many = cut.pieces > 16;              // a warp joins up to 16 pieces in two rounds of loads
         cfg.gridDim = dim3((unsigned)(many ? a.n_q : (a.n_q + kJoinWarps - 1) / kJoinWarps), (unsigned)a.batch);
         cfg.blockDim = dim3(32 * kJoinWarps);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
+        cfg.dynamicSmemBytes = 0;
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
         cfg.numAttrs = 1;
         e = many ? cudaLaunchKernelEx(&cfg, k_attn_decode_join<DP, kJoinWarps, Tout>, a, cut)
                  : cudaLaunchKernelEx(&cfg, k_attn_decode_join<DP, 1, Tout>, a, cut);
@@ -673,18 +724,24 @@ int launch(const AttnDecodeArgs& a, cudaStream_t stream, const char** why) {
     return -1;
 }
 
+template <bool I8, int DP, int NT, typename Tout>
+int launch_cut(const AttnDecodeArgs& a, cudaStream_t stream, const char** why) {
+    const Cut cut = cut_of(a.batch, a.n_q, a.c.n_kv, a.max_len);
+    return cut.cluster ? launch<I8, DP, NT, true, Tout>(a, cut, stream, why) : launch<I8, DP, NT, false, Tout>(a, cut, stream, why);
+}
+
 template <bool I8, typename Tout>
 int launch_shape(const AttnDecodeArgs& a, cudaStream_t stream, const char** why) {
     const bool wide = a.n_q / a.c.n_kv > 8;
-    if (a.c.dim <= 64) return wide ? launch<I8, 64, 2, Tout>(a, stream, why) : launch<I8, 64, 1, Tout>(a, stream, why);
-    return wide ? launch<I8, 128, 2, Tout>(a, stream, why) : launch<I8, 128, 1, Tout>(a, stream, why);
+    if (a.c.dim <= 64) return wide ? launch_cut<I8, 64, 2, Tout>(a, stream, why) : launch_cut<I8, 64, 1, Tout>(a, stream, why);
+    return wide ? launch_cut<I8, 128, 2, Tout>(a, stream, why) : launch_cut<I8, 128, 1, Tout>(a, stream, why);
 }
 
 }  // namespace
 
 size_t attn_decode_workspace(int batch, int n_q, int n_kv, int dim, int max_len) {
     const Cut c = cut_of(batch, n_q, n_kv, max_len);
-    return c.pieces == 1 ? 0 : (size_t)batch * n_q * c.pieces * ((dim <= 64 ? 64 : 128) + 2) * sizeof(float);
+    return c.pieces == 1 || c.cluster ? 0 : (size_t)batch * n_q * c.pieces * ((dim <= 64 ? 64 : 128) + 2) * sizeof(float);
 }
 
 int launch_attn_decode(const AttnDecodeArgs& a, bool cache_i8, bool out_bf16, cudaStream_t stream, const char** why) {
