@@ -548,12 +548,12 @@ int attn_cache_read(int batch, int64_t n_tokens, int n_kv_heads, int head_dim, s
  * its earlier tokens, and a query with no visible key gives zeros and lse -inf.
  *   s_ij = scale * q_i . k_j;  out_i = sum_j softmax_j(s_ij) v_j;  lse_i = ln sum_j exp(s_ij)
  * bf16 products with fp32 accumulation; the softmax weights are rounded to bf16 for the second
- * product, their sum is not.  What lies in keys and values that a query does not see, NaN and
+ * product (kept to 16 bits when total_q * n_q_heads <= 256), their sum is not.  What lies in keys and values that a query does not see, NaN and
  * infinities included, does not reach its output.
  *
  *   batch, total_q, total_k      1..65535; rows of q/out and of k/v (>= 0; total_q == 0 does nothing)
  *   max_q                        an upper bound of the sequences' query rows (rows past it are not
- *                                computed)
+ *                                computed); ceil(max_q / 256) * batch * H must stay below 2^28
  *   in_dtype                     SSM_BF16; SSM_F32 returns SSM_ERR_UNSUPPORTED
  *   q, k, v                      views as above       cu_q, cu_k: [batch + 1] int32, not decreasing
  *   scale                        finite, > 0

@@ -18,13 +18,22 @@
 //     scores in registers; they write p over their scores in TMEM, where tcgen05.mma takes it as
 //     its A operand, and rescale and store o;
 //   * warp 8: TMA loads of the two query tiles and a ring of key and value blocks;
-//   * warp 9: issues the MMAs: per block and tile o += P V, then the next block's S = Q K^T;
+//   * warp 9: issues the MMAs: per block and tile o += P V, then the next block's S = Q K^T, the tiles
+//     in turn (issued independently the tiles fall into step, and both softmaxes then run while the
+//     tensor cores idle: 2.98 ms instead of 2.51 in the case below);
 //   * warps 10-11: make the value rows of blocks that some row does not wholly see harmless: the
 //     product multiplies an unseen value by 0, which a NaN or an infinity survives.  Rows past the
 //     sequence are zeroed; non-finite values are zeroed and noted (the first key of each column
 //     that holds +inf, -inf, NaN), and the rows that do see them get them back at the end.
+// Where the items are few and the keys many, the CTAs of a cluster share an item's key blocks and join
+// their (m, l, o) through distributed shared memory.
 // TMEM: scores of tile t at column 128 t, output at 256 + 128 t; all 512 columns, one CTA per SM.
 // The grid runs the longest rows first (the last tiles of every head and sequence), so the tail is short.
+//
+// Measured (CUDA events): 16384 tokens, 56 query and 8 kv heads of 128: 2.39 ms, 1611 TFLOP/s, 0.85 of
+// cuBLAS's bf16 rate; the products alone 2.2 ms, as Q K^T reads 128 bytes of shared memory a cycle, all
+// there is.  8 packed prompts of 260 to 4096 tokens, 32 / 8 heads: 197 us, half of it the starts and ends
+// of short CTAs.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
