@@ -326,3 +326,25 @@ def test_decode_workspace_is_kept_inside():
     assert bool((buf[:256] == 0xA5).all()) and bool((buf[256 + need:] == 0xA5).all())
     assert bool((obuf[:, 0] == 7.0).all()) and bool((obuf[:, -1] == 7.0).all())
     check_attention(out, None, _decode_ref(q, c, lens, D ** -0.5), D, torch.bfloat16, W_DECODE)
+
+
+@pytest.mark.parametrize("rows,keys,H,Hk", [(700, 700, 8, 2), (8, 4008, 8, 2)])
+def test_prefill_gives_the_same_bits_again(rows, keys, H, Hk):
+    """No atomics and a fixed order of the joins: calls on the same inputs agree bit by bit, whether one
+    CTA takes an item's keys or a cluster shares them."""
+    g = torch.Generator().manual_seed(rows)
+    q, k, v = (heads(g, n, h, 128).to(DEV) for n, h in ((rows, H), (keys, Hk), (keys, Hk)))
+    first, *rest = [ssm.attn_prefill(q, k, v, cu([rows]).to(DEV), cu([keys]).to(DEV), rows, lse=True) for _ in range(4)]
+    for out, lse in rest:
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("i8", [True, False])
+@pytest.mark.parametrize("lens", [[900, 33], [9000, 1, 4097]])
+def test_decode_gives_the_same_bits_again(lens, i8):
+    g = torch.Generator().manual_seed(sum(lens))
+    c = paged(torch.randn(sum(lens), 2, 128, generator=g), torch.randn(sum(lens), 2, 128, generator=g), lens, 64, i8)
+    q = heads(g, len(lens), 16, 128)
+    first, *rest = [_decode(q, c, lens, lse=True) for _ in range(4)]
+    for out, lse in rest:
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
