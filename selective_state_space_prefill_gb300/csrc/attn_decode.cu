@@ -28,7 +28,8 @@
 // Precision: scores, m, l and o are fp32.  With int8 rows the query is held in fp16 after scaling
 // by a power of two (exact for bf16 queries within 2^-25 of their head's maximum) and the weights
 // w_j = 2^(s_j - mw) scale_j in fp16 (11 bits; mw is a running reference of the exponent with the
-// scale in it, so that they fit whatever the rows' scales are).  With bf16 rows the weights are a
+// scale in it, so that they fit whatever the rows' scales are; below 2^-20 of the largest they lose
+// bits, below 2^-31 they are zero, either way under 2^-31 of the largest each).  With bf16 rows the weights are a
 // bf16 pair hi + lo.  The references are raised only when a weight would pass them by more than 2^8,
 // so rescaling o is rare.
 #include <cooperative_groups.h>
