@@ -30,7 +30,7 @@
 // w_j = 2^(s_j - mw) scale_j in fp16 (11 bits; mw is a running reference of the exponent with the
 // scale in it, so that they fit whatever the rows' scales are; below 2^-20 of the largest they lose
 // bits, below 2^-31 they are zero, either way under 2^-31 of the largest each).  With bf16 rows the weights are a
-// bf16 pair hi + lo.  The references are raised only when a weight would pass them by more than 2^8,
+// bf16 pair hi + lo, both positive, so that an infinite value keeps its sign.  The references are raised only when a weight would pass them by more than 2^8,
 // so rescaling o is rare.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
@@ -471,9 +471,8 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
                     pb[i][r] = transpose8(pack_h(w0, w1));
                     pl[i][r] = 0u;
                 } else {
-                    const uint32_t hi = pack_b(w0, w1);
-                    pb[i][r] = transpose8(hi);
-                    pl[i][r] = transpose8(pack_b(w0 - __uint_as_float(hi << 16), w1 - __uint_as_float(hi & 0xffff0000u)));
+                    pb[i][r] = transpose8(high_parts(w0, w1));
+                    pl[i][r] = transpose8(pack_b(low_part(w0), low_part(w1)));
                 }
             }
         // ---- O^T += V^T P^T

@@ -43,6 +43,19 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
+// The low bf16 part of a softmax weight w >= 0 whose high part is w's upper 16 bits (cut off, not rounded).
+// Cut off, the rest is never negative, and it is raised to 2^-24 of w (half of w's own last place), or to
+// the smallest bf16, so that it is 0 only where w is: both parts are then multiplied by the same value, and
+// an infinite one stays infinite (0 x inf and inf - inf are NaN).  hi + lo is w to 16 bits.
+__device__ __forceinline__ float low_part(float w) {
+    const float hi = __uint_as_float(__float_as_uint(w) & 0xffff0000u);
+    return fmaxf(w - hi, fmaxf(hi * 0x1p-24f, fminf(hi, 0x1p-133f)));
+}
+// The upper 16 bits of two floats.
+__device__ __forceinline__ uint32_t high_parts(float w0, float w1) {
+    return __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
+}
+
 // softplus(v) = log(1 + e^v), with e = e^v from MUFU.EX2:
 //   v > 20       -> v: the correction log1p(e^-v) < 2.1e-9 is below the fp32 resolution of v;
 //   e < 1/16     -> log1p(e) by its alternating Taylor series e - e^2/2 + e^3/3 - e^4/4 + e^5/5
