@@ -548,8 +548,10 @@ int attn_cache_read(int batch, int64_t n_tokens, int n_kv_heads, int head_dim, s
  * its earlier tokens, and a query with no visible key gives zeros and lse -inf.
  *   s_ij = scale * q_i . k_j;  out_i = sum_j softmax_j(s_ij) v_j;  lse_i = ln sum_j exp(s_ij)
  * bf16 products with fp32 accumulation; the softmax weights are rounded to bf16 for the second
- * product (kept to 16 bits when total_q * n_q_heads <= 256), their sum is not.  What lies in keys and values that a query does not see, NaN and
- * infinities included, does not reach its output.
+ * product (kept to 16 bits when total_q * n_q_heads <= 256), their sum is not.  What lies in keys and
+ * values that a query does not see, NaN and infinities included, does not reach its output.  A value of
+ * +-inf that it sees makes that element +-inf (NaN where both signs meet, and it may be NaN where the
+ * value's weight underflows fp32).
  *
  *   batch, total_q, total_k      1..65535; rows of q/out and of k/v (>= 0; total_q == 0 does nothing)
  *   max_q                        an upper bound of the sequences' query rows (rows past it are not
@@ -579,7 +581,9 @@ size_t attn_decode_workspace_bytes(int batch, int n_q_heads, int n_kv_heads, int
  *   batch                1..65535 requests
  *   q                    view [batch][H][D] bf16       lens: [batch] int32, tokens cached for each;
  *                        0 gives zeros and lse -inf.  A length below 0, above max_len or past the
- *                        table's row is cut to the range and sets SSM_DEV_BAD_INDEX.
+ *                        table's row is cut to the range and sets SSM_DEV_BAD_INDEX.  An infinity in
+ *                        a bf16 value row counts as attn_prefill says; an int8 row that held one
+ *                        reads as NaN.
  *   max_len              an upper bound of lens, 1 .. 2^30
  *   cache                as above; a page outside [0, n_pages) counts as not visible and sets
  *                        SSM_DEV_BAD_INDEX

@@ -156,7 +156,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// kPair: the weights as bf16 pairs hi + lo, both multiplied with the values.
+// kPair: the weights as bf16 pairs hi + lo, both multiplied with the values and both positive where the weight
+// is, so that an infinite value keeps its sign.
 // kSplit: the CTAs of a cluster share the key blocks of an item and join their outputs through
 // distributed shared memory.
 template <int DP, bool kPair, bool kSplit, typename Tout>
@@ -328,9 +329,8 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     x0 = ex2(x0);
                     x1 = ex2(x1);
                     sum[i & 3] = add2(sum[i & 3], pair(x0, x1));
-                    p[i] = pack_bf16(x0, x1);
-                    if constexpr (kPair)
-                        p_lo[i] = pack_bf16(x0 - __uint_as_float(p[i] << 16), x1 - __uint_as_float(p[i] & 0xffff0000u));
+                    p[i] = kPair ? high_parts(x0, x1) : pack_bf16(x0, x1);
+                    if constexpr (kPair) p_lo[i] = pack_bf16(low_part(x0), low_part(x1));
                 }
                 tmem_st32(ts + 32u * q, p);
                 if constexpr (kPair) tmem_st32(ts + 64u + 32u * q, p_lo);

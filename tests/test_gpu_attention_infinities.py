@@ -65,3 +65,24 @@ def test_decode_int8_row_with_an_infinity_reads_as_nan():
     assert bool(seen.isnan().all())
     before, _ = _decode(c, q, 11, max_len=n)
     assert bool(before.isfinite().all())
+
+
+# 256 rows x heads or fewer (weights as bf16 pairs), whole and with the keys split; more of them
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("rows,keys,H,D", [
+    (1, 1, 2, 64), (60, 700, 4, 128), (9, 5000, 8, 64), (3, 4400, 2, 80), (300, 900, 2, 128), (300, 5000, 3, 64),
+])
+def test_prefill_seen_infinity(rows, keys, H, D, sign):
+    """The infinite value in a block that every row sees, in one that some rows see, and at the last key."""
+    g = torch.Generator().manual_seed(rows + keys)
+    q, k, v = heads(g, rows, H, D).to(DEV), heads(g, keys, 1, D).to(DEV), heads(g, keys, 1, D).to(DEV)
+    cq, ck = cu([rows]).to(DEV), cu([keys]).to(DEV)
+    clean, cl = ssm.attn_prefill(q, k, v, cq, ck, rows, lse=True, out_dtype=torch.float32)
+    for at in sorted({0, keys // 2, keys - rows // 2 - 1, keys - 1}):
+        v2 = v.clone()
+        v2[at, 0, 5] = sign * INF
+        out, lse = ssm.attn_prefill(q, k, v2, cq, ck, rows, lse=True, out_dtype=torch.float32)
+        first = max(0, at - (keys - rows))                  # the first row that sees it
+        assert bool((out[first:, :, 5] == sign * INF).all()), at
+        out[first:, :, 5] = clean[first:, :, 5]
+        assert torch.equal(out, clean) and torch.equal(lse, cl)
