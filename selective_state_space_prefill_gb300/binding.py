@@ -615,8 +615,9 @@ def attn_rope_table(inv_freq, n_pos, scale=1.0, device="cuda", stream=None):
     cos = torch.empty(n_pos, len(freqs), device=device, dtype=torch.float32)
     sin = torch.empty_like(cos)
     _need_cuda(cos)
-    rc = lib.attn_rope_table(n_pos, len(freqs), ctypes.cast(arr, ctypes.c_void_p), float(scale), _ptr(cos), _ptr(sin),
-                             _stream(stream))
+    with torch.cuda.device(cos.device):         # the library works on the current device
+        rc = lib.attn_rope_table(n_pos, len(freqs), ctypes.cast(arr, ctypes.c_void_p), float(scale), _ptr(cos), _ptr(sin),
+                                 _stream(stream))
     _check(lib, "attn_rope_table", rc)
     return cos, sin
 

@@ -8,11 +8,14 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
+#include <optional>
 #include <stdexcept>
 #include <string>
 
@@ -41,6 +44,34 @@ const at::Tensor& cuda_tensor(PyObject* o, const char* name) {
     return t;
 }
 bool given(PyObject* o) { return o != nullptr && o != Py_None; }
+
+// The one GPU that a call's tensors lie on, made current while the call allocates and launches: the
+// library works on the current device, whatever the pointers are.
+struct Arg {
+    int at;
+    const char* name;
+};
+class OnDevice {
+public:
+    OnDevice(PyObject* const* a, std::initializer_list<Arg> tensors) {
+        for (const Arg& x : tensors) {
+            PyObject* o = a[x.at];
+            if (!given(o) || PyBool_Check(o) || !THPVariable_Check(o)) continue;
+            const at::Tensor& t = THPVariable_Unpack(o);
+            if (!t.is_cuda()) continue;                 // what has to be a CUDA tensor is seen to by name
+            const int i = t.get_device();
+            if (index_ >= 0 && i != index_)
+                value_error(std::string(x.name) + " is on cuda:" + std::to_string(i) + ", other arguments on cuda:" +
+                            std::to_string(index_));
+            index_ = i;
+        }
+        if (index_ >= 0) guard_.emplace(static_cast<c10::DeviceIndex>(index_));
+    }
+
+private:
+    int index_ = -1;
+    std::optional<c10::cuda::CUDAGuard> guard_;
+};
 
 // A [tokens, heads, dim] view.  A stride along an extent of one moves nothing, so it is given as a
 // value the library accepts.
@@ -198,6 +229,8 @@ PyObject* two(const at::Tensor& a, const at::Tensor& b) {
 
 // (q, k, v, positions, cos, sin, k_cache, v_cache, slots, k_scale, v_scale, interleaved, q_out, k_out, stream)
 PyObject* do_append(PyObject* const* a) {
+    const OnDevice on(a, {{1, "k"}, {0, "q"}, {2, "v"}, {3, "positions"}, {4, "cos"}, {5, "sin"}, {6, "k_cache"}, {7, "v_cache"},
+                          {8, "slots"}, {9, "k_scale"}, {10, "v_scale"}, {12, "q_out"}, {13, "k_out"}});
     const Cache c = cache(a[6], a[7], a[9], a[10]);
     const at::Tensor &k = cuda_tensor(a[1], "k"), &v = cuda_tensor(a[2], "v");
     need_type(k, at::kBFloat16, "k", "bfloat16");
@@ -256,6 +289,8 @@ PyObject* do_append(PyObject* const* a) {
 
 // (k_cache, v_cache, page_table, cu_len, n_tokens, k_scale, v_scale, first, k_out, v_out, out_dtype, stream)
 PyObject* do_read(PyObject* const* a) {
+    const OnDevice on(a, {{0, "k_cache"}, {1, "v_cache"}, {2, "page_table"}, {3, "cu_len"}, {5, "k_scale"}, {6, "v_scale"},
+                          {7, "first"}, {8, "k_out"}, {9, "v_out"}});
     const Cache c = cache(a[0], a[1], a[5], a[6]);
     const at::Tensor& kc = THPVariable_Unpack(a[0]);
     const int64_t batch = cuda_tensor(a[3], "cu_len").numel() - 1, n = integer(a[4], "n_tokens");
@@ -281,6 +316,7 @@ double scale_of(PyObject* o, int64_t d) { return given(o) ? number(o, "scale") :
 
 // (q, k, v, cu_q, cu_k, max_q, scale, out, out_dtype, lse, stream)
 PyObject* do_prefill(PyObject* const* a) {
+    const OnDevice on(a, {{0, "q"}, {1, "k"}, {2, "v"}, {3, "cu_q"}, {4, "cu_k"}, {7, "out"}, {9, "lse"}});
     const at::Tensor &q = cuda_tensor(a[0], "q"), &k = cuda_tensor(a[1], "k"), &v = cuda_tensor(a[2], "v");
     const View qv = view(q, "q"), kv = view(k, "k"), vv = view(v, "v");
     if (kv.d != qv.d || vv.d != qv.d || vv.h != kv.h || vv.n != kv.n)
@@ -303,6 +339,8 @@ PyObject* do_prefill(PyObject* const* a) {
 
 // (q, k_cache, v_cache, page_table, lens, max_len, k_scale, v_scale, scale, out, out_dtype, lse, workspace, stream)
 PyObject* do_decode(PyObject* const* a) {
+    const OnDevice on(a, {{0, "q"}, {1, "k_cache"}, {2, "v_cache"}, {3, "page_table"}, {4, "lens"}, {6, "k_scale"},
+                          {7, "v_scale"}, {9, "out"}, {11, "lse"}, {12, "workspace"}});
     const Cache c = cache(a[1], a[2], a[6], a[7]);
     const at::Tensor& q = cuda_tensor(a[0], "q");
     const View qv = view(q, "q");
