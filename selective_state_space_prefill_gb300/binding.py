@@ -8,6 +8,7 @@ Output tensors are allocated with torch when the caller does not pass them.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from pathlib import Path
 
@@ -570,6 +571,9 @@ def ssd_decode_step(xBC, z, dt, conv_w, conv_b, A, D, dt_bias, n_heads, n_groups
 
 
 # ------------------------------------------------------------------ attention (hybrid layers)
+# The tensors of a call lie on one GPU, which need not be the current one.  With ``stream`` the call runs on
+# that stream, which the caller makes wait for its inputs; outputs made here come from that stream's memory
+# and may be used on the current stream once it waits for that one.
 _calls = None
 
 
@@ -612,13 +616,21 @@ def attn_rope_table(inv_freq, n_pos, scale=1.0, device="cuda", stream=None):
     lib = load()
     freqs = [float(f) for f in inv_freq]
     arr = (ctypes.c_double * max(1, len(freqs)))(*freqs)
-    cos = torch.empty(n_pos, len(freqs), device=device, dtype=torch.float32)
-    sin = torch.empty_like(cos)
-    _need_cuda(cos)
-    with torch.cuda.device(cos.device):         # the library works on the current device
-        rc = lib.attn_rope_table(n_pos, len(freqs), ctypes.cast(arr, ctypes.c_void_p), float(scale), _ptr(cos), _ptr(sin),
-                                 _stream(stream))
-    _check(lib, "attn_rope_table", rc)
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError("libssm takes CUDA tensors only (no CPU path)")
+    with torch.cuda.device(dev):                # the library works on the current device
+        current = torch.cuda.current_stream()
+        # the tables come from the memory of the stream that fills them
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            cos = torch.empty(n_pos, len(freqs), device=dev, dtype=torch.float32)
+            sin = torch.empty_like(cos)
+            rc = lib.attn_rope_table(n_pos, len(freqs), ctypes.cast(arr, ctypes.c_void_p), float(scale), _ptr(cos),
+                                     _ptr(sin), _stream(stream))
+        _check(lib, "attn_rope_table", rc)
+        if stream is not None:
+            cos.record_stream(current)
+            sin.record_stream(current)
     return cos, sin
 
 

@@ -45,15 +45,18 @@ const at::Tensor& cuda_tensor(PyObject* o, const char* name) {
 }
 bool given(PyObject* o) { return o != nullptr && o != Py_None; }
 
-// The one GPU that a call's tensors lie on, made current while the call allocates and launches: the
-// library works on the current device, whatever the pointers are.
 struct Arg {
     int at;
     const char* name;
 };
-class OnDevice {
+// Where a call works.  The one GPU that its tensors lie on is made current while it allocates and
+// launches: the library works on the current device, whatever the pointers are.  A caller's stream is
+// made current too: an output or workspace made here then comes from that stream's memory, and what is
+// written into it follows whatever still uses that memory there.  (Memory of another stream may be free to
+// be handed out on that stream and yet be in use: its last work there need not have run.)
+class Place {
 public:
-    OnDevice(PyObject* const* a, std::initializer_list<Arg> tensors) {
+    Place(PyObject* const* a, std::initializer_list<Arg> tensors, PyObject* stream) {
         for (const Arg& x : tensors) {
             PyObject* o = a[x.at];
             if (!given(o) || PyBool_Check(o) || !THPVariable_Check(o)) continue;
@@ -65,12 +68,36 @@ public:
                             std::to_string(index_));
             index_ = i;
         }
-        if (index_ >= 0) guard_.emplace(static_cast<c10::DeviceIndex>(index_));
+        if (index_ < 0) return;
+        device_.emplace(static_cast<c10::DeviceIndex>(index_));
+        before_ = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index_));
+        if (!given(stream)) return;
+        const unsigned long long raw = PyLong_AsUnsignedLongLong(stream);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            throw TypeProblem("stream must be a CUDA stream");
+        }
+        auto* handle = reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(raw));
+        if (handle != before_->stream())
+            stream_.emplace(c10::cuda::getStreamFromExternal(handle, static_cast<c10::DeviceIndex>(index_)));
+    }
+    void* stream() const { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index_)).stream(); }
+    // Memory of the call's stream.
+    at::Tensor scratch(at::IntArrayRef shape, at::ScalarType s, const at::Tensor& like) const {
+        return at::empty(shape, like.options().dtype(s).memory_format(c10::nullopt).requires_grad(false));
+    }
+    // An output: the caller goes on with it on the stream that was current, so that is noted as its user.
+    at::Tensor fresh(at::IntArrayRef shape, at::ScalarType s, const at::Tensor& like) const {
+        at::Tensor t = scratch(shape, s, like);
+        if (stream_ && t.numel() > 0) t.record_stream(before_->unwrap());
+        return t;
     }
 
 private:
     int index_ = -1;
-    std::optional<c10::cuda::CUDAGuard> guard_;
+    std::optional<c10::cuda::CUDAGuard> device_;
+    std::optional<c10::cuda::CUDAStream> before_;
+    std::optional<c10::cuda::CUDAStreamGuard> stream_;
 };
 
 // A [tokens, heads, dim] view.  A stride along an extent of one moves nothing, so it is given as a
@@ -128,21 +155,6 @@ at::ScalarType scalar_type(PyObject* o) {
     if (!THPDtype_Check(o)) throw TypeProblem("out_dtype must be a torch dtype");
     return reinterpret_cast<THPDtype*>(o)->scalar_type;
 }
-at::Tensor fresh(at::IntArrayRef shape, at::ScalarType s, const at::Tensor& like) {
-    return at::empty(shape, like.options().dtype(s).memory_format(c10::nullopt).requires_grad(false));
-}
-// The caller's stream, or torch's current one on t's device.
-void* stream_of(PyObject* o, const at::Tensor& t) {
-    if (given(o)) return reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(o)));
-    return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
-}
-// Memory made here belongs to the current stream; a caller's other stream is noted as its user, so that
-// it is not handed out again while the call still runs there.
-void used_on(PyObject* o, void* stream, const at::Tensor& t) {
-    if (given(o) && t.defined() && t.numel() > 0)
-        t.record_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), t.get_device()).unwrap());
-}
-
 struct Cache {
     ssm_dtype_t code;
     int n_pages, h, page, d;
@@ -193,16 +205,16 @@ Table table(PyObject* o, int64_t batch) {
 }
 
 // The attention output: given, shaped like q, or made.
-at::Tensor attn_out(PyObject* o, PyObject* dtype, const at::Tensor& q) {
-    if (!given(o)) return fresh(q.sizes(), scalar_type(dtype), q);
+at::Tensor attn_out(PyObject* o, PyObject* dtype, const at::Tensor& q, const Place& on) {
+    if (!given(o)) return on.fresh(q.sizes(), scalar_type(dtype), q);
     const at::Tensor& t = cuda_tensor(o, "out");
     if (t.sizes() != q.sizes()) value_error("out must be shaped like q");
     return t;
 }
 // The lse tensor to write: given, made for True, or none.
-at::Tensor attn_lse(PyObject* o, const at::Tensor& q) {
+at::Tensor attn_lse(PyObject* o, const at::Tensor& q, const Place& on) {
     if (!given(o) || o == Py_False) return at::Tensor();
-    if (o == Py_True) return fresh(q.sizes().slice(0, 2), at::kFloat, q);
+    if (o == Py_True) return on.fresh(q.sizes().slice(0, 2), at::kFloat, q);
     const at::Tensor& t = cuda_tensor(o, "lse");
     if (t.scalar_type() != at::kFloat || t.sizes() != q.sizes().slice(0, 2) || !t.is_contiguous())
         value_error("lse must be contiguous float32 [tokens, heads]");
@@ -229,8 +241,8 @@ PyObject* two(const at::Tensor& a, const at::Tensor& b) {
 
 // (q, k, v, positions, cos, sin, k_cache, v_cache, slots, k_scale, v_scale, interleaved, q_out, k_out, stream)
 PyObject* do_append(PyObject* const* a) {
-    const OnDevice on(a, {{1, "k"}, {0, "q"}, {2, "v"}, {3, "positions"}, {4, "cos"}, {5, "sin"}, {6, "k_cache"}, {7, "v_cache"},
-                          {8, "slots"}, {9, "k_scale"}, {10, "v_scale"}, {12, "q_out"}, {13, "k_out"}});
+    const Place on(a, {{1, "k"}, {0, "q"}, {2, "v"}, {3, "positions"}, {4, "cos"}, {5, "sin"}, {6, "k_cache"}, {7, "v_cache"},
+                          {8, "slots"}, {9, "k_scale"}, {10, "v_scale"}, {12, "q_out"}, {13, "k_out"}}, a[14]);
     const Cache c = cache(a[6], a[7], a[9], a[10]);
     const at::Tensor &k = cuda_tensor(a[1], "k"), &v = cuda_tensor(a[2], "v");
     need_type(k, at::kBFloat16, "k", "bfloat16");
@@ -262,7 +274,7 @@ PyObject* do_append(PyObject* const* a) {
             q_out = cuda_tensor(a[12], "q_out");
             if (q_out.scalar_type() != at::kBFloat16 || q_out.sizes() != q.sizes()) value_error("q_out must be shaped like q, bfloat16");
         } else {
-            q_out = fresh(q.sizes(), at::kBFloat16, q);
+            q_out = on.fresh(q.sizes(), at::kBFloat16, q);
         }
         qo = view(q_out, "q_out");
     } else if (given(a[12])) {
@@ -270,7 +282,7 @@ PyObject* do_append(PyObject* const* a) {
     }
     if (given(a[13]) && a[13] != Py_False) {
         if (a[13] == Py_True) {
-            k_out = fresh(k.sizes(), at::kBFloat16, k);
+            k_out = on.fresh(k.sizes(), at::kBFloat16, k);
         } else {
             k_out = cuda_tensor(a[13], "k_out");
             if (k_out.scalar_type() != at::kBFloat16 || k_out.sizes() != k.sizes()) value_error("k_out must be shaped like k, bfloat16");
@@ -278,19 +290,16 @@ PyObject* do_append(PyObject* const* a) {
         ko = view(k_out, "k_out");
     }
     const int inter = PyObject_IsTrue(a[11]);
-    void* stream = stream_of(a[14], k);
-    if (!given(a[12])) used_on(a[14], stream, q_out);
-    if (a[13] == Py_True) used_on(a[14], stream, k_out);
     const int rc = f_append(kv.n, as_int(qv.p || given(a[0]) ? qv.h : c.h, "heads"), c.h, c.d, as_int(2 * half, "rot_dim"), inter > 0,
                             qv.p, qv.st, qv.sh, kv.p, kv.st, kv.sh, vv.p, vv.st, vv.sh, positions, cp, sp, n_pos, slots,
-                            c.code, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, qo.p, qo.st, qo.sh, ko.p, ko.st, ko.sh, stream);
+                            c.code, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, qo.p, qo.st, qo.sh, ko.p, ko.st, ko.sh, on.stream());
     return rc ? PyLong_FromLong(rc) : two(q_out, k_out);
 }
 
 // (k_cache, v_cache, page_table, cu_len, n_tokens, k_scale, v_scale, first, k_out, v_out, out_dtype, stream)
 PyObject* do_read(PyObject* const* a) {
-    const OnDevice on(a, {{0, "k_cache"}, {1, "v_cache"}, {2, "page_table"}, {3, "cu_len"}, {5, "k_scale"}, {6, "v_scale"},
-                          {7, "first"}, {8, "k_out"}, {9, "v_out"}});
+    const Place on(a, {{0, "k_cache"}, {1, "v_cache"}, {2, "page_table"}, {3, "cu_len"}, {5, "k_scale"}, {6, "v_scale"},
+                          {7, "first"}, {8, "k_out"}, {9, "v_out"}}, a[11]);
     const Cache c = cache(a[0], a[1], a[5], a[6]);
     const at::Tensor& kc = THPVariable_Unpack(a[0]);
     const int64_t batch = cuda_tensor(a[3], "cu_len").numel() - 1, n = integer(a[4], "n_tokens");
@@ -299,16 +308,13 @@ PyObject* do_read(PyObject* const* a) {
     const int32_t* first = given(a[7]) ? int32s(a[7], batch, "first") : nullptr;
     const Table tb = table(a[2], batch);
     const int64_t shape[3] = {n, c.h, c.d};
-    at::Tensor k = given(a[8]) ? cuda_tensor(a[8], "k_out") : fresh(shape, scalar_type(a[10]), kc);
-    at::Tensor v = given(a[9]) ? cuda_tensor(a[9], "v_out") : fresh(shape, k.scalar_type(), kc);
+    at::Tensor k = given(a[8]) ? cuda_tensor(a[8], "k_out") : on.fresh(shape, scalar_type(a[10]), kc);
+    at::Tensor v = given(a[9]) ? cuda_tensor(a[9], "v_out") : on.fresh(shape, k.scalar_type(), kc);
     if (k.sizes() != at::IntArrayRef(shape, 3) || v.sizes() != k.sizes() || v.scalar_type() != k.scalar_type() ||
         !k.is_contiguous() || !v.is_contiguous())
         value_error("k_out and v_out must be contiguous [n_tokens, kv_heads, head_dim] of one dtype");
-    void* stream = stream_of(a[11], kc);
-    if (!given(a[8])) used_on(a[11], stream, k);
-    if (!given(a[9])) used_on(a[11], stream, v);
     const int rc = f_read(as_int(batch, "batch"), n, c.h, c.d, c.code, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, tb.p, tb.stride,
-                          tb.n, cu, first, out_code(k.scalar_type()), k.data_ptr(), v.data_ptr(), stream);
+                          tb.n, cu, first, out_code(k.scalar_type()), k.data_ptr(), v.data_ptr(), on.stream());
     return rc ? PyLong_FromLong(rc) : two(k, v);
 }
 
@@ -316,7 +322,7 @@ double scale_of(PyObject* o, int64_t d) { return given(o) ? number(o, "scale") :
 
 // (q, k, v, cu_q, cu_k, max_q, scale, out, out_dtype, lse, stream)
 PyObject* do_prefill(PyObject* const* a) {
-    const OnDevice on(a, {{0, "q"}, {1, "k"}, {2, "v"}, {3, "cu_q"}, {4, "cu_k"}, {7, "out"}, {9, "lse"}});
+    const Place on(a, {{0, "q"}, {1, "k"}, {2, "v"}, {3, "cu_q"}, {4, "cu_k"}, {7, "out"}, {9, "lse"}}, a[10]);
     const at::Tensor &q = cuda_tensor(a[0], "q"), &k = cuda_tensor(a[1], "k"), &v = cuda_tensor(a[2], "v");
     const View qv = view(q, "q"), kv = view(k, "k"), vv = view(v, "v");
     if (kv.d != qv.d || vv.d != qv.d || vv.h != kv.h || vv.n != kv.n)
@@ -324,23 +330,20 @@ PyObject* do_prefill(PyObject* const* a) {
     if (k.scalar_type() != q.scalar_type() || v.scalar_type() != q.scalar_type()) value_error("q, k and v must share one dtype");
     const int64_t batch = cuda_tensor(a[3], "cu_q").numel() - 1;
     const int32_t *cq = int32s(a[3], batch + 1, "cu_q"), *ck = int32s(a[4], batch + 1, "cu_k");
-    const at::Tensor out = attn_out(a[7], a[8], q), lse = attn_lse(a[9], q);
+    const at::Tensor out = attn_out(a[7], a[8], q, on), lse = attn_lse(a[9], q, on);
     const View ov = view(out, "out");
-    void* stream = stream_of(a[10], q);
-    if (!given(a[7])) used_on(a[10], stream, out);
-    if (a[9] == Py_True) used_on(a[10], stream, lse);
     const int rc = f_prefill(as_int(batch, "batch"), qv.n, kv.n, as_int(integer(a[5], "max_q"), "max_q"), as_int(qv.h, "heads"),
                              as_int(kv.h, "kv_heads"), as_int(qv.d, "head_dim"), out_code(q.scalar_type()),
                              out_code(out.scalar_type()), qv.p, qv.st, qv.sh, kv.p, kv.st, kv.sh, vv.p, vv.st, vv.sh, cq, ck,
                              (float)scale_of(a[6], qv.d), ov.p, ov.st, ov.sh,
-                             lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, stream);
+                             lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, on.stream());
     return rc ? PyLong_FromLong(rc) : two(out, lse);
 }
 
 // (q, k_cache, v_cache, page_table, lens, max_len, k_scale, v_scale, scale, out, out_dtype, lse, workspace, stream)
 PyObject* do_decode(PyObject* const* a) {
-    const OnDevice on(a, {{0, "q"}, {1, "k_cache"}, {2, "v_cache"}, {3, "page_table"}, {4, "lens"}, {6, "k_scale"},
-                          {7, "v_scale"}, {9, "out"}, {11, "lse"}, {12, "workspace"}});
+    const Place on(a, {{0, "q"}, {1, "k_cache"}, {2, "v_cache"}, {3, "page_table"}, {4, "lens"}, {6, "k_scale"},
+                          {7, "v_scale"}, {9, "out"}, {11, "lse"}, {12, "workspace"}}, a[13]);
     const Cache c = cache(a[1], a[2], a[6], a[7]);
     const at::Tensor& q = cuda_tensor(a[0], "q");
     const View qv = view(q, "q");
@@ -348,7 +351,7 @@ PyObject* do_decode(PyObject* const* a) {
     const int32_t* lens = int32s(a[4], qv.n, "lens");
     const int max_len = as_int(integer(a[5], "max_len"), "max_len"), batch = as_int(qv.n, "batch"), heads = as_int(qv.h, "heads");
     const Table tb = table(a[3], qv.n);
-    const at::Tensor out = attn_out(a[9], a[10], q), lse = attn_lse(a[11], q);
+    const at::Tensor out = attn_out(a[9], a[10], q, on), lse = attn_lse(a[11], q, on);
     const View ov = view(out, "out");
     at::Tensor ws;
     if (given(a[12])) {
@@ -356,17 +359,13 @@ PyObject* do_decode(PyObject* const* a) {
         if (!ws.is_contiguous()) value_error("workspace must be contiguous");
     } else {
         const size_t need = f_decode_bytes(batch, heads, c.h, c.d, max_len);
-        if (need) ws = fresh({(int64_t)need}, at::kByte, q);
+        if (need) ws = on.scratch({(int64_t)need}, at::kByte, q);
     }
-    void* stream = stream_of(a[13], q);
-    if (!given(a[9])) used_on(a[13], stream, out);
-    if (a[11] == Py_True) used_on(a[13], stream, lse);
-    if (!given(a[12])) used_on(a[13], stream, ws);
     const int rc = f_decode(batch, heads, c.h, c.d, out_code(q.scalar_type()), out_code(out.scalar_type()), qv.p, qv.st, qv.sh,
                             c.code, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, tb.p, tb.stride, tb.n, lens, max_len,
                             (float)scale_of(a[8], c.d), ov.p, ov.st, ov.sh,
                             lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
-                            ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.nbytes() : 0, stream);
+                            ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.nbytes() : 0, on.stream());
     return rc ? PyLong_FromLong(rc) : two(out, lse);
 }
 
