@@ -8,8 +8,9 @@ Output tensors are allocated with torch when the caller does not pass them.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
+import inspect
 from pathlib import Path
 
 import torch
@@ -133,6 +134,29 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on_stream(fn):
+    """A call given ``stream`` runs with that stream current, so that outputs and workspaces made in it come
+    from that stream's memory: a block of the current stream may be free there and still be used by work that
+    has not run, and would be free again, on return, before the call has run.  New outputs are noted as used
+    on the stream that was current, where the caller goes on with them."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        current = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            out = fn(*args, **kw)
+        given = {id(x) for x in (*args, *kw.values())}
+        for t in out if isinstance(out, tuple) else (out,):
+            if isinstance(t, torch.Tensor) and id(t) not in given:
+                t.record_stream(current)
+        return out
+    return call
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
@@ -180,6 +204,7 @@ def suggest_seg_len(batch: int, seqlen: int, d_inner: int, n_sm: int, ctas_per_s
     return ((seqlen + n_seg - 1) // n_seg + 63) // 64 * 64
 
 
+@_on_stream
 def prefill(x, z, dt, B, C, A, D, dt_bias, conv_w, conv_b, conv_state_in=None, ssm_state_in=None,
             out=None, out_dtype=torch.float32, conv_state_out=None, ssm_state_out=None, stream=None,
             seg_len=None, workspace=None, noalloc=False):
@@ -251,6 +276,7 @@ def prefill(x, z, dt, B, C, A, D, dt_bias, conv_w, conv_b, conv_state_in=None, s
     return out, conv_state_out, ssm_state_out
 
 
+@_on_stream
 def decode_step(x, z, dt, B, C, A, D, dt_bias, conv_w, conv_b, conv_state, ssm_state, state_slot=None,
                 out=None, out_dtype=torch.float32, stream=None):
     """ssm_decode_step: x/z/dt [batch, d_inner], B/C [batch, 16]; states updated in place.
@@ -291,6 +317,7 @@ def decode_step(x, z, dt, B, C, A, D, dt_bias, conv_w, conv_b, conv_state, ssm_s
     return out
 
 
+@_on_stream
 def decode_tokens(x, z, dt, B, C, A, D, dt_bias, conv_w, conv_b, conv_state, ssm_state, state_slot=None,
                   out=None, out_dtype=torch.float32, stream=None):
     """ssm_decode_tokens: x/z/dt [batch, T, d_inner] (channel-stride-1 views), B/C [batch, T, 16];
@@ -328,6 +355,7 @@ def decode_tokens(x, z, dt, B, C, A, D, dt_bias, conv_w, conv_b, conv_state, ssm
     return out
 
 
+@_on_stream
 def q8_reduce(partials, block=128, out=None, out_dtype=None, sums=None, scales=None, stream=None):
     """q8_reduce_partials over P equal-shaped partial tensors (flattened).
 
@@ -358,6 +386,7 @@ def q8_reduce(partials, block=128, out=None, out_dtype=None, sums=None, scales=N
     return out, sums, scales
 
 
+@_on_stream
 def q8_block_absmax(x, block=128, out=None, stream=None):
     """q8_block_absmax: per-128-block maxima of |x| (x flattened, contiguous) -> float32 [nblk]."""
     lib = load()
@@ -372,6 +401,7 @@ def q8_block_absmax(x, block=128, out=None, stream=None):
     return out
 
 
+@_on_stream
 def q8_quantize_shared(x, block_amax, block=128, codes=None, scales=None, stream=None):
     """q8_quantize_shared: int8 codes of x with the shared per-block maxima.
 
@@ -396,6 +426,7 @@ def q8_quantize_shared(x, block_amax, block=128, codes=None, scales=None, stream
     return codes, scales
 
 
+@_on_stream
 def q8_sum_dequant(codes, scales, block=128, out=None, out_dtype=torch.float32, sums=None, stream=None):
     """q8_sum_dequant over P equal-shaped int8 code tensors with their shared scales.
 
@@ -430,6 +461,7 @@ def device_status(clear: bool = True) -> int:
     return int(v.value)
 
 
+@_on_stream
 def out_proj_partial(y, W, out=None, out_dtype=torch.bfloat16, block_amax=True, stream=None):
     """ssm_out_proj_partial: y [M, K] bf16 and W [N, K] bf16 (row views with stride-1 K).
 
@@ -487,6 +519,7 @@ def _ssd_states(t, batch, H, Cx, name, conv):
         raise ValueError(f"{name} must be contiguous float32 {shape}")
 
 
+@_on_stream
 def ssd_prefill(xBC, z, dt, conv_w, conv_b, A, D, dt_bias, n_heads, n_groups, conv_state_in=None,
                 ssm_state_in=None, out=None, out_dtype=torch.float32, conv_state_out=None, ssm_state_out=None,
                 workspace=None, stream=None):
@@ -534,6 +567,7 @@ def ssd_prefill(xBC, z, dt, conv_w, conv_b, A, D, dt_bias, n_heads, n_groups, co
     return out, conv_state_out, ssm_state_out
 
 
+@_on_stream
 def ssd_decode_step(xBC, z, dt, conv_w, conv_b, A, D, dt_bias, n_heads, n_groups, conv_state, ssm_state,
                     state_slot=None, out=None, out_dtype=torch.float32, stream=None):
     """ssd_decode_step: xBC [batch, Cx], z [batch, 64 H], dt [batch, H] (contiguous); the cached
@@ -610,6 +644,7 @@ def _raw(stream):
     return None if stream is None else stream.cuda_stream
 
 
+@_on_stream
 def attn_rope_table(inv_freq, n_pos, scale=1.0, device="cuda", stream=None):
     """attn_rope_table: (cos, sin) float32 [n_pos, half] for positions 0 .. n_pos-1; ``inv_freq`` is a
     sequence of half floats (see rope.rope_frequencies)."""
@@ -620,17 +655,11 @@ def attn_rope_table(inv_freq, n_pos, scale=1.0, device="cuda", stream=None):
     if dev.type != "cuda":
         raise ValueError("libssm takes CUDA tensors only (no CPU path)")
     with torch.cuda.device(dev):                # the library works on the current device
-        current = torch.cuda.current_stream()
-        # the tables come from the memory of the stream that fills them
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            cos = torch.empty(n_pos, len(freqs), device=dev, dtype=torch.float32)
-            sin = torch.empty_like(cos)
-            rc = lib.attn_rope_table(n_pos, len(freqs), ctypes.cast(arr, ctypes.c_void_p), float(scale), _ptr(cos),
-                                     _ptr(sin), _stream(stream))
+        cos = torch.empty(n_pos, len(freqs), device=dev, dtype=torch.float32)
+        sin = torch.empty_like(cos)
+        rc = lib.attn_rope_table(n_pos, len(freqs), ctypes.cast(arr, ctypes.c_void_p), float(scale), _ptr(cos),
+                                 _ptr(sin), _stream(stream))
         _check(lib, "attn_rope_table", rc)
-        if stream is not None:
-            cos.record_stream(current)
-            sin.record_stream(current)
     return cos, sin
 
 
