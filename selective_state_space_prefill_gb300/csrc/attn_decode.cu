@@ -123,8 +123,10 @@ struct Ring {
     static constexpr int kLine = kRow < 128 ? kRow : 128;
     static constexpr int kRows = kUnit * kRow;          // bytes of 16 rows
     static constexpr int kStage = 2 * kRows + (I8 ? 128 : 0);
-    // so many that three or four CTAs share an SM with some 100 KB of copies in flight
-    static constexpr int kStages = kStage > 8000 ? 3 : (kStage > 4000 ? 3 : 4);
+    static constexpr int kStages = kStage > 4000 ? 3 : 4;
+    // CTAs that share an SM (up to 8 query heads): by its 227 KB of shared memory 4 with int8 rows of 128
+    // and with bf16 rows of 64, 2 with bf16 rows of 128, by its registers 4 with int8 rows of 64; 100 to 135
+    // KB of copies are then in flight.
     static constexpr int kPer = kLine / 16;             // chunks of a line
     // byte offset of 16-byte chunk c of row r
     static __device__ __forceinline__ uint32_t at(int r, int c) {
@@ -172,7 +174,7 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* p, float4 v, float l) {
 
 // DP: head_dim padded to 64 or 128.  NT: groups of 8 query heads a CTA serves.
 template <bool I8, int DP, int NT, bool kCluster, typename Tout>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? (I8 ? 4 : 3) : 2)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? (I8 ? 4 : DP == 64 ? 3 : 2) : 2)
 k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
     constexpr int kHeads = 8 * NT;
     constexpr int kSteps = DP / 16;                     // products over the head's dimensions
@@ -665,9 +667,12 @@ Cut cut_of(int batch, int n_q, int n_kv, int64_t max_len) {
         c.tokens = (int)(((max_len + p - 1) / p + 63) / 64 * 64);
         c.pieces = (int)((max_len + c.tokens - 1) / c.tokens);
     };
-    // A short call: at most eight pieces of 64 keys or more, all on the GPU at once and joined by their
-    // cluster without a second launch: one request of 1024 keys 12.9 -> 10.9 us, nine of 4096 31 -> 27.  A
-    // request or two of 4096 keys on 8 kv heads want more than 64 CTAs: there 17 us against 13.
+    // A short call: at most eight pieces of 64 keys or more, joined by their cluster without a second launch:
+    // one request of 1024 keys 12.9 -> 10.9 us, nine of 4096 31 -> 27.  A request or two of 4096 keys on 8 kv
+    // heads want more than 64 CTAs: there 17 us against 13.  608 CTAs are on the GPU at once with int8 rows (152
+    // SMs x 4).  The rule does not see the rows' type, and bf16 rows of 128 take two turns from 304 on: 8
+    // requests on 8 kv heads by clusters / by pieces and join: 512 keys 12.1 / 8.6 us, 1024 15.5 / 14.6, 2048 20.2 /
+    // 21.9, 4096 30 / 32 (int8: 8.8 / 9.0, 11.4 / 12.3, 14.9 / 18.9, 22 / 25).
     if (max_len > 64 && side * 8 <= 608 && (max_len <= 2048 || (max_len <= 4096 && side * 8 >= 152))) {
         const int64_t p = (max_len + 63) / 64;
         even(p < 8 ? p : 8);
@@ -676,8 +681,8 @@ Cut cut_of(int batch, int n_q, int n_kv, int64_t max_len) {
     }
     c.cluster = false;
     // Many CTAs of at least 512 keys, so that requests of different lengths fill the GPU evenly and the
-    // join reads little; where that leaves fewer than two per resident slot (152 SMs x 3), pieces
-    // down to 128 keys.
+    // join reads little; where that leaves fewer than 912 (1.5 turns of the 608 that are on the GPU at once
+    // with int8 rows, three of the 304 with bf16 rows of 128), pieces down to 128 keys.
     int64_t p = (3648 + side - 1) / side;
     const int64_t most = (max_len + 511) / 512;
     if (p > most) p = most;
