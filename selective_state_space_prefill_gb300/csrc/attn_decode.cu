@@ -474,7 +474,7 @@ k_attn_decode(const AttnDecodeArgs a, const Cut cut) {
                     pl[i][r] = 0u;
                 } else {
                     pb[i][r] = transpose8(high_parts(w0, w1));
-                    pl[i][r] = transpose8(pack_b(low_part(w0), low_part(w1)));
+                    pl[i][r] = transpose8(low_parts(w0, w1));
                 }
             }
         // ---- O^T += V^T P^T

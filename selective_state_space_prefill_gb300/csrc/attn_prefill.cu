@@ -330,7 +330,7 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     x1 = ex2(x1);
                     sum[i & 3] = add2(sum[i & 3], pair(x0, x1));
                     p[i] = kPair ? high_parts(x0, x1) : pack_bf16(x0, x1);
-                    if constexpr (kPair) p_lo[i] = pack_bf16(low_part(x0), low_part(x1));
+                    if constexpr (kPair) p_lo[i] = low_parts(x0, x1);
                 }
                 tmem_st32(ts + 32u * q, p);
                 if constexpr (kPair) tmem_st32(ts + 64u + 32u * q, p_lo);

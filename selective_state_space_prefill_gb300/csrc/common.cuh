@@ -43,17 +43,18 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
-// The low bf16 part of a softmax weight w >= 0 whose high part is w's upper 16 bits (cut off, not rounded).
-// Cut off, the rest is never negative, and it is raised to 2^-24 of w (half of w's own last place), or to
-// the smallest bf16, so that it is 0 only where w is: both parts are then multiplied by the same value, and
-// an infinite one stays infinite (0 x inf and inf - inf are NaN).  hi + lo is w to 16 bits.
-__device__ __forceinline__ float low_part(float w) {
-    const float hi = __uint_as_float(__float_as_uint(w) & 0xffff0000u);
-    return fmaxf(w - hi, fmaxf(hi * 0x1p-24f, fminf(hi, 0x1p-133f)));
-}
-// The upper 16 bits of two floats.
+// Two softmax weights >= 0 as bf16 pairs hi + lo (w0 in the lower half), w to 16 bits.  hi is w's upper 16
+// bits, cut off and not rounded, so that the rest is never negative; it is taken with 2^-24 of w more (half of
+// w's own last place), and the smallest bf16 at least, so that lo is 0 only where w is.  Both parts are
+// multiplied by the same value, and an infinite one stays infinite: 0 x inf and inf - inf would be NaN.
 __device__ __forceinline__ uint32_t high_parts(float w0, float w1) {
     return __byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632);
+}
+__device__ __forceinline__ uint32_t low_parts(float w0, float w1) {
+    const float h0 = __uint_as_float(__float_as_uint(w0) & 0xffff0000u), h1 = __uint_as_float(__float_as_uint(w1) & 0xffff0000u);
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(fmaf(h0, -0x0.ffffffp0f, w0), fmaf(h1, -0x0.ffffffp0f, w1));
+    // positive bf16 compare as integers
+    return __vmaxu2(*reinterpret_cast<const uint32_t*>(&lo), __vminu2(high_parts(w0, w1), 0x00010001u));
 }
 
 // softplus(v) = log(1 + e^v), with e = e^v from MUFU.EX2:
