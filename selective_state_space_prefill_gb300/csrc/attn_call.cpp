@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -60,17 +61,19 @@ public:
         for (const Arg& x : tensors) {
             PyObject* o = a[x.at];
             if (!given(o) || PyBool_Check(o) || !THPVariable_Check(o)) continue;
-            const at::Tensor& t = THPVariable_Unpack(o);
-            if (!t.is_cuda()) continue;                 // what has to be a CUDA tensor is seen to by name
-            const int i = t.get_device();
+            const c10::Device d = THPVariable_Unpack(o).device();
+            if (!d.is_cuda()) continue;                 // what has to be a CUDA tensor is seen to by name
+            const int i = d.index();
             if (index_ >= 0 && i != index_)
                 value_error(std::string(x.name) + " is on cuda:" + std::to_string(i) + ", other arguments on cuda:" +
                             std::to_string(index_));
             index_ = i;
         }
         if (index_ < 0) return;
-        device_.emplace(static_cast<c10::DeviceIndex>(index_));
-        before_ = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index_));
+        const auto index = static_cast<c10::DeviceIndex>(index_);
+        if (c10::cuda::device_count() > 1 && c10::cuda::current_device() != index) device_.emplace(index);
+        const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(index);
+        launch_ = current.stream();
         if (!given(stream)) return;
         const unsigned long long raw = PyLong_AsUnsignedLongLong(stream);
         if (PyErr_Occurred()) {
@@ -78,10 +81,12 @@ public:
             throw TypeProblem("stream must be a CUDA stream");
         }
         auto* handle = reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(raw));
-        if (handle != before_->stream())
-            stream_.emplace(c10::cuda::getStreamFromExternal(handle, static_cast<c10::DeviceIndex>(index_)));
+        if (handle == launch_) return;
+        launch_ = handle;
+        before_ = current.unwrap();
+        stream_.emplace(c10::cuda::getStreamFromExternal(handle, index));
     }
-    void* stream() const { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index_)).stream(); }
+    void* stream() const { return launch_; }
     // Memory of the call's stream.
     at::Tensor scratch(at::IntArrayRef shape, at::ScalarType s, const at::Tensor& like) const {
         return at::empty(shape, like.options().dtype(s).memory_format(c10::nullopt).requires_grad(false));
@@ -89,14 +94,15 @@ public:
     // An output: the caller goes on with it on the stream that was current, so that is noted as its user.
     at::Tensor fresh(at::IntArrayRef shape, at::ScalarType s, const at::Tensor& like) const {
         at::Tensor t = scratch(shape, s, like);
-        if (stream_ && t.numel() > 0) t.record_stream(before_->unwrap());
+        if (stream_ && t.numel() > 0) t.record_stream(*before_);
         return t;
     }
 
 private:
     int index_ = -1;
+    cudaStream_t launch_ = nullptr;
     std::optional<c10::cuda::CUDAGuard> device_;
-    std::optional<c10::cuda::CUDAStream> before_;
+    std::optional<c10::Stream> before_;
     std::optional<c10::cuda::CUDAStreamGuard> stream_;
 };
 
