@@ -152,6 +152,14 @@ double number(PyObject* o, const char* name) {
     }
     return v;
 }
+bool truth(PyObject* o, const char* name) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {
+        PyErr_Clear();
+        throw TypeProblem(std::string(name) + " must be a truth value");
+    }
+    return v != 0;
+}
 ssm_dtype_t out_code(at::ScalarType s) {
     if (s == at::kFloat) return SSM_F32;
     if (s == at::kBFloat16) return SSM_BF16;
@@ -249,6 +257,7 @@ PyObject* two(const at::Tensor& a, const at::Tensor& b) {
 PyObject* do_append(PyObject* const* a) {
     const Place on(a, {{1, "k"}, {0, "q"}, {2, "v"}, {3, "positions"}, {4, "cos"}, {5, "sin"}, {6, "k_cache"}, {7, "v_cache"},
                           {8, "slots"}, {9, "k_scale"}, {10, "v_scale"}, {12, "q_out"}, {13, "k_out"}}, a[14]);
+    const bool inter = truth(a[11], "interleaved");
     const Cache c = cache(a[6], a[7], a[9], a[10]);
     const at::Tensor &k = cuda_tensor(a[1], "k"), &v = cuda_tensor(a[2], "v");
     need_type(k, at::kBFloat16, "k", "bfloat16");
@@ -295,8 +304,7 @@ PyObject* do_append(PyObject* const* a) {
         }
         ko = view(k_out, "k_out");
     }
-    const int inter = PyObject_IsTrue(a[11]);
-    const int rc = f_append(kv.n, as_int(qv.p || given(a[0]) ? qv.h : c.h, "heads"), c.h, c.d, as_int(2 * half, "rot_dim"), inter > 0,
+    const int rc = f_append(kv.n, as_int(qv.p || given(a[0]) ? qv.h : c.h, "heads"), c.h, c.d, as_int(2 * half, "rot_dim"), inter,
                             qv.p, qv.st, qv.sh, kv.p, kv.st, kv.sh, vv.p, vv.st, vv.sh, positions, cp, sp, n_pos, slots,
                             c.code, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, qo.p, qo.st, qo.sh, ko.p, ko.st, ko.sh, on.stream());
     return rc ? PyLong_FromLong(rc) : two(q_out, k_out);
