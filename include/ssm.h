@@ -72,7 +72,9 @@ enum {
                                    table; that token or page was skipped, that length cut */
 };
 
-/* ABI version of this header (major * 100 + minor). */
+/* ABI version of this header (major * 100 + minor).  The attention calls (attn_*), SSM_I8 and
+ * SSM_DEV_BAD_INDEX came without a new number and changed no earlier call: a caller that has to work
+ * with a library of version 108 without them looks up the symbol attn_append. */
 int ssm_abi_version(void);
 
 /*

@@ -9,9 +9,9 @@
 //   k_attn_read         cache rows back to packed tokens
 //
 // All three are elementwise over rows: the bytes moved bound them (and launch latency, for a few
-// tokens).  Measured: 16384 tokens of 56 + 8 + 8 heads of 128 appended to an int8 cache in 108 us (5.6
-// TB/s); 124 K tokens of 8 heads of 128 read back from int8 to bf16 in 116 us (6.6 TB/s); a step's single
-// token 6 us a call, the launch and two or three dependent loads.
+// tokens).  Measured: 16384 tokens of 56 + 8 + 8 heads of 128 appended to an int8 cache and read back from it
+// in 125 us (5.7 TB/s); 124 K tokens of 8 heads of 128 read back from int8 to bf16 in 119 us (6.5 TB/s); a step's
+// single token 6 us a call, the launch and two or three dependent loads.
 #include <type_traits>
 
 #include "common.cuh"

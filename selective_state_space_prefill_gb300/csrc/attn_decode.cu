@@ -12,8 +12,9 @@
 //   * keys and values are the 16-row A operand of m16n8k16 tensor-core products and the (up to 8)
 //     query heads of the kv head their 8 columns: S^T = K q^T, O^T = V^T P^T (a tcgen05 tile of 128
 //     rows would be all but empty, and int8 rows would have to be widened in shared memory first; the
-//     tensor pipe is 14 % busy like this), the operands read as 8 x 8 matrices (the values' transposed).  The order of the reduction index is free, so two
-//     int8 dimensions travel as one 16-bit element;
+//     tensor pipe is 11 to 14 % busy like this), the operands read as 8 x 8 matrices (the values'
+//     transposed).  The order of the reduction index is free, so two int8 dimensions travel as one 16-bit
+//     element;
 //   * int8 codes become fp16 exactly, two at a time: code + 128 as the significand of 1024 + x for the
 //     values (1152 subtracted), as a subnormal, x 2^-24, for the keys, whose 128 is taken off the
 //     scores' starting value; the row scales multiply the scores after the first product and the
@@ -21,17 +22,19 @@
 //   * the long axis is cut into pieces, one CTA each; a second kernel joins the pieces' (m, l, o), or, for
 //     short calls, the cluster that the pieces form.
 //
-// Measured (CUDA events): 4 x 65536 tokens of 8 kv heads of 128, bf16: 175 us, 6.1 TB/s; the same in
-// int8 110 us, 5.0 TB/s, where the conversions take over half of the issue slots; 64 ragged requests up to
-// 8192 tokens, int8: 72 us a call, 4.6 TB/s; one of 4096 tokens 9.5 us a call.
+// Measured: 4 x 65536 tokens of 8 kv heads of 128, bf16: 168 us, 6.4 TB/s; the same in int8 112 us, 4.9 TB/s;
+// 64 ragged requests up to 8192 tokens, int8: 72 us a call, 4.6 TB/s; one of 4096 tokens 9.5 us a call.  With
+// int8 rows no unit is full (64 ragged requests: 0.60 instructions a cycle and scheduler, ALU pipe 59 %, DRAM
+// 64 %): some 14 warps an SM go through each unit's chain of conversions, products and softmax one after
+// the other, waiting for results and for the ALU more than for memory.
 //
 // Precision: scores, m, l and o are fp32.  With int8 rows the query is held in fp16 after scaling
 // by a power of two (exact for bf16 queries within 2^-25 of their head's maximum) and the weights
 // w_j = 2^(s_j - mw) scale_j in fp16 (11 bits; mw is a running reference of the exponent with the
 // scale in it, so that they fit whatever the rows' scales are; below 2^-20 of the largest they lose
-// bits, below 2^-31 they are zero, either way under 2^-31 of the largest each).  With bf16 rows the weights are a
-// bf16 pair hi + lo, both positive, so that an infinite value keeps its sign.  The references are raised only when a weight would pass them by more than 2^8,
-// so rescaling o is rare.
+// bits, below 2^-31 they are zero, either way under 2^-31 of the largest each).  With bf16 rows the
+// weights are a bf16 pair hi + lo, both positive, so that an infinite value keeps its sign.  The
+// references are raised only when a weight would pass them by more than 2^8, so rescaling o is rare.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 

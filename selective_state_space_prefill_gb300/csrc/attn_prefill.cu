@@ -7,8 +7,10 @@
 //   p_j = 2^(c (s_j - m)), c = scale log2(e);   l += sum p_j;   o += sum p_j v_j
 // out = o / l, lse = ln 2 (c m + log2 l).  Any m gives the same quotient; it is raised to the
 // running maximum only when that has grown by more than 2^8 (kSlack, in units of c s), so that p
-// stays below 2^8 and o is seldom rescaled.  p is rounded to bf16 for the second product, as the
-// tensor cores take it with bf16 values; l sums it unrounded.  For few rows p is a bf16 pair.
+// stays below 2^8 and o is seldom rescaled.  (The running softmax, the reference raised late, and two tiles in
+// turn with P kept in TMEM are published methods; the code is written from the formulas.)  p is rounded to
+// bf16 for the second product, as the tensor cores take it with bf16 values; l sums it unrounded.  For few
+// rows p is a bf16 pair.
 //
 // Two dense products per block bound it: 2 x 128 x 128 x D multiply-adds on the tensor cores and
 // 128 x 128 exponentials.  The design keeps the tensor cores fed while the exponentials run:
@@ -30,10 +32,12 @@
 // TMEM: scores of tile t at column 128 t, output at 256 + 128 t; all 512 columns, one CTA per SM.
 // The grid runs the longest rows first (the last tiles of every head and sequence), so the tail is short.
 //
-// Measured (CUDA events): 16384 tokens, 56 query and 8 kv heads of 128: 2.39 ms, 1611 TFLOP/s, 0.85 of
-// cuBLAS's bf16 rate; the products alone 2.2 ms, as Q K^T reads 128 bytes of shared memory a cycle, all
-// there is.  8 packed prompts of 260 to 4096 tokens, 32 / 8 heads: 197 us, half of it the starts and ends
-// of short CTAs.
+// Measured: 16384 tokens, 56 query and 8 kv heads of 128: 2.55 ms a call among hundreds, 1510 TFLOP/s, 0.80 of
+// cuBLAS's bf16 rate in a burst and 0.89 of its rate in a loop of seconds, under the power cap as these calls
+// are; 2.38 ms (CUDA events over a few calls with pauses), of which the products alone take 2.2, as Q K^T reads
+// 128 bytes of shared memory a cycle, all there is.  8 packed prompts of 266 to 4096 tokens, 32 / 8 heads: 194
+// us, half of it the starts and ends of short CTAs: the grid has 4096, for the longest prompt's tiles of every
+// sequence, of which 2752 find no rows.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -451,7 +455,14 @@ k_attn_prefill(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 if ((t ? n1 : n0) > 0 && !mbar_wait_bounded(&q_full[t], 0)) expired();
         } else if (warp == 9 && nb > 0) {
             // ---- MMA issuer: the whole warp walks the loop, so that descriptors stay in uniform registers
-            // (32 products a block leave 64 cycles for each), one elected lane issues
+            // (32 products a block leave 64 cycles for each), one elected lane issues.
+            // S_t(j + 1) is issued right behind O_t += P_t(j) V and overwrites the columns that hold P_t(j).  This
+            // relies on a CTA's products running in the order of their issue: the PTX manual promises that
+            // for products of one accumulator and shape, and these have two.  They do run in order: with a wait
+            // for O_t's commit in between every output has the same bits (8 shapes, heads of 64 to 128, whole,
+            // paired and split, 60 calls each), and a call takes 12 % longer (16384 tokens 2.56 -> 2.87 ms,
+            // 2 x 2048 rows over 14337 keys 1054 -> 1188 us, ragged prompts 194 -> 212 us).  TMEM has no columns
+            // for P beside 2 x 128 of scores and 2 x 128 of outputs.
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity))) {
