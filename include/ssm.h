@@ -51,7 +51,8 @@
 extern "C" {
 #endif
 
-/* SSM_I8 is a type of the attention cache only: int8 codes with one fp32 scale per row. */
+/* SSM_I8: int8 codes with fp32 scales, of the attention cache (a scale per row), and between norm_rms and
+ * w4_linear (a scale per row and group of channels). */
 typedef enum { SSM_F32 = 0, SSM_BF16 = 1, SSM_I8 = 2 } ssm_dtype_t;
 
 enum {
@@ -69,12 +70,14 @@ enum {
     SSM_DEV_BAD_SLOT = 2u,      /* a decode request named a state slot outside [0, n_slots) */
     SSM_DEV_SMEM_ALIGN = 4u,    /* shared memory was not 128-byte aligned; the prefill did nothing */
     SSM_DEV_BAD_INDEX = 8u      /* an attention call met a position, slot, page or length outside its
-                                   table; that token or page was skipped, that length cut */
+                                   table; that token or page was skipped, that length cut.  Likewise
+                                   a drafted token or a count of them in spec_verify */
 };
 
 /* ABI version of this header (major * 100 + minor).  The attention calls (attn_*), SSM_I8 and
- * SSM_DEV_BAD_INDEX came without a new number and changed no earlier call: a caller that has to work
- * with a library of version 108 without them looks up the symbol attn_append. */
+ * SSM_DEV_BAD_INDEX came without a new number and changed no earlier call, and so did the calls around the
+ * mixers of a decode step (norm_rms, w4_*, spec_*): a caller that has to work with a library of version 108
+ * without them looks up the symbols attn_append and norm_rms. */
 int ssm_abi_version(void);
 
 /*
@@ -602,6 +605,124 @@ int attn_decode_step(int batch, int n_q_heads, int n_kv_heads, int head_dim, ssm
                      const int32_t* page_table, int64_t table_stride, int n_table, const int32_t* lens,
                      int max_len, float scale, void* out, int64_t out_stride_t, int64_t out_stride_h,
                      float* lse, void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/*
+ * The calls around the mixers of a served model's decode step: the norm between blocks, projections with
+ * 4-bit weights, and the verification of drafted tokens (the blocks that ssm_decode_tokens runs).  The pages
+ * name the models (Overview: Mamba, Falcon-Mamba, Zamba) and their decoding with cached states (Methodology
+ * 3) but none of these steps; they follow the published layers and methods.
+ */
+
+/*
+ * norm_rms -- residual addition and root-mean-square norm over the row or over equal groups of its channels
+ * (the norm after an SSD mixer has groups).  With g = width / n_groups, for row t and the group of channel c:
+ *   r = x + residual (fp32; residual NULL: r = x);  residual_out = r, rounded to its type
+ *   y = r * (mean over the group of r^2, + eps)^(-1/2) * weight[c]      (weight NULL: 1), from the unrounded r
+ * out_dtype SSM_I8: a scale per row and group, the attention cache's rule: amax = max |y| over the group,
+ * scale = amax / 127, code = round_half_even(y * (127 / amax)) clamped to [-127, 127], IEEE fp32; amax == 0
+ * gives scale and codes 0, a NaN is ignored by amax and gets code 0, an infinite amax gives scale +inf and
+ * codes 0.  Squares are summed in fp32: |r| from 2^60 on can overflow the mean.
+ *
+ *   n_rows               >= 0 (0 does nothing); n_rows * n_groups < 2^31
+ *   width, n_groups      n_groups divides width; a group is a multiple of 8 channels, up to 32768
+ *   in_dtype, x          view [n_rows][width], SSM_BF16 or SSM_F32
+ *   res_dtype, residual  NULL or a view, SSM_BF16 or SSM_F32     residual_out: NULL or a view of res_dtype,
+ *                        may be residual itself with its stride
+ *   weight               NULL or [width] float32, 16-byte aligned       eps  finite, >= 0
+ *   out_dtype, out       view, SSM_BF16, SSM_F32 or SSM_I8       out_scale: [n_rows][n_groups] float32 for
+ *                        SSM_I8, else NULL
+ * Views are 16-byte aligned (an SSM_I8 out: 8), row strides are multiples of 8 elements and >= width.
+ */
+int norm_rms(int64_t n_rows, int width, int n_groups, ssm_dtype_t in_dtype, const void* x, int64_t x_stride,
+             ssm_dtype_t res_dtype, const void* residual, int64_t res_stride, void* residual_out, int64_t ro_stride,
+             const float* weight, float eps, ssm_dtype_t out_dtype, void* out, int64_t out_stride,
+             float* out_scale, void* cuda_stream);
+
+/*
+ * 4-bit weights.  A weight W [N][K] is held as codes 0 .. 15 with a scale, and possibly a zero, for each group
+ * of `group` consecutive elements of a row:
+ *   W[n][k] = (code[n][k] - zero[n][k / group]) * scale[n][k / group]         (zeros NULL: zero 8)
+ *   codes    [N][K / 2] bytes, element 2j in the low half of byte j, 2j + 1 in the high half; row stride ldc
+ *            bytes, a multiple of 16
+ *   scales   [N][K / group] SSM_BF16 or SSM_F32, row stride lds elements, a multiple of 16 bytes
+ *   zeros    NULL or [N][K / group] bytes 0 .. 15 (the low half counts), row stride ldz, a multiple of 16
+ * All 16-byte aligned; a row of scales or zeros is readable up to the next multiple of 16 bytes.  group is
+ * 32, 64 or 128, K a multiple of group up to 65536, N in 1 .. 2^27.
+ */
+
+/*
+ * w4_quantize -- codes and scales of W.  Without zeros: scale = amax / 7, code = 8 + round_half_even(w / scale)
+ * within 1 .. 15.  With zeros: lo = min(0, min w), hi = max(0, max w), scale = (hi - lo) / 15, zero =
+ * round_half_even(-lo / scale) and code = zero + round_half_even(w / scale), both within 0 .. 15.  The scale is
+ * rounded to its type first; a group whose scale is 0 gets zero 8 and codes 8.  Values must be finite.
+ *
+ *   in_dtype, W, ldw     [N][K] SSM_BF16 or SSM_F32, row stride ldw >= K, element aligned
+ */
+int w4_quantize(int64_t N, int64_t K, int group, ssm_dtype_t in_dtype, const void* W, int64_t ldw,
+                uint8_t* codes, int64_t ldc, ssm_dtype_t scale_dtype, void* scales, int64_t lds,
+                uint8_t* zeros, int64_t ldz, void* cuda_stream);
+
+/*
+ * w4_linear -- out[m][n] = sum_k x[m][k] W[n][k] with a 4-bit W, for the few rows of a decode step.  Products
+ * of x and (code - zero) are exact and are summed in fp32 within a group, the groups' sums times their scales
+ * in fp32, in an order that the sizes alone choose.
+ *
+ *   M                    >= 0 (0 does nothing), up to 2^20; made for up to about 64, more rows go through in
+ *                        turns of 32 that each unpack the weight again
+ *   x_dtype, x, ldx      [M][K] SSM_BF16 or SSM_I8; 16-byte aligned, row stride ldx >= K, a multiple of 16 bytes
+ *   x_scale, x_blocks    SSM_I8: [M][x_blocks] float32, a scale for each K / x_blocks consecutive elements of a
+ *                        row (a multiple of group); x_blocks up to 64.  SSM_BF16: NULL and 1
+ *   out_dtype, out, ldo  [M][N] SSM_BF16 or SSM_F32, row stride ldo >= N, element aligned
+ */
+int w4_linear(int64_t M, int64_t N, int64_t K, int group, ssm_dtype_t x_dtype, const void* x, int64_t ldx,
+              const float* x_scale, int x_blocks, const uint8_t* codes, int64_t ldc,
+              ssm_dtype_t scale_dtype, const void* scales, int64_t lds, const uint8_t* zeros, int64_t ldz,
+              ssm_dtype_t out_dtype, void* out, int64_t ldo, void* cuda_stream);
+
+/*
+ * spec_probs -- probabilities of logits: p[r][i] = exp(x_i / t) / sum_j exp(x_j / t) with t = temperature[r].
+ * A temperature of 2^-100 or less, negative ones included, is greedy: 1 at the first largest logit, 0 elsewhere.
+ * A logit of -inf has probability 0; a row whose logits are all -inf gives zeros.  A NaN or +inf among a row's
+ * logits, or a NaN temperature, gives a row of NaN.  A temperature of +inf counts as the largest finite one.
+ *
+ *   n_rows, vocab        n_rows >= 0 (0 does nothing) < 2^28; vocab 1 .. 2^24
+ *   in_dtype, logits     [n_rows][vocab] SSM_BF16 or SSM_F32, row stride ld_in >= vocab, element aligned
+ *   temperature          NULL (1) or [n_rows] float32
+ *   probs                [n_rows][vocab] float32, row stride ld_out >= vocab, element aligned
+ */
+int spec_probs(int64_t n_rows, int64_t vocab, ssm_dtype_t in_dtype, const void* logits, int64_t ld_in,
+               const float* temperature, float* probs, int64_t ld_out, void* cuda_stream);
+
+/*
+ * spec_verify -- how many of a request's drafted tokens are kept, and the token after them.  Request b has
+ * n = n_draft[b] drafted tokens d_0 .. d_{n-1}, the target's probabilities p_0 .. p_n at their places and after
+ * them, the drafts' probabilities q_0 .. q_{n-1} that they were drawn with, and uniform numbers u.  Token i is
+ * kept while u_i q_i(d_i) < p_i(d_i).  If token a is the first not kept, the next token is drawn from
+ * max(p_a - q_a, 0) (from p_a, if that is 0 everywhere); if all n are kept, from p_n.  Tokens so chosen have the
+ * target's distribution.  With draft_probs NULL the drafts were certain: q_i is 1 at d_i and 0 elsewhere.
+ *   drawn from w at v = u[b][n_max]: the smallest index whose running sum of w exceeds v * (sum of w)
+ * Running sums are taken in integers of 2^-62 (exact for values from 2^-38 on), so the token depends on nothing
+ * but the values.
+ *
+ *   batch, n_max         batch >= 0 (0 does nothing) up to 65535; 0 .. 1024 drafted tokens a request, the bound
+ *                        of n_draft.  n_max = 0 draws a token from p_0.
+ *   vocab                1 .. 2^24
+ *   draft                [batch][n_max] int32.  A token outside the vocabulary counts as one of probability 0
+ *                        and sets SSM_DEV_BAD_INDEX when it is looked at.
+ *   n_draft              NULL (n_max) or [batch] int32; one outside [0, n_max] is cut and sets SSM_DEV_BAD_INDEX
+ *   target_probs         [batch][n_max + 1][vocab] float32 view: element (b, i, v) at b*tp_stride_b +
+ *                        i*tp_stride_t + v, element aligned
+ *   draft_probs          NULL or such a view [batch][n_max][vocab]
+ *   u                    [batch][n_max + 1] float32 in [0, 1); below 0 or NaN counts as 0, 1 and more as 1 - 2^-24
+ *   tokens               [batch][n_max + 1] int32: the kept tokens, the next one, then -1
+ *   n_kept               [batch] int32
+ * Probabilities are >= 0 and sum up to about 1: a negative one or a NaN counts as 0, and a row that is drawn from
+ * and sums up to 0 or to 4 or more gives token -1.
+ */
+int spec_verify(int batch, int n_max, int64_t vocab, const int32_t* draft, const int32_t* n_draft,
+                const float* target_probs, int64_t tp_stride_b, int64_t tp_stride_t,
+                const float* draft_probs, int64_t dp_stride_b, int64_t dp_stride_t, const float* u,
+                int32_t* tokens, int32_t* n_kept, void* cuda_stream);
 
 /*
  * ssm_selftest_expire_wait -- a diagnostic with no counterpart in the pages: launches one

@@ -15,7 +15,7 @@ from pathlib import Path
 
 import torch
 
-from .build import CALLS, LIB
+from .build import CALLS, LIB, STEP_CALLS
 
 SSM_F32, SSM_BF16, SSM_I8 = 0, 1, 2
 _STATUS = {0: "SSM_OK", -1: "SSM_ERR_INVALID_ARG", -2: "SSM_ERR_UNSUPPORTED", -3: "SSM_ERR_MISALIGNED",
@@ -27,7 +27,7 @@ EXPORTS = ("ssm_abi_version", "ssm_prefill", "ssm_prefill_workspace_bytes", "ssm
            "q8_reduce_partials", "q8_block_absmax", "q8_quantize_shared", "q8_sum_dequant",
            "ssd_prefill_workspace_bytes", "ssd_prefill", "ssd_decode_step",
            "attn_rope_table", "attn_append", "attn_cache_read", "attn_prefill", "attn_decode_workspace_bytes",
-           "attn_decode_step",
+           "attn_decode_step", "norm_rms", "w4_quantize", "w4_linear", "spec_probs", "spec_verify",
            "ssm_selftest_expire_wait", "ssm_device_status", "ssm_last_error")
 NOALLOC_SCRATCH_BYTES = 4 << 20     # SSM_NOALLOC_SCRATCH_BYTES
 
@@ -103,6 +103,16 @@ def load(path: Path | str | None = None):
     lib.attn_decode_step.argtypes = [I, I, I, I, I, I, P, L, L, I, P, P, P, P, I, I, P, L, I, P, I, F, P, L, L,
                                      P, P, Z, P]
     lib.attn_decode_step.restype = I
+    lib.norm_rms.argtypes = [L, I, I, I, P, L, I, P, L, P, L, P, F, I, P, L, P, P]
+    lib.norm_rms.restype = I
+    lib.w4_quantize.argtypes = [L, L, I, I, P, L, P, L, I, P, L, P, L, P]
+    lib.w4_quantize.restype = I
+    lib.w4_linear.argtypes = [L, L, L, I, I, P, L, P, I, P, L, I, P, L, P, L, I, P, L, P]
+    lib.w4_linear.restype = I
+    lib.spec_probs.argtypes = [L, L, I, P, L, P, P, L, P]
+    lib.spec_probs.restype = I
+    lib.spec_verify.argtypes = [I, I, L, P, P, P, L, L, P, L, L, P, P, P, P]
+    lib.spec_verify.restype = I
     lib.ssm_selftest_expire_wait.argtypes = [I, P]
     lib.ssm_selftest_expire_wait.restype = I
     lib.ssm_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), I]
@@ -611,30 +621,34 @@ def ssd_decode_step(xBC, z, dt, conv_w, conv_b, A, D, dt_bias, n_heads, n_groups
 _calls = None
 
 
+def _extension(path, entries):
+    """An extension of the build that marshals calls, with libssm's entry points handed over."""
+    import importlib.machinery
+    import importlib.util
+
+    if not path.exists():
+        raise ImportError(f"{path.stem} is not built ({path} missing): run "
+                          "`python -c 'import __graft_entry__ as g; g.build()'` first")
+    loader = importlib.machinery.ExtensionFileLoader(path.stem, str(path))
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader(path.stem, loader))
+    loader.exec_module(mod)
+    lib = load()
+    mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in entries))
+    return mod
+
+
 def attn_calls():
     """The extension that marshals the attention calls (csrc/attn_call.cpp): it checks the tensors,
     allocates missing outputs and calls libssm, in the microsecond that a short step allows."""
     global _calls
     if _calls is None:
-        import importlib.machinery
-        import importlib.util
-
-        if not CALLS.exists():
-            raise ImportError(f"the attention calls are not built ({CALLS} missing): run "
-                              "`python -c 'import __graft_entry__ as g; g.build()'` first")
-        loader = importlib.machinery.ExtensionFileLoader("_attn_call", str(CALLS))
-        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_attn_call", loader))
-        loader.exec_module(mod)
-        lib = load()
-        mod.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.attn_append, lib.attn_cache_read, lib.attn_prefill, lib.attn_decode_workspace_bytes,
-            lib.attn_decode_step)))
-        _calls = mod
+        _calls = _extension(CALLS, ("attn_append", "attn_cache_read", "attn_prefill", "attn_decode_workspace_bytes",
+                                    "attn_decode_step"))
     return _calls
 
 
 def _outcome(r, fn):
-    """What an attention call returned: its outputs, or the status of its refusal."""
+    """What an extension's call returned: its outputs, or the status of its refusal."""
     if type(r) is int:
         raise SSMError(fn, r, load().ssm_last_error().decode())
     return r
@@ -709,3 +723,63 @@ def attn_decode_step(q, k_cache, v_cache, page_table, lens, max_len, k_scale=Non
     here with torch when not given.  Returns (out, lse)."""
     return _outcome((_calls or attn_calls()).decode(q, k_cache, v_cache, page_table, lens, max_len, k_scale, v_scale, scale,
                                                     out, out_dtype, lse, workspace, _raw(stream)), "attn_decode_step")
+
+
+# ------------------------------------------------------------------ around the mixers of a decode step
+# The norm between blocks, projections with 4-bit weights, and the verification of drafted tokens.  Devices and
+# streams are as for the attention calls.
+_steps = None
+
+
+def step_calls():
+    """The extension that marshals these calls (csrc/step_call.cpp)."""
+    global _steps
+    if _steps is None:
+        _steps = _extension(STEP_CALLS, ("norm_rms", "w4_quantize", "w4_linear", "spec_probs", "spec_verify"))
+    return _steps
+
+
+def norm_rms(x, weight=None, residual=None, eps=1e-5, n_groups=1, out=None, out_dtype=torch.bfloat16, residual_out=None,
+             out_scale=None, stream=None):
+    """norm_rms: r = x + residual, and r / sqrt(mean(r^2) + eps) * weight over the row or over ``n_groups`` equal
+    groups of its channels.
+
+    x [rows, width] bfloat16 or float32; weight [width] float32; residual like x, bfloat16 or float32.
+    ``residual_out`` takes r in residual's dtype: allocated when not given, residual itself for in place, False to
+    skip it.  ``out_dtype`` bfloat16, float32, or int8 with a scale per row and group (out_scale [rows, n_groups]
+    float32), which is what w4_linear takes as x and x_scale.  Returns (out, residual_out, out_scale), None for
+    what there is not."""
+    return _outcome((_steps or step_calls()).norm(x, weight, residual, eps, n_groups, out, out_dtype, residual_out, out_scale,
+                                                  _raw(stream)), "norm_rms")
+
+
+def w4_quantize(W, group=128, zeros=False, scale_dtype=torch.bfloat16, stream=None):
+    """w4_quantize: W [N, K] (bfloat16 or float32) to 4 bits, ``group`` (32, 64 or 128) elements of a row sharing a
+    scale and, with ``zeros``, a zero.  Returns (codes [N, K / 2] uint8, even elements in the low half; scales
+    [N, K / group] bfloat16 or float32; zeros [N, K / group] uint8 or None), rows padded to 16 bytes."""
+    return _outcome((_steps or step_calls()).quantize(W, group, zeros, scale_dtype, _raw(stream)), "w4_quantize")
+
+
+def w4_linear(x, codes, scales, zeros=None, x_scale=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """w4_linear: x [M, K] times the transpose of a 4-bit weight (w4_quantize's layout), for the few rows of a
+    decode step.  x is bfloat16, or int8 with x_scale [M] or [M, blocks] float32 (norm_rms's).  ``zeros`` None
+    stands for 8.  Returns out [M, N] (bfloat16 or float32)."""
+    return _outcome((_steps or step_calls()).linear(x, codes, scales, zeros, x_scale, out, out_dtype, _raw(stream)), "w4_linear")[0]
+
+
+def spec_probs(logits, temperature=None, out=None, stream=None):
+    """spec_probs: probabilities [rows, vocab] float32 of logits [rows, vocab] (bfloat16 or float32) at the rows'
+    temperatures [rows] float32 (None: 1; 0: greedy, the first largest logit)."""
+    return _outcome((_steps or step_calls()).probs(logits, temperature, out, _raw(stream)), "spec_probs")[0]
+
+
+def spec_verify(draft, target_probs, u, draft_probs=None, n_draft=None, tokens=None, n_kept=None, stream=None):
+    """spec_verify: drafted tokens against the target's probabilities.
+
+    draft [batch, n] int32; target_probs [batch, n + 1, vocab] float32, at the drafted places and after them; u
+    [batch, n + 1] float32, uniform in [0, 1); draft_probs [batch, n, vocab] float32 that the drafts were drawn
+    with (None: they were certain); n_draft [batch] int32, how many of the n a request has (None: all).  n may be
+    0: a token is drawn from target_probs.  Returns (tokens [batch, n + 1] int32: the kept drafts, the next token,
+    then -1; n_kept [batch] int32)."""
+    return _outcome((_steps or step_calls()).verify(draft, target_probs, u, draft_probs, n_draft, tokens, n_kept, _raw(stream)),
+                    "spec_verify")

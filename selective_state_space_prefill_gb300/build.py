@@ -100,13 +100,15 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     return LIB
 
 
-# ------------------------------------------------------------------ the attention calls' marshalling
+# ------------------------------------------------------------------ the marshalling of short calls
+# Python extensions: the attention calls, and the calls around the mixers of a decode step.
 CALLS_SRC = "attn_call.cpp"
 CALLS = BUILD / "_attn_call.so"
-CALLS_STAMP = BUILD / "_attn_call.sha256"
+STEP_CALLS_SRC = "step_call.cpp"
+STEP_CALLS = BUILD / "_step_call.so"
 
 
-def _calls_command(out: Path) -> list[str]:
+def _calls_command(src: str, out: Path) -> list[str]:
     """One g++ run against the torch and Python of this interpreter."""
     import sysconfig
 
@@ -118,39 +120,49 @@ def _calls_command(out: Path) -> list[str]:
             "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             "-I", str(INCLUDE), "-I", sysconfig.get_paths()["include"], "-I", str(root / "include"),
             "-I", str(root / "include/torch/csrc/api/include"), "-I", str(cuda / "include"),
-            str(CSRC / CALLS_SRC), "-o", str(out), "-L", str(root / "lib"), f"-Wl,-rpath,{root / 'lib'}",
+            str(CSRC / src), "-o", str(out), "-L", str(root / "lib"), f"-Wl,-rpath,{root / 'lib'}",
             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
-def build_calls(force: bool = False) -> Path:
-    """Compile the Python extension that marshals the attention calls; returns its path.
-
-    Reused only when its stamp holds the digest of its source, the ABI header, the command, and the
-    versions of Python and torch that it was compiled against."""
+def _build_extension(src: str, out: Path, force: bool) -> Path:
+    """Compile one extension.  Reused only when its stamp holds the digest of its source, the headers, the
+    command, and the versions of Python and torch that it was compiled against."""
     import sys
 
     import torch
 
     h = hashlib.sha256()
-    for p in (CSRC / CALLS_SRC, INCLUDE / "ssm.h"):
+    for p in (CSRC / src, CSRC / "call.h", INCLUDE / "ssm.h"):
         h.update(p.name.encode() + b"\0" + p.read_bytes() + b"\0")
-    h.update(" ".join(_calls_command(CALLS)).encode())
+    h.update(" ".join(_calls_command(src, out)).encode())
     h.update(f"{sys.version} {torch.__version__}".encode())
     digest = h.hexdigest()
-    if not force and CALLS.exists() and CALLS_STAMP.exists() and CALLS_STAMP.read_text().strip() == digest:
-        return CALLS
+    stamp = out.with_suffix(".sha256")
+    if not force and out.exists() and stamp.exists() and stamp.read_text().strip() == digest:
+        return out
     BUILD.mkdir(parents=True, exist_ok=True)
-    tmp = BUILD / f"_attn_call.{os.getpid()}.tmp"
-    r = subprocess.run(_calls_command(tmp), capture_output=True, text=True)
+    tmp = BUILD / f"{out.stem}.{os.getpid()}.tmp"
+    r = subprocess.run(_calls_command(src, tmp), capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
-    stamp_tmp = BUILD / f"_attn_call.sha256.{os.getpid()}.tmp"
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    stamp_tmp = BUILD / f"{out.stem}.sha256.{os.getpid()}.tmp"
     stamp_tmp.write_text(digest + "\n")
-    os.replace(stamp_tmp, CALLS_STAMP)
-    return CALLS
+    os.replace(stamp_tmp, stamp)
+    return out
+
+
+def build_calls(force: bool = False) -> Path:
+    """Compile the extension that marshals the attention calls; returns its path."""
+    return _build_extension(CALLS_SRC, CALLS, force)
+
+
+def build_step_calls(force: bool = False) -> Path:
+    """Compile the extension that marshals the calls around a decode step's mixers; returns its path."""
+    return _build_extension(STEP_CALLS_SRC, STEP_CALLS, force)
 
 
 if __name__ == "__main__":
     print(build(force=True, verbose=True))
     print(build_calls(force=True))
+    print(build_step_calls(force=True))

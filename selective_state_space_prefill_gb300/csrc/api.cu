@@ -1050,3 +1050,209 @@ int attn_decode_step(int batch, int n_q_heads, int n_kv_heads, int head_dim, ssm
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------ around the mixers of a decode step
+namespace {
+
+// Rows of a 2-D view that is read or written eight elements at a time.
+int check_rows(const char* fn, const char* name, const void* p, int64_t stride, int64_t width, unsigned align) {
+    if (!p) return fail(SSM_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+    if (stride < width) return fail(SSM_ERR_INVALID_ARG, "%s: the row stride of %s is below the row", fn, name);
+    if (!aligned(p, align) || stride % 8 != 0)
+        return fail(SSM_ERR_MISALIGNED, "%s: %s must be %u-byte aligned with a row stride that is a multiple of 8", fn, name, align);
+    return SSM_OK;
+}
+
+int check_w4(const char* fn, int64_t N, int64_t K, int group, const void* codes, int64_t ldc, int scale_dtype,
+             const void* scales, int64_t lds, const void* zeros, int64_t ldz) {
+    if (N < 1 || N > (1LL << 27)) return fail(SSM_ERR_INVALID_ARG, "%s: N %lld not in [1, 2^27]", fn, (long long)N);
+    if (group != 32 && group != 64 && group != 128)
+        return fail(SSM_ERR_UNSUPPORTED, "%s: group %d unsupported (32, 64 or 128)", fn, group);
+    if (K < 1 || K % group != 0) return fail(SSM_ERR_INVALID_ARG, "%s: K %lld is not a multiple of the group %d", fn, (long long)K, group);
+    if (K > 65536) return fail(SSM_ERR_UNSUPPORTED, "%s: K %lld above 65536", fn, (long long)K);
+    if (!dtype_ok(scale_dtype)) return fail(SSM_ERR_INVALID_ARG, "%s: unknown scale dtype", fn);
+    if (!codes || !scales) return fail(SSM_ERR_INVALID_ARG, "%s: codes or scales is NULL", fn);
+    if (ldc < K / 2 || lds < K / group || (zeros && ldz < K / group))
+        return fail(SSM_ERR_INVALID_ARG, "%s: a row stride of the weight is below the row length", fn);
+    if (!aligned(codes, 16) || ldc % 16 != 0 || !aligned(scales, 16) || lds * esize(scale_dtype) % 16 != 0 ||
+        (zeros && (!aligned(zeros, 16) || ldz % 16 != 0)))
+        return fail(SSM_ERR_MISALIGNED, "%s: rows of codes, scales and zeros must start on 16 bytes", fn);
+    return SSM_OK;
+}
+
+ssm::W4Weight make_w4(int64_t N, int64_t K, int group, const uint8_t* codes, int64_t ldc, int scale_dtype, const void* scales,
+                      int64_t lds, const uint8_t* zeros, int64_t ldz) {
+    return ssm::W4Weight{(int)N, (int)K, group, codes, zeros, scales, scale_dtype == SSM_BF16, ldc, lds, ldz};
+}
+
+}  // namespace
+
+extern "C" {
+
+int norm_rms(int64_t n_rows, int width, int n_groups, ssm_dtype_t in_dtype, const void* x, int64_t x_stride,
+             ssm_dtype_t res_dtype, const void* residual, int64_t res_stride, void* residual_out, int64_t ro_stride,
+             const float* weight, float eps, ssm_dtype_t out_dtype, void* out, int64_t out_stride,
+             float* out_scale, void* cuda_stream) {
+    static const char* fn = "norm_rms";
+    g_err[0] = 0;
+    int rc;
+    if (n_rows < 0) return fail(SSM_ERR_INVALID_ARG, "%s: n_rows %lld < 0", fn, (long long)n_rows);
+    if (width < 1 || n_groups < 1 || width % n_groups != 0)
+        return fail(SSM_ERR_INVALID_ARG, "%s: %d channels in %d groups", fn, width, n_groups);
+    if (width / n_groups % 8 != 0 || width / n_groups > 32768)
+        return fail(SSM_ERR_UNSUPPORTED, "%s: a group of %d channels (multiples of 8 up to 32768)", fn, width / n_groups);
+    if (n_rows >= (1LL << 31) / n_groups)
+        return fail(SSM_ERR_UNSUPPORTED, "%s: %lld rows of %d groups pass 2^31", fn, (long long)n_rows, n_groups);
+    if (!dtype_ok(in_dtype) || ((residual || residual_out) && !dtype_ok(res_dtype)) || !(dtype_ok(out_dtype) || out_dtype == SSM_I8))
+        return fail(SSM_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+    if (!(eps >= 0.0f) || !(eps - eps == 0.0f)) return fail(SSM_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+    if (residual_out && !residual) return fail(SSM_ERR_INVALID_ARG, "%s: residual_out needs residual", fn);
+    if (n_rows == 0) return SSM_OK;
+    if ((rc = check_rows(fn, "x", x, x_stride, width, 16)) != SSM_OK) return rc;
+    if (residual && (rc = check_rows(fn, "residual", residual, res_stride, width, 16)) != SSM_OK) return rc;
+    if (residual_out && (rc = check_rows(fn, "residual_out", residual_out, ro_stride, width, 16)) != SSM_OK) return rc;
+    if (residual_out == residual && residual && ro_stride != res_stride)
+        return fail(SSM_ERR_INVALID_ARG, "%s: residual_out is residual with another stride", fn);
+    if ((rc = check_rows(fn, "out", out, out_stride, width, out_dtype == SSM_I8 ? 8 : 16)) != SSM_OK) return rc;
+    if ((out_dtype == SSM_I8) != (out_scale != nullptr))
+        return fail(SSM_ERR_INVALID_ARG, "%s: out_scale goes with an SSM_I8 out", fn);
+    if ((weight && !aligned(weight, 16)) || (out_scale && !aligned(out_scale, 4)))
+        return fail(SSM_ERR_MISALIGNED, "%s: weight must be 16-byte aligned, out_scale element aligned", fn);
+    int serr = 0;
+    status_ptr(&serr);
+    if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
+    ssm::NormArgs a{};
+    a.n_rows = n_rows;
+    a.width = width;
+    a.n_groups = n_groups;
+    a.in_type = in_dtype;
+    a.res_type = residual ? res_dtype : SSM_BF16;
+    a.out_type = out_dtype;
+    a.x = x;
+    a.residual = residual;
+    a.residual_out = residual_out;
+    a.out = out;
+    a.x_st = x_stride;
+    a.res_st = res_stride;
+    a.ro_st = ro_stride;
+    a.out_st = out_stride;
+    a.weight = weight;
+    a.eps = eps;
+    a.out_scale = out_scale;
+    const char* why = "";
+    if (ssm::launch_norm_rms(a, static_cast<cudaStream_t>(cuda_stream), &why) != 0) return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
+    return SSM_OK;
+}
+
+int w4_quantize(int64_t N, int64_t K, int group, ssm_dtype_t in_dtype, const void* W, int64_t ldw,
+                uint8_t* codes, int64_t ldc, ssm_dtype_t scale_dtype, void* scales, int64_t lds,
+                uint8_t* zeros, int64_t ldz, void* cuda_stream) {
+    static const char* fn = "w4_quantize";
+    g_err[0] = 0;
+    const int rc = check_w4(fn, N, K, group, codes, ldc, scale_dtype, scales, lds, zeros, ldz);
+    if (rc != SSM_OK) return rc;
+    if (!dtype_ok(in_dtype)) return fail(SSM_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+    if (!W) return fail(SSM_ERR_INVALID_ARG, "%s: W is NULL", fn);
+    if (ldw < K) return fail(SSM_ERR_INVALID_ARG, "%s: ldw is below K", fn);
+    if (!aligned(W, esize(in_dtype))) return fail(SSM_ERR_MISALIGNED, "%s: W is not element aligned", fn);
+    int serr = 0;
+    status_ptr(&serr);
+    if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
+    const char* why = "";
+    if (ssm::launch_w4_quantize(make_w4(N, K, group, codes, ldc, scale_dtype, scales, lds, zeros, ldz), W, ldw,
+                                in_dtype == SSM_BF16, static_cast<cudaStream_t>(cuda_stream), &why) != 0)
+        return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
+    return SSM_OK;
+}
+
+int w4_linear(int64_t M, int64_t N, int64_t K, int group, ssm_dtype_t x_dtype, const void* x, int64_t ldx,
+              const float* x_scale, int x_blocks, const uint8_t* codes, int64_t ldc,
+              ssm_dtype_t scale_dtype, const void* scales, int64_t lds, const uint8_t* zeros, int64_t ldz,
+              ssm_dtype_t out_dtype, void* out, int64_t ldo, void* cuda_stream) {
+    static const char* fn = "w4_linear";
+    g_err[0] = 0;
+    if (M < 0 || M > (1LL << 20)) return fail(SSM_ERR_INVALID_ARG, "%s: M %lld not in [0, 2^20]", fn, (long long)M);
+    const int rc = check_w4(fn, N, K, group, codes, ldc, scale_dtype, scales, lds, zeros, ldz);
+    if (rc != SSM_OK) return rc;
+    if (x_dtype != SSM_BF16 && x_dtype != SSM_I8)
+        return fail(x_dtype == SSM_F32 ? SSM_ERR_UNSUPPORTED : SSM_ERR_INVALID_ARG, "%s: x must be SSM_BF16 or SSM_I8", fn);
+    if (!dtype_ok(out_dtype)) return fail(SSM_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+    if (M == 0) return SSM_OK;
+    if (!x || !out) return fail(SSM_ERR_INVALID_ARG, "%s: x or out is NULL", fn);
+    if (ldx < K || ldo < N) return fail(SSM_ERR_INVALID_ARG, "%s: a row stride of x or out is below the row length", fn);
+    if (!aligned(x, 16) || ldx * (x_dtype == SSM_I8 ? 1 : 2) % 16 != 0)
+        return fail(SSM_ERR_MISALIGNED, "%s: rows of x must start on 16 bytes", fn);
+    if ((x_dtype == SSM_I8) != (x_scale != nullptr)) return fail(SSM_ERR_INVALID_ARG, "%s: x_scale goes with SSM_I8 x", fn);
+    if (x_blocks < 1 || x_blocks > 64 || (!x_scale && x_blocks != 1) || K % ((int64_t)x_blocks * group) != 0)
+        return fail(SSM_ERR_INVALID_ARG, "%s: %d blocks of x (1 to 64 for SSM_I8, each a multiple of the group)", fn, x_blocks);
+    if (!aligned(out, esize(out_dtype)) || (x_scale && !aligned(x_scale, 4)))
+        return fail(SSM_ERR_MISALIGNED, "%s: out or x_scale is not element aligned", fn);
+    int serr = 0;
+    status_ptr(&serr);
+    if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
+    ssm::W4LinearArgs a{};
+    a.M = (int)M;
+    a.w = make_w4(N, K, group, codes, ldc, scale_dtype, scales, lds, zeros, ldz);
+    a.x = x;
+    a.x_i8 = x_dtype == SSM_I8;
+    a.out_bf16 = out_dtype == SSM_BF16;
+    a.ldx = ldx;
+    a.x_scale = x_scale;
+    a.x_blocks = x_blocks;
+    a.out = out;
+    a.ldo = ldo;
+    const char* why = "";
+    if (ssm::launch_w4_linear(a, static_cast<cudaStream_t>(cuda_stream), &why) != 0) return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
+    return SSM_OK;
+}
+
+int spec_probs(int64_t n_rows, int64_t vocab, ssm_dtype_t in_dtype, const void* logits, int64_t ld_in,
+               const float* temperature, float* probs, int64_t ld_out, void* cuda_stream) {
+    static const char* fn = "spec_probs";
+    g_err[0] = 0;
+    if (n_rows < 0 || n_rows >= (1LL << 28)) return fail(SSM_ERR_INVALID_ARG, "%s: n_rows %lld not in [0, 2^28)", fn, (long long)n_rows);
+    if (vocab < 1 || vocab > (1LL << 24)) return fail(SSM_ERR_INVALID_ARG, "%s: vocab %lld not in [1, 2^24]", fn, (long long)vocab);
+    if (!dtype_ok(in_dtype)) return fail(SSM_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+    if (n_rows == 0) return SSM_OK;
+    if (!logits || !probs) return fail(SSM_ERR_INVALID_ARG, "%s: logits or probs is NULL", fn);
+    if (ld_in < vocab || ld_out < vocab) return fail(SSM_ERR_INVALID_ARG, "%s: a row stride is below vocab", fn);
+    if (!aligned(logits, esize(in_dtype)) || !aligned(probs, 4) || (temperature && !aligned(temperature, 4)))
+        return fail(SSM_ERR_MISALIGNED, "%s: a tensor is not element aligned", fn);
+    int serr = 0;
+    status_ptr(&serr);
+    if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
+    const ssm::ProbsArgs a{n_rows, vocab, logits, ld_in, ld_out, temperature, probs};
+    const char* why = "";
+    if (ssm::launch_spec_probs(a, in_dtype == SSM_BF16, static_cast<cudaStream_t>(cuda_stream), &why) != 0)
+        return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
+    return SSM_OK;
+}
+
+int spec_verify(int batch, int n_max, int64_t vocab, const int32_t* draft, const int32_t* n_draft,
+                const float* target_probs, int64_t tp_stride_b, int64_t tp_stride_t,
+                const float* draft_probs, int64_t dp_stride_b, int64_t dp_stride_t, const float* u,
+                int32_t* tokens, int32_t* n_kept, void* cuda_stream) {
+    static const char* fn = "spec_verify";
+    g_err[0] = 0;
+    if (batch < 0 || batch > 65535) return fail(SSM_ERR_INVALID_ARG, "%s: batch %d not in [0, 65535]", fn, batch);
+    if (n_max < 0 || n_max > 1024) return fail(SSM_ERR_INVALID_ARG, "%s: n_max %d not in [0, 1024]", fn, n_max);
+    if (vocab < 1 || vocab > (1LL << 24)) return fail(SSM_ERR_INVALID_ARG, "%s: vocab %lld not in [1, 2^24]", fn, (long long)vocab);
+    if (batch == 0) return SSM_OK;
+    if ((n_max > 0 && !draft) || !target_probs || !u || !tokens || !n_kept)
+        return fail(SSM_ERR_INVALID_ARG, "%s: a required pointer is NULL", fn);
+    if (tp_stride_t < vocab || tp_stride_b < vocab || (draft_probs && n_max > 0 && (dp_stride_t < vocab || dp_stride_b < vocab)))
+        return fail(SSM_ERR_INVALID_ARG, "%s: a stride of the probabilities is below vocab", fn);
+    for (const void* p : {(const void*)draft, (const void*)n_draft, (const void*)target_probs, (const void*)draft_probs,
+                          (const void*)u, (const void*)tokens, (const void*)n_kept})
+        if (!aligned(p, 4)) return fail(SSM_ERR_MISALIGNED, "%s: a tensor is not element aligned", fn);
+    int serr = 0;
+    unsigned int* status = status_ptr(&serr);
+    if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
+    const ssm::VerifyArgs a{batch, n_max, vocab, draft, n_draft, target_probs, n_max > 0 ? draft_probs : nullptr, u,
+                            tp_stride_b, tp_stride_t, dp_stride_b, dp_stride_t, tokens, n_kept, status};
+    const char* why = "";
+    if (ssm::launch_spec_verify(a, static_cast<cudaStream_t>(cuda_stream), &why) != 0) return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
+    return SSM_OK;
+}
+
+}  // extern "C"

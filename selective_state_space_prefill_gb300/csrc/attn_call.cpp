@@ -5,106 +5,17 @@
 // binding would: check the tensors, allocate the outputs that were not passed, and call libssm's
 // entry point (include/ssm.h) with device pointers, element strides and the current stream.  It
 // computes nothing.  Each function returns its outputs, or the library's negative status as an int.
-#include <Python.h>
-
-#include <ATen/ATen.h>
-#include <c10/cuda/CUDAFunctions.h>
-#include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAStream.h>
-#include <torch/csrc/Dtype.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <initializer_list>
-#include <optional>
-#include <stdexcept>
-#include <string>
-
-#include "ssm.h"
+#include "call.h"
 
 namespace {
+
+using namespace ssm_call;
 
 decltype(&attn_append) f_append = nullptr;
 decltype(&attn_cache_read) f_read = nullptr;
 decltype(&attn_prefill) f_prefill = nullptr;
 decltype(&attn_decode_workspace_bytes) f_decode_bytes = nullptr;
 decltype(&attn_decode_step) f_decode = nullptr;
-
-struct TypeProblem : std::runtime_error {
-    using std::runtime_error::runtime_error;
-};
-[[noreturn]] void value_error(const std::string& s) { throw std::invalid_argument(s); }
-
-const at::Tensor& tensor(PyObject* o, const char* name) {
-    if (!THPVariable_Check(o)) throw TypeProblem(std::string(name) + " must be a tensor");
-    return THPVariable_Unpack(o);
-}
-const at::Tensor& cuda_tensor(PyObject* o, const char* name) {
-    const at::Tensor& t = tensor(o, name);
-    if (!t.is_cuda()) value_error(std::string(name) + " must be a CUDA tensor (libssm has no CPU path)");
-    return t;
-}
-bool given(PyObject* o) { return o != nullptr && o != Py_None; }
-
-struct Arg {
-    int at;
-    const char* name;
-};
-// Where a call works.  The one GPU that its tensors lie on is made current while it allocates and
-// launches: the library works on the current device, whatever the pointers are.  A caller's stream is
-// made current too: an output or workspace made here then comes from that stream's memory, and what is
-// written into it follows whatever still uses that memory there.  (Memory of another stream may be free to
-// be handed out on that stream and yet be in use: its last work there need not have run.)
-class Place {
-public:
-    Place(PyObject* const* a, std::initializer_list<Arg> tensors, PyObject* stream) {
-        for (const Arg& x : tensors) {
-            PyObject* o = a[x.at];
-            if (!given(o) || PyBool_Check(o) || !THPVariable_Check(o)) continue;
-            const c10::Device d = THPVariable_Unpack(o).device();
-            if (!d.is_cuda()) continue;                 // what has to be a CUDA tensor is seen to by name
-            const int i = d.index();
-            if (index_ >= 0 && i != index_)
-                value_error(std::string(x.name) + " is on cuda:" + std::to_string(i) + ", other arguments on cuda:" +
-                            std::to_string(index_));
-            index_ = i;
-        }
-        if (index_ < 0) return;
-        const auto index = static_cast<c10::DeviceIndex>(index_);
-        if (c10::cuda::device_count() > 1 && c10::cuda::current_device() != index) device_.emplace(index);
-        const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(index);
-        launch_ = current.stream();
-        if (!given(stream)) return;
-        const unsigned long long raw = PyLong_AsUnsignedLongLong(stream);
-        if (PyErr_Occurred()) {
-            PyErr_Clear();
-            throw TypeProblem("stream must be a CUDA stream");
-        }
-        auto* handle = reinterpret_cast<cudaStream_t>(static_cast<uintptr_t>(raw));
-        if (handle == launch_) return;
-        launch_ = handle;
-        before_ = current.unwrap();
-        stream_.emplace(c10::cuda::getStreamFromExternal(handle, index));
-    }
-    void* stream() const { return launch_; }
-    // Memory of the call's stream.
-    at::Tensor scratch(at::IntArrayRef shape, at::ScalarType s, const at::Tensor& like) const {
-        return at::empty(shape, like.options().dtype(s).memory_format(c10::nullopt).requires_grad(false));
-    }
-    // An output: the caller goes on with it on the stream that was current, so that is noted as its user.
-    at::Tensor fresh(at::IntArrayRef shape, at::ScalarType s, const at::Tensor& like) const {
-        at::Tensor t = scratch(shape, s, like);
-        if (stream_ && t.numel() > 0) t.record_stream(*before_);
-        return t;
-    }
-
-private:
-    int index_ = -1;
-    cudaStream_t launch_ = nullptr;
-    std::optional<c10::cuda::CUDAGuard> device_;
-    std::optional<c10::Stream> before_;
-    std::optional<c10::cuda::CUDAStreamGuard> stream_;
-};
 
 // A [tokens, heads, dim] view.  A stride along an extent of one moves nothing, so it is given as a
 // value the library accepts.
@@ -123,51 +34,11 @@ View view(const at::Tensor& t, const char* name) {
     v.p = t.data_ptr();
     return v;
 }
-void need_type(const at::Tensor& t, at::ScalarType s, const char* name, const char* what) {
-    if (t.scalar_type() != s) value_error(std::string(name) + " must be " + what);
-}
 int32_t* int32s(PyObject* o, int64_t n, const char* name) {
     const at::Tensor& t = cuda_tensor(o, name);
     if (t.scalar_type() != at::kInt || t.dim() != 1 || t.size(0) != n || !t.is_contiguous())
         value_error(std::string(name) + " must be contiguous int32 [" + std::to_string(n) + "]");
     return static_cast<int32_t*>(t.data_ptr());
-}
-int as_int(int64_t v, const char* name) {
-    if (v < INT32_MIN || v > INT32_MAX) value_error(std::string(name) + " does not fit 32 bits");
-    return static_cast<int>(v);
-}
-int64_t integer(PyObject* o, const char* name) {
-    const int64_t v = PyLong_AsLongLong(o);
-    if (v == -1 && PyErr_Occurred()) {
-        PyErr_Clear();
-        throw TypeProblem(std::string(name) + " must be an integer");
-    }
-    return v;
-}
-double number(PyObject* o, const char* name) {
-    const double v = PyFloat_AsDouble(o);
-    if (v == -1.0 && PyErr_Occurred()) {
-        PyErr_Clear();
-        throw TypeProblem(std::string(name) + " must be a number");
-    }
-    return v;
-}
-bool truth(PyObject* o, const char* name) {
-    const int v = PyObject_IsTrue(o);
-    if (v < 0) {
-        PyErr_Clear();
-        throw TypeProblem(std::string(name) + " must be a truth value");
-    }
-    return v != 0;
-}
-ssm_dtype_t out_code(at::ScalarType s) {
-    if (s == at::kFloat) return SSM_F32;
-    if (s == at::kBFloat16) return SSM_BF16;
-    throw TypeProblem("unsupported dtype (float32 or bfloat16)");
-}
-at::ScalarType scalar_type(PyObject* o) {
-    if (!THPDtype_Check(o)) throw TypeProblem("out_dtype must be a torch dtype");
-    return reinterpret_cast<THPDtype*>(o)->scalar_type;
 }
 struct Cache {
     ssm_dtype_t code;
@@ -235,24 +106,6 @@ at::Tensor attn_lse(PyObject* o, const at::Tensor& q, const Place& on) {
     return t;
 }
 
-PyObject* wrap(const at::Tensor& t) {
-    if (!t.defined()) Py_RETURN_NONE;
-    return THPVariable_Wrap(t);
-}
-PyObject* two(const at::Tensor& a, const at::Tensor& b) {
-    PyObject* x = wrap(a);
-    PyObject* y = x ? wrap(b) : nullptr;
-    PyObject* r = y ? PyTuple_New(2) : nullptr;
-    if (!r) {
-        Py_XDECREF(x);
-        Py_XDECREF(y);
-        return nullptr;
-    }
-    PyTuple_SET_ITEM(r, 0, x);
-    PyTuple_SET_ITEM(r, 1, y);
-    return r;
-}
-
 // (q, k, v, positions, cos, sin, k_cache, v_cache, slots, k_scale, v_scale, interleaved, q_out, k_out, stream)
 PyObject* do_append(PyObject* const* a) {
     const Place on(a, {{1, "k"}, {0, "q"}, {2, "v"}, {3, "positions"}, {4, "cos"}, {5, "sin"}, {6, "k_cache"}, {7, "v_cache"},
@@ -307,7 +160,7 @@ PyObject* do_append(PyObject* const* a) {
     const int rc = f_append(kv.n, as_int(qv.p || given(a[0]) ? qv.h : c.h, "heads"), c.h, c.d, as_int(2 * half, "rot_dim"), inter,
                             qv.p, qv.st, qv.sh, kv.p, kv.st, kv.sh, vv.p, vv.st, vv.sh, positions, cp, sp, n_pos, slots,
                             c.code, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, qo.p, qo.st, qo.sh, ko.p, ko.st, ko.sh, on.stream());
-    return rc ? PyLong_FromLong(rc) : two(q_out, k_out);
+    return rc ? PyLong_FromLong(rc) : several({q_out, k_out});
 }
 
 // (k_cache, v_cache, page_table, cu_len, n_tokens, k_scale, v_scale, first, k_out, v_out, out_dtype, stream)
@@ -329,7 +182,7 @@ PyObject* do_read(PyObject* const* a) {
         value_error("k_out and v_out must be contiguous [n_tokens, kv_heads, head_dim] of one dtype");
     const int rc = f_read(as_int(batch, "batch"), n, c.h, c.d, c.code, c.k, c.v, c.ks, c.vs, c.n_pages, c.page, tb.p, tb.stride,
                           tb.n, cu, first, out_code(k.scalar_type()), k.data_ptr(), v.data_ptr(), on.stream());
-    return rc ? PyLong_FromLong(rc) : two(k, v);
+    return rc ? PyLong_FromLong(rc) : several({k, v});
 }
 
 double scale_of(PyObject* o, int64_t d) { return given(o) ? number(o, "scale") : 1.0 / std::sqrt((double)d); }
@@ -351,7 +204,7 @@ PyObject* do_prefill(PyObject* const* a) {
                              out_code(out.scalar_type()), qv.p, qv.st, qv.sh, kv.p, kv.st, kv.sh, vv.p, vv.st, vv.sh, cq, ck,
                              (float)scale_of(a[6], qv.d), ov.p, ov.st, ov.sh,
                              lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr, on.stream());
-    return rc ? PyLong_FromLong(rc) : two(out, lse);
+    return rc ? PyLong_FromLong(rc) : several({out, lse});
 }
 
 // (q, k_cache, v_cache, page_table, lens, max_len, k_scale, v_scale, scale, out, out_dtype, lse, workspace, stream)
@@ -380,42 +233,13 @@ PyObject* do_decode(PyObject* const* a) {
                             (float)scale_of(a[8], c.d), ov.p, ov.st, ov.sh,
                             lse.defined() ? static_cast<float*>(lse.data_ptr()) : nullptr,
                             ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.nbytes() : 0, on.stream());
-    return rc ? PyLong_FromLong(rc) : two(out, lse);
-}
-
-// No C++ exception leaves the module.
-template <PyObject* (*F)(PyObject* const*), int kArgs>
-PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != kArgs) {
-        PyErr_Format(PyExc_TypeError, "%d arguments expected, %zd given", kArgs, n);
-        return nullptr;
-    }
-    try {
-        return F(a);
-    } catch (const TypeProblem& e) {
-        PyErr_SetString(PyExc_TypeError, e.what());
-    } catch (const std::invalid_argument& e) {
-        PyErr_SetString(PyExc_ValueError, e.what());
-    } catch (...) {                                     // torch's own (out of memory among them)
-        torch::translate_exception_to_python(std::current_exception());
-    }
-    return nullptr;
+    return rc ? PyLong_FromLong(rc) : several({out, lse});
 }
 
 // bind(addresses of attn_append, attn_cache_read, attn_prefill, attn_decode_workspace_bytes, attn_decode_step)
 PyObject* do_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* p[5];
-    if (n != 5) {
-        PyErr_SetString(PyExc_TypeError, "five addresses expected");
-        return nullptr;
-    }
-    for (int i = 0; i < 5; ++i) {
-        p[i] = PyLong_AsVoidPtr(a[i]);
-        if (!p[i]) {
-            if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
-            return nullptr;
-        }
-    }
+    if (!addresses(a, n, p, 5)) return nullptr;
     f_append = reinterpret_cast<decltype(f_append)>(p[0]);
     f_read = reinterpret_cast<decltype(f_read)>(p[1]);
     f_prefill = reinterpret_cast<decltype(f_prefill)>(p[2]);
@@ -423,9 +247,6 @@ PyObject* do_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     f_decode = reinterpret_cast<decltype(f_decode)>(p[4]);
     Py_RETURN_NONE;
 }
-
-template <typename F>
-PyCFunction fast(F f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)); }
 
 PyMethodDef methods[] = {
     {"bind", fast(do_bind), METH_FASTCALL, "Take libssm's entry points."},

@@ -262,6 +262,64 @@ int launch_attn_read(const AttnReadArgs& a, bool cache_i8, bool out_bf16, cudaSt
 int launch_attn_prefill(const AttnPrefillArgs& a, bool out_bf16, cudaStream_t stream, const char** why);
 int launch_attn_decode(const AttnDecodeArgs& a, bool cache_i8, bool out_bf16, cudaStream_t stream, const char** why);
 
+// ------------------------------------------------------------------ around the mixers of a decode step
+// Types are ssm_dtype_t's values.
+struct NormArgs {
+    int64_t n_rows;
+    int width, n_groups;
+    int in_type, res_type, out_type;
+    const void *x, *residual;
+    void *residual_out, *out;
+    int64_t x_st, res_st, ro_st, out_st;
+    const float* weight;
+    float eps;
+    float* out_scale;
+};
+
+struct W4Weight {
+    int N, K, group;
+    const uint8_t *codes, *zeros;
+    const void* scales;
+    bool scale_bf16;
+    int64_t ldc, lds, ldz;
+};
+
+struct W4LinearArgs {
+    int M;
+    W4Weight w;
+    const void* x;
+    bool x_i8, out_bf16;
+    int64_t ldx;
+    const float* x_scale;
+    int x_blocks;
+    void* out;
+    int64_t ldo;
+};
+
+struct ProbsArgs {
+    int64_t n_rows, vocab;
+    const void* logits;
+    int64_t ld_in, ld_out;
+    const float* temperature;
+    float* probs;
+};
+
+struct VerifyArgs {
+    int batch, n_max;
+    int64_t vocab;
+    const int32_t *draft, *n_draft;
+    const float *p, *q, *u;
+    int64_t p_sb, p_st, q_sb, q_st;
+    int32_t *tokens, *n_kept;
+    unsigned int* status;
+};
+
+int launch_norm_rms(const NormArgs& a, cudaStream_t stream, const char** why);
+int launch_w4_quantize(const W4Weight& w, const void* W, int64_t ldw, bool in_bf16, cudaStream_t stream, const char** why);
+int launch_w4_linear(const W4LinearArgs& a, cudaStream_t stream, const char** why);
+int launch_spec_probs(const ProbsArgs& a, bool in_bf16, cudaStream_t stream, const char** why);
+int launch_spec_verify(const VerifyArgs& a, cudaStream_t stream, const char** why);
+
 // Each returns 0 on success, or -1 with *why set to a static message.
 int launch_ssd_prefill(const SsdArgs& a, bool out_bf16, cudaStream_t stream, const char** why);
 int launch_ssd_decode(const SsdDecodeArgs& a, bool in_bf16, bool out_bf16, cudaStream_t stream, const char** why);
