@@ -647,7 +647,7 @@ int norm_rms(int64_t n_rows, int width, int n_groups, ssm_dtype_t in_dtype, cons
  *   scales   [N][K / group] SSM_BF16 or SSM_F32, row stride lds elements, a multiple of 16 bytes
  *   zeros    NULL or [N][K / group] bytes 0 .. 15 (the low half counts), row stride ldz, a multiple of 16
  * All 16-byte aligned; a row of scales or zeros is readable up to the next multiple of 16 bytes.  group is
- * 32, 64 or 128, K a multiple of group up to 65536, N in 1 .. 2^27.
+ * 32, 64 or 128, K a multiple of group up to 32768, N in 1 .. 2^27.
  */
 
 /*
@@ -662,22 +662,29 @@ int w4_quantize(int64_t N, int64_t K, int group, ssm_dtype_t in_dtype, const voi
                 uint8_t* codes, int64_t ldc, ssm_dtype_t scale_dtype, void* scales, int64_t lds,
                 uint8_t* zeros, int64_t ldz, void* cuda_stream);
 
+/* Bytes of device workspace w4_linear needs for these sizes (0 on a bad size): the sums of the slices into which
+ * long rows are cut. */
+size_t w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);
+
 /*
  * w4_linear -- out[m][n] = sum_k x[m][k] W[n][k] with a 4-bit W, for the few rows of a decode step.  Products
- * of x and (code - zero) are exact and are summed in fp32 within a group, the groups' sums times their scales
- * in fp32, in an order that the sizes alone choose.
+ * of x and codes are exact and are summed in fp32 within a group, the groups' sums times their scales in fp32, in
+ * an order that the sizes alone choose.  An infinity or NaN in a row of x makes that row's outputs NaN.
  *
- *   M                    >= 0 (0 does nothing), up to 2^20; made for up to about 64, more rows go through in
- *                        turns of 32 that each unpack the weight again
+ *   M                    0 .. 256 (0 does nothing); more return SSM_ERR_UNSUPPORTED: they belong to a product with
+ *                        the whole weight
  *   x_dtype, x, ldx      [M][K] SSM_BF16 or SSM_I8; 16-byte aligned, row stride ldx >= K, a multiple of 16 bytes
  *   x_scale, x_blocks    SSM_I8: [M][x_blocks] float32, a scale for each K / x_blocks consecutive elements of a
  *                        row (a multiple of group); x_blocks up to 64.  SSM_BF16: NULL and 1
  *   out_dtype, out, ldo  [M][N] SSM_BF16 or SSM_F32, row stride ldo >= N, element aligned
+ *   workspace            at least w4_linear_workspace_bytes(...) bytes, 16-byte aligned (NULL allowed where that
+ *                        is 0); its contents on entry do not matter.  Calls that share a workspace must not
+ *                        overlap on the GPU.
  */
 int w4_linear(int64_t M, int64_t N, int64_t K, int group, ssm_dtype_t x_dtype, const void* x, int64_t ldx,
               const float* x_scale, int x_blocks, const uint8_t* codes, int64_t ldc,
               ssm_dtype_t scale_dtype, const void* scales, int64_t lds, const uint8_t* zeros, int64_t ldz,
-              ssm_dtype_t out_dtype, void* out, int64_t ldo, void* cuda_stream);
+              ssm_dtype_t out_dtype, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* cuda_stream);
 
 /*
  * spec_probs -- probabilities of logits: p[r][i] = exp(x_i / t) / sum_j exp(x_j / t) with t = temperature[r].

@@ -27,7 +27,8 @@ EXPORTS = ("ssm_abi_version", "ssm_prefill", "ssm_prefill_workspace_bytes", "ssm
            "q8_reduce_partials", "q8_block_absmax", "q8_quantize_shared", "q8_sum_dequant",
            "ssd_prefill_workspace_bytes", "ssd_prefill", "ssd_decode_step",
            "attn_rope_table", "attn_append", "attn_cache_read", "attn_prefill", "attn_decode_workspace_bytes",
-           "attn_decode_step", "norm_rms", "w4_quantize", "w4_linear", "spec_probs", "spec_verify",
+           "attn_decode_step", "norm_rms", "w4_quantize", "w4_linear_workspace_bytes", "w4_linear", "spec_probs",
+           "spec_verify",
            "ssm_selftest_expire_wait", "ssm_device_status", "ssm_last_error")
 NOALLOC_SCRATCH_BYTES = 4 << 20     # SSM_NOALLOC_SCRATCH_BYTES
 
@@ -107,8 +108,10 @@ def load(path: Path | str | None = None):
     lib.norm_rms.restype = I
     lib.w4_quantize.argtypes = [L, L, I, I, P, L, P, L, I, P, L, P, L, P]
     lib.w4_quantize.restype = I
-    lib.w4_linear.argtypes = [L, L, L, I, I, P, L, P, I, P, L, I, P, L, P, L, I, P, L, P]
+    lib.w4_linear.argtypes = [L, L, L, I, I, P, L, P, I, P, L, I, P, L, P, L, I, P, L, P, Z, P]
     lib.w4_linear.restype = I
+    lib.w4_linear_workspace_bytes.argtypes = [L, L, L, I]
+    lib.w4_linear_workspace_bytes.restype = Z
     lib.spec_probs.argtypes = [L, L, I, P, L, P, P, L, P]
     lib.spec_probs.restype = I
     lib.spec_verify.argtypes = [I, I, L, P, P, P, L, L, P, L, L, P, P, P, P]
@@ -735,7 +738,7 @@ def step_calls():
     """The extension that marshals these calls (csrc/step_call.cpp)."""
     global _steps
     if _steps is None:
-        _steps = _extension(STEP_CALLS, ("norm_rms", "w4_quantize", "w4_linear", "spec_probs", "spec_verify"))
+        _steps = _extension(STEP_CALLS, ("norm_rms", "w4_quantize", "w4_linear_workspace_bytes", "w4_linear", "spec_probs", "spec_verify"))
     return _steps
 
 
@@ -760,11 +763,18 @@ def w4_quantize(W, group=128, zeros=False, scale_dtype=torch.bfloat16, stream=No
     return _outcome((_steps or step_calls()).quantize(W, group, zeros, scale_dtype, _raw(stream)), "w4_quantize")
 
 
-def w4_linear(x, codes, scales, zeros=None, x_scale=None, out=None, out_dtype=torch.bfloat16, stream=None):
-    """w4_linear: x [M, K] times the transpose of a 4-bit weight (w4_quantize's layout), for the few rows of a
-    decode step.  x is bfloat16, or int8 with x_scale [M] or [M, blocks] float32 (norm_rms's).  ``zeros`` None
-    stands for 8.  Returns out [M, N] (bfloat16 or float32)."""
-    return _outcome((_steps or step_calls()).linear(x, codes, scales, zeros, x_scale, out, out_dtype, _raw(stream)), "w4_linear")[0]
+def w4_linear_workspace_bytes(M: int, N: int, K: int, group: int) -> int:
+    """w4_linear_workspace_bytes: device bytes w4_linear needs."""
+    return int(load().w4_linear_workspace_bytes(M, N, K, group))
+
+
+def w4_linear(x, codes, scales, zeros=None, x_scale=None, out=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """w4_linear: x [M, K] times the transpose of a 4-bit weight (w4_quantize's layout), for the few rows (up to
+    256) of a decode step.  x is bfloat16, or int8 with x_scale [M] or [M, blocks] float32 (norm_rms's).  ``zeros``
+    None stands for 8.  ``workspace`` (a CUDA uint8 tensor of at least w4_linear_workspace_bytes(...) bytes) is
+    allocated here with torch when not given.  Returns out [M, N] (bfloat16 or float32)."""
+    return _outcome((_steps or step_calls()).linear(x, codes, scales, zeros, x_scale, out, out_dtype, workspace, _raw(stream)),
+                    "w4_linear")[0]
 
 
 def spec_probs(logits, temperature=None, out=None, stream=None):

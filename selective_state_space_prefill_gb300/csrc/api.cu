@@ -1069,7 +1069,7 @@ int check_w4(const char* fn, int64_t N, int64_t K, int group, const void* codes,
     if (group != 32 && group != 64 && group != 128)
         return fail(SSM_ERR_UNSUPPORTED, "%s: group %d unsupported (32, 64 or 128)", fn, group);
     if (K < 1 || K % group != 0) return fail(SSM_ERR_INVALID_ARG, "%s: K %lld is not a multiple of the group %d", fn, (long long)K, group);
-    if (K > 65536) return fail(SSM_ERR_UNSUPPORTED, "%s: K %lld above 65536", fn, (long long)K);
+    if (K > 32768) return fail(SSM_ERR_UNSUPPORTED, "%s: K %lld above 32768", fn, (long long)K);
     if (!dtype_ok(scale_dtype)) return fail(SSM_ERR_INVALID_ARG, "%s: unknown scale dtype", fn);
     if (!codes || !scales) return fail(SSM_ERR_INVALID_ARG, "%s: codes or scales is NULL", fn);
     if (ldc < K / 2 || lds < K / group || (zeros && ldz < K / group))
@@ -1165,13 +1165,20 @@ int w4_quantize(int64_t N, int64_t K, int group, ssm_dtype_t in_dtype, const voi
     return SSM_OK;
 }
 
+size_t w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
+    if (M < 1 || M > 256 || N < 1 || N > (1LL << 27) || (group != 32 && group != 64 && group != 128) || K < 1 || K % group != 0 || K > 32768)
+        return 0;
+    return ssm::w4_linear_workspace((int)M, make_w4(N, K, group, nullptr, 0, SSM_F32, nullptr, 0, nullptr, 0));
+}
+
 int w4_linear(int64_t M, int64_t N, int64_t K, int group, ssm_dtype_t x_dtype, const void* x, int64_t ldx,
               const float* x_scale, int x_blocks, const uint8_t* codes, int64_t ldc,
               ssm_dtype_t scale_dtype, const void* scales, int64_t lds, const uint8_t* zeros, int64_t ldz,
-              ssm_dtype_t out_dtype, void* out, int64_t ldo, void* cuda_stream) {
+              ssm_dtype_t out_dtype, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* cuda_stream) {
     static const char* fn = "w4_linear";
     g_err[0] = 0;
-    if (M < 0 || M > (1LL << 20)) return fail(SSM_ERR_INVALID_ARG, "%s: M %lld not in [0, 2^20]", fn, (long long)M);
+    if (M < 0) return fail(SSM_ERR_INVALID_ARG, "%s: M %lld < 0", fn, (long long)M);
+    if (M > 256) return fail(SSM_ERR_UNSUPPORTED, "%s: M %lld above 256", fn, (long long)M);
     const int rc = check_w4(fn, N, K, group, codes, ldc, scale_dtype, scales, lds, zeros, ldz);
     if (rc != SSM_OK) return rc;
     if (x_dtype != SSM_BF16 && x_dtype != SSM_I8)
@@ -1187,12 +1194,18 @@ int w4_linear(int64_t M, int64_t N, int64_t K, int group, ssm_dtype_t x_dtype, c
         return fail(SSM_ERR_INVALID_ARG, "%s: %d blocks of x (1 to 64 for SSM_I8, each a multiple of the group)", fn, x_blocks);
     if (!aligned(out, esize(out_dtype)) || (x_scale && !aligned(x_scale, 4)))
         return fail(SSM_ERR_MISALIGNED, "%s: out or x_scale is not element aligned", fn);
+    const ssm::W4Weight w = make_w4(N, K, group, codes, ldc, scale_dtype, scales, lds, zeros, ldz);
+    const size_t need = ssm::w4_linear_workspace((int)M, w);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(SSM_ERR_INVALID_ARG, "%s: workspace of %zu bytes given, %zu needed", fn,
+                    workspace ? workspace_bytes : (size_t)0, need);
+    if (need > 0 && !aligned(workspace, 16)) return fail(SSM_ERR_MISALIGNED, "%s: workspace must be 16-byte aligned", fn);
     int serr = 0;
-    status_ptr(&serr);
+    unsigned int* status = status_ptr(&serr);
     if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
     ssm::W4LinearArgs a{};
     a.M = (int)M;
-    a.w = make_w4(N, K, group, codes, ldc, scale_dtype, scales, lds, zeros, ldz);
+    a.w = w;
     a.x = x;
     a.x_i8 = x_dtype == SSM_I8;
     a.out_bf16 = out_dtype == SSM_BF16;
@@ -1201,8 +1214,9 @@ int w4_linear(int64_t M, int64_t N, int64_t K, int group, ssm_dtype_t x_dtype, c
     a.x_blocks = x_blocks;
     a.out = out;
     a.ldo = ldo;
+    a.parts = static_cast<float*>(workspace);
     const char* why = "";
-    if (ssm::launch_w4_linear(a, static_cast<cudaStream_t>(cuda_stream), &why) != 0) return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
+    if (ssm::launch_w4_linear(a, status, static_cast<cudaStream_t>(cuda_stream), &why) != 0) return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
     return SSM_OK;
 }
 

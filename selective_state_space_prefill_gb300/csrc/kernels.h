@@ -294,6 +294,7 @@ struct W4LinearArgs {
     int x_blocks;
     void* out;
     int64_t ldo;
+    float* parts;                   // [slices of K][M][N], where the plan has several
 };
 
 struct ProbsArgs {
@@ -316,7 +317,8 @@ struct VerifyArgs {
 
 int launch_norm_rms(const NormArgs& a, cudaStream_t stream, const char** why);
 int launch_w4_quantize(const W4Weight& w, const void* W, int64_t ldw, bool in_bf16, cudaStream_t stream, const char** why);
-int launch_w4_linear(const W4LinearArgs& a, cudaStream_t stream, const char** why);
+size_t w4_linear_workspace(int M, const W4Weight& w);
+int launch_w4_linear(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, const char** why);
 int launch_spec_probs(const ProbsArgs& a, bool in_bf16, cudaStream_t stream, const char** why);
 int launch_spec_verify(const VerifyArgs& a, cudaStream_t stream, const char** why);
 

@@ -13,6 +13,7 @@ using namespace ssm_call;
 
 decltype(&norm_rms) f_norm = nullptr;
 decltype(&w4_quantize) f_quantize = nullptr;
+decltype(&w4_linear_workspace_bytes) f_linear_bytes = nullptr;
 decltype(&w4_linear) f_linear = nullptr;
 decltype(&spec_probs) f_probs = nullptr;
 decltype(&spec_verify) f_verify = nullptr;
@@ -128,9 +129,9 @@ Rows grouped(const at::Tensor& t, int64_t n, int64_t groups, const char* name) {
     return r;
 }
 
-// (x, codes, scales, zeros, x_scale, out, out_dtype, stream)
+// (x, codes, scales, zeros, x_scale, out, out_dtype, workspace, stream)
 PyObject* do_linear(PyObject* const* a) {
-    const Place on(a, {{0, "x"}, {1, "codes"}, {2, "scales"}, {3, "zeros"}, {4, "x_scale"}, {5, "out"}}, a[7]);
+    const Place on(a, {{0, "x"}, {1, "codes"}, {2, "scales"}, {3, "zeros"}, {4, "x_scale"}, {5, "out"}, {7, "workspace"}}, a[8]);
     const at::Tensor &x = cuda_tensor(a[0], "x"), &codes = cuda_tensor(a[1], "codes"), &scales = cuda_tensor(a[2], "scales");
     const Rows xv = rows(x, "x"), cv = rows(codes, "codes");
     need_type(codes, at::kByte, "codes", "uint8");
@@ -161,9 +162,19 @@ PyObject* do_linear(PyObject* const* a) {
     const at::Tensor out = given(a[5]) ? cuda_tensor(a[5], "out") : on.fresh(at::IntArrayRef(shape, 2), scalar_type(a[6]), x);
     if (out.sizes() != at::IntArrayRef(shape, 2)) value_error("out must be [M, N]");
     const Rows ov = rows(out, "out");
-    const int rc = f_linear(xv.n, cv.n, xv.w, as_int(xv.w / groups, "group"), xc, xv.p, xv.st, xs, as_int(blocks, "x_blocks"),
+    const int group = as_int(xv.w / groups, "group");
+    at::Tensor ws;
+    if (given(a[7])) {
+        ws = cuda_tensor(a[7], "workspace");
+        if (!ws.is_contiguous()) value_error("workspace must be contiguous");
+    } else {
+        const size_t need = f_linear_bytes(xv.n, cv.n, xv.w, group);
+        if (need) ws = on.scratch({(int64_t)need}, at::kByte, x);
+    }
+    const int rc = f_linear(xv.n, cv.n, xv.w, group, xc, xv.p, xv.st, xs, as_int(blocks, "x_blocks"),
                             static_cast<const uint8_t*>(cv.p), cv.st, sc, sv.p, sv.st, static_cast<const uint8_t*>(zv.p), zv.st,
-                            out_code(out.scalar_type()), ov.p, ov.st, on.stream());
+                            out_code(out.scalar_type()), ov.p, ov.st, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.nbytes() : 0,
+                            on.stream());
     return rc ? PyLong_FromLong(rc) : several({out});
 }
 
@@ -220,15 +231,16 @@ PyObject* do_verify(PyObject* const* a) {
     return rc ? PyLong_FromLong(rc) : several({tokens, kept});
 }
 
-// bind(addresses of norm_rms, w4_quantize, w4_linear, spec_probs, spec_verify)
+// bind(addresses of norm_rms, w4_quantize, w4_linear_workspace_bytes, w4_linear, spec_probs, spec_verify)
 PyObject* do_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    void* p[5];
-    if (!addresses(a, n, p, 5)) return nullptr;
+    void* p[6];
+    if (!addresses(a, n, p, 6)) return nullptr;
     f_norm = reinterpret_cast<decltype(f_norm)>(p[0]);
     f_quantize = reinterpret_cast<decltype(f_quantize)>(p[1]);
-    f_linear = reinterpret_cast<decltype(f_linear)>(p[2]);
-    f_probs = reinterpret_cast<decltype(f_probs)>(p[3]);
-    f_verify = reinterpret_cast<decltype(f_verify)>(p[4]);
+    f_linear_bytes = reinterpret_cast<decltype(f_linear_bytes)>(p[2]);
+    f_linear = reinterpret_cast<decltype(f_linear)>(p[3]);
+    f_probs = reinterpret_cast<decltype(f_probs)>(p[4]);
+    f_verify = reinterpret_cast<decltype(f_verify)>(p[5]);
     Py_RETURN_NONE;
 }
 
@@ -236,7 +248,7 @@ PyMethodDef methods[] = {
     {"bind", fast(do_bind), METH_FASTCALL, "Take libssm's entry points."},
     {"norm", fast(guarded<do_norm, 10>), METH_FASTCALL, "norm_rms"},
     {"quantize", fast(guarded<do_quantize, 5>), METH_FASTCALL, "w4_quantize"},
-    {"linear", fast(guarded<do_linear, 8>), METH_FASTCALL, "w4_linear"},
+    {"linear", fast(guarded<do_linear, 9>), METH_FASTCALL, "w4_linear"},
     {"probs", fast(guarded<do_probs, 4>), METH_FASTCALL, "spec_probs"},
     {"verify", fast(guarded<do_verify, 8>), METH_FASTCALL, "spec_verify"},
     {nullptr, nullptr, 0, nullptr},

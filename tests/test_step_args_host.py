@@ -24,7 +24,7 @@ NORM = dict(n_rows=2, width=64, n_groups=1, in_dtype=BF16, x=FAKE, x_stride=64, 
 QUANT = dict(N=4, K=256, group=128, in_dtype=BF16, W=FAKE, ldw=256, codes=FAKE, ldc=128, scale_dtype=BF16, scales=FAKE, lds=8,
              zeros=FAKE, ldz=16, stream=None)
 LINEAR = dict(M=2, N=4, K=256, group=128, x_dtype=BF16, x=FAKE, ldx=256, x_scale=None, x_blocks=1, codes=FAKE, ldc=128, scale_dtype=F32,
-              scales=FAKE, lds=4, zeros=None, ldz=0, out_dtype=F32, out=FAKE, ldo=4, stream=None)
+              scales=FAKE, lds=4, zeros=None, ldz=0, out_dtype=F32, out=FAKE, ldo=4, workspace=None, workspace_bytes=0, stream=None)
 PROBS = dict(n_rows=2, vocab=10, in_dtype=BF16, logits=FAKE, ld_in=10, temperature=FAKE, probs=FAKE, ld_out=10, stream=None)
 VERIFY = dict(batch=2, n_max=3, vocab=10, draft=FAKE, n_draft=FAKE, target_probs=FAKE, tp_sb=40, tp_st=10, draft_probs=FAKE, dp_sb=30,
               dp_st=10, u=FAKE, tokens=FAKE, n_kept=FAKE, stream=None)
@@ -42,13 +42,13 @@ REFUSED = [
         (dict(out_dtype=I8, out_scale=FAKE, out=FAKE + 4), MISALIGNED)]),
     ("w4_quantize", QUANT, [
         (dict(N=0), INVALID), (dict(N=(1 << 27) + 1), INVALID), (dict(K=0), INVALID), (dict(K=192), INVALID), (dict(group=16), UNSUPPORTED),
-        (dict(group=256), UNSUPPORTED), (dict(K=65664, ldw=65664, ldc=32832, lds=520, ldz=528), UNSUPPORTED), (dict(in_dtype=2), INVALID),
+        (dict(group=256), UNSUPPORTED), (dict(K=32896, ldw=32896, ldc=16448, lds=520, ldz=528), UNSUPPORTED), (dict(in_dtype=2), INVALID),
         (dict(scale_dtype=2), INVALID), (dict(W=None), INVALID), (dict(codes=None), INVALID), (dict(scales=None), INVALID),
         (dict(ldw=255), INVALID), (dict(ldc=112), INVALID), (dict(lds=1), INVALID), (dict(ldz=1), INVALID), (dict(ldc=136), MISALIGNED),
         (dict(lds=4), MISALIGNED), (dict(ldz=8), MISALIGNED), (dict(codes=FAKE + 8), MISALIGNED), (dict(scales=FAKE + 8), MISALIGNED),
         (dict(zeros=FAKE + 4), MISALIGNED), (dict(W=FAKE + 1), MISALIGNED)]),
     ("w4_linear", LINEAR, [
-        (dict(M=-1), INVALID), (dict(M=(1 << 20) + 1), INVALID), (dict(N=0), INVALID), (dict(K=192), INVALID), (dict(group=96), UNSUPPORTED),
+        (dict(M=-1), INVALID), (dict(M=257), UNSUPPORTED), (dict(N=0), INVALID), (dict(K=192), INVALID), (dict(group=96), UNSUPPORTED),
         (dict(x_dtype=F32), UNSUPPORTED), (dict(x_dtype=5), INVALID), (dict(out_dtype=2), INVALID), (dict(x=None), INVALID),
         (dict(out=None), INVALID), (dict(ldx=248), INVALID), (dict(ldo=3), INVALID), (dict(ldx=260), MISALIGNED), (dict(x=FAKE + 8), MISALIGNED),
         (dict(x_scale=FAKE), INVALID), (dict(x_dtype=I8), INVALID), (dict(x_dtype=I8, x_scale=FAKE, x_blocks=0), INVALID),
@@ -79,6 +79,19 @@ def test_library_refuses(lib, fn, base, change, code):
     assert lib.ssm_last_error().decode().startswith(fn)
 
 
+def test_linear_wants_a_workspace_for_long_rows(lib):
+    need = lib.w4_linear_workspace_bytes(2, 4, 32768, 128)
+    assert need >= 8 * 2 * 4 * 4 and need % (2 * 4 * 4) == 0                # at least eight slices' sums
+    long = dict(LINEAR, K=32768, ldx=32768, ldc=16384, lds=256)
+    for more, code in ((dict(), INVALID), (dict(workspace=FAKE, workspace_bytes=need - 1), INVALID),
+                       (dict(workspace=FAKE + 8, workspace_bytes=need), MISALIGNED)):
+        assert lib.w4_linear(*{**long, **more}.values()) == code
+        assert "workspace" in lib.ssm_last_error().decode()
+    assert lib.w4_linear_workspace_bytes(8, 16384, 4096, 128) == 0          # 4096 elements are one slice
+    for bad in ((0, 4, 128, 128), (257, 4, 128, 128), (1, 0, 128, 128), (1, 4, 192, 128), (1, 4, 128, 16), (1, 4, 32896, 128)):
+        assert lib.w4_linear_workspace_bytes(*bad) == 0
+
+
 @pytest.mark.parametrize("fn,base,change", [("norm_rms", NORM, dict(n_rows=0, x=None, out=None)), ("w4_linear", LINEAR, dict(M=0, x=None, out=None)),
                                             ("spec_probs", PROBS, dict(n_rows=0, logits=None, probs=None)),
                                             ("spec_verify", VERIFY, dict(batch=0, target_probs=None, u=None))])
@@ -107,13 +120,14 @@ CALLS = {
     "norm_rms": lambda: dict(x=_t(4, 64), weight=_f(64), residual=_t(4, 64), out=_t(4, 64, dtype=torch.int8), residual_out=_t(4, 64),
                              out_scale=_f(4, 1)),
     "w4_quantize": lambda: dict(W=_t(8, 256)),
-    "w4_linear": lambda: dict(x=_t(4, 256, dtype=torch.int8), codes=_u8(8, 128), scales=_f(8, 4), zeros=_u8(8, 4), x_scale=_f(4), out=_t(4, 8)),
+    "w4_linear": lambda: dict(x=_t(4, 256, dtype=torch.int8), codes=_u8(8, 128), scales=_f(8, 4), zeros=_u8(8, 4), x_scale=_f(4), out=_t(4, 8),
+                              workspace=_u8(64)),
     "spec_probs": lambda: dict(logits=_t(4, 100), temperature=_f(4), out=_f(4, 100)),
     "spec_verify": lambda: dict(draft=_i(2, 3), target_probs=_f(2, 4, 10), u=_f(2, 4), draft_probs=_f(2, 3, 10), n_draft=_i(2), tokens=_i(2, 4),
                                 n_kept=_i(2)),
 }
 NAMES = [(fn, name) for fn, names in {
-    "norm_rms": "x weight residual out residual_out out_scale", "w4_linear": "x codes scales zeros x_scale out",
+    "norm_rms": "x weight residual out residual_out out_scale", "w4_linear": "x codes scales zeros x_scale out workspace",
     "spec_probs": "logits temperature out", "spec_verify": "draft target_probs u draft_probs n_draft tokens n_kept",
 }.items() for name in names.split()]
 
