@@ -1,8 +1,11 @@
 // norm.cu -- norm_rms: residual addition and root-mean-square norm over groups of a row's channels, with an
 // output in bf16, fp32, or int8 with a scale per row and group.
 //
-// A first form: one CTA per row and group, the fp32 sum r in shared memory between its three uses (mean of
-// squares, maximum, output).
+// Bytes in and out over the copy rate are the floor.  A row's group stays in registers between its uses (mean of
+// squares, maximum, output), so that everything is read and written once: a thread holds up to V vectors of eight
+// channels, all loads in flight before the first is used.  Small groups are a warp's, several to a CTA, without a
+// barrier; larger ones a CTA's of 64 .. 1024 threads, with as few vectors a thread as that allows for few rows
+// (latency) and four for many (loads in flight, fewer threads at the barriers).
 #include "common.cuh"
 #include "kernels.h"
 #include "ssm.h"
@@ -10,33 +13,41 @@
 namespace ssm {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kSms = 152;
 
-__device__ __forceinline__ void load8(const void* p, int64_t at, bool bf16, float* v) {
-    if (bf16) {
-        const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p) + at);
+// Eight channels.
+template <typename T> struct Vec;
+template <> struct Vec<__nv_bfloat16> {
+    uint4 q;
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
+        q = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p) + at);
+    }
+    __device__ __forceinline__ void get(float* v) const {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    } else {
+    }
+};
+template <> struct Vec<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
         const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
-        const float4 a = q[0], b = q[1];
+        a = q[0], b = q[1];
+    }
+    __device__ __forceinline__ void get(float* v) const {
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
-}
+};
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void store8(void* p, int64_t at, bool bf16, const float* v) {
-    if (bf16) {
-        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p) + at) =
-            make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-    } else {
-        float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + at);
-        q[0] = make_float4(v[0], v[1], v[2], v[3]);
-        q[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 // round_half_even(y * inv) within [-127, 127]; a NaN gives 0
 __device__ __forceinline__ uint32_t code(float y, float inv) {
@@ -44,64 +55,138 @@ __device__ __forceinline__ uint32_t code(float y, float inv) {
     return c == c ? (uint32_t)__float2int_rn(fminf(fmaxf(c, -127.f), 127.f)) & 0xffu : 0u;
 }
 
-template <bool kMax>
-__device__ float across(float v, float* s) {
+// The sum or maximum over a group's threads: a warp, or a CTA of W warps.
+template <int W, bool kMax>
+__device__ __forceinline__ float across(float v, float* s) {
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const float w = __shfl_xor_sync(~0u, v, o);
         v = kMax ? fmaxf(v, w) : v + w;
     }
-    __syncthreads();
+    if (W == 1) return v;
     if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
     __syncthreads();
-    v = s[0];
-    for (int i = 1; i < kThreads / 32; ++i) v = kMax ? fmaxf(v, s[i]) : v + s[i];
-    return v;
+    const int lane = threadIdx.x % 32;
+    v = lane < W ? s[lane] : 0.f;                       // a sum of squares and a maximum of magnitudes start at 0
+#pragma unroll
+    for (int o = W > 16 ? 16 : W > 8 ? 8 : W > 4 ? 4 : W > 2 ? 2 : 1; o > 0; o >>= 1) {
+        const float w = __shfl_xor_sync(~0u, v, o);
+        v = kMax ? fmaxf(v, w) : v + w;
+    }
+    return __shfl_sync(~0u, v, 0);
 }
 
-__global__ void __launch_bounds__(kThreads) k_norm_rms(const NormArgs a) {
-    extern __shared__ float s_r[];
-    __shared__ float s_part[kThreads / 32];
-    const int64_t row = blockIdx.x / a.n_groups;
-    const int group = blockIdx.x % a.n_groups, n = a.width / a.n_groups, c0 = group * n;
-    float sum = 0.f;
-    for (int c = 8 * threadIdx.x; c < n; c += 8 * kThreads) {
-        float v[8], w[8];
-        load8(a.x, row * a.x_st + c0 + c, a.in_type == SSM_BF16, v);
-        if (a.residual) {
-            load8(a.residual, row * a.res_st + c0 + c, a.res_type == SSM_BF16, w);
-            for (int i = 0; i < 8; ++i) v[i] += w[i];
-            if (a.residual_out) store8(a.residual_out, row * a.ro_st + c0 + c, a.res_type == SSM_BF16, v);
+// W warps for a group (1: four groups to a CTA), V vectors a thread.
+template <typename Tx, typename Tr, typename To, int W, int V>
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) k_norm_rms(const NormArgs a) {
+    constexpr bool kI8 = sizeof(To) == 1;
+    constexpr int kStep = 8 * 32 * W;                   // channels of a group between a thread's vectors
+    __shared__ float s_sum[W], s_max[W];
+    const int n = a.width / a.n_groups, tid = W == 1 ? threadIdx.x % 32 : threadIdx.x;
+    const unsigned unit = W == 1 ? blockIdx.x * 4 + threadIdx.x / 32 : blockIdx.x;
+    const unsigned row = unit / (unsigned)a.n_groups, group = unit - row * (unsigned)a.n_groups;
+    if (W == 1 && row >= a.n_rows) return;
+    const int c0 = group * n, first = 8 * tid;
+    Vec<Tx> x[V];
+    Vec<Tr> r[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (first + i * kStep < n) {
+            x[i].load(a.x, row * a.x_st + c0 + first + i * kStep);
+            if (a.residual) r[i].load(a.residual, row * a.res_st + c0 + first + i * kStep);
         }
-        for (int i = 0; i < 8; ++i) sum = fmaf(v[i], v[i], sum), s_r[c + i] = v[i];
-    }
-    const float f = rsqrtf(across<false>(sum, s_part) / n + a.eps);
+    float v[V][8], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (first + i * kStep < n) {
+            x[i].get(v[i]);
+            if (a.residual) {
+                float w[8];
+                r[i].get(w);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[i][k] += w[k];
+                if (a.residual_out) store8(reinterpret_cast<Tr*>(a.residual_out) + row * a.ro_st + c0 + first + i * kStep, v[i]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum = fmaf(v[i][k], v[i][k], sum);
+        }
+    const float f = rsqrtf(across<W, false>(sum, s_sum) / n + a.eps);
     float amax = 0.f;
-    if (a.out_type == SSM_I8) {
-        for (int c = 8 * threadIdx.x; c < n; c += 8 * kThreads)
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(s_r[c + i] * f * (a.weight ? a.weight[c0 + c + i] : 1.f)));
-        amax = across<true>(amax, s_part);
-        if (threadIdx.x == 0) a.out_scale[row * a.n_groups + group] = __fdiv_rn(amax, 127.f);
-    }
-    const float inv = amax > 0.f ? __fdiv_rn(127.f, amax) : 0.f;
-    for (int c = 8 * threadIdx.x; c < n; c += 8 * kThreads) {
-        float y[8];
-        for (int i = 0; i < 8; ++i) y[i] = s_r[c + i] * f * (a.weight ? a.weight[c0 + c + i] : 1.f);
-        if (a.out_type == SSM_I8) {
-            uint32_t q[2] = {0, 0};
-            for (int i = 0; i < 8; ++i) q[i / 4] |= code(y[i], inv) << (8 * (i % 4));
-            *reinterpret_cast<uint2*>(reinterpret_cast<int8_t*>(a.out) + row * a.out_st + c0 + c) = make_uint2(q[0], q[1]);
-        } else {
-            store8(a.out, row * a.out_st + c0 + c, a.out_type == SSM_BF16, y);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (first + i * kStep < n) {
+            float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+            if (a.weight) {
+                Vec<float> q;
+                q.load(a.weight, c0 + first + i * kStep);
+                q.get(w);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[i][k] = v[i][k] * f * w[k];
+                if (kI8) amax = fmaxf(amax, fabsf(v[i][k]));
+            }
+            if constexpr (!kI8) store8(reinterpret_cast<To*>(a.out) + row * a.out_st + c0 + first + i * kStep, v[i]);
         }
+    if constexpr (kI8) {
+        amax = across<W, true>(amax, s_max);
+        if (tid == 0) a.out_scale[(int64_t)row * a.n_groups + group] = __fdiv_rn(amax, 127.f);
+        const float inv = amax > 0.f ? __fdiv_rn(127.f, amax) : 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (first + i * kStep < n) {
+                uint32_t q[2] = {0, 0};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) q[k / 4] |= code(v[i][k], inv) << (8 * (k % 4));
+                *reinterpret_cast<uint2*>(reinterpret_cast<int8_t*>(a.out) + row * a.out_st + c0 + first + i * kStep) = make_uint2(q[0], q[1]);
+            }
     }
+}
+
+template <typename Tx, typename Tr, typename To, int W, int V>
+void go(const NormArgs& a, cudaStream_t stream) {
+    const int64_t units = a.n_rows * a.n_groups;
+    k_norm_rms<Tx, Tr, To, W, V><<<(unsigned)(W == 1 ? (units + 3) / 4 : units), W == 1 ? 128 : 32 * W, 0, stream>>>(a);
+}
+
+template <typename Tx, typename Tr, typename To>
+void launch(const NormArgs& a, cudaStream_t stream) {
+    const int vecs = a.width / a.n_groups / 8;
+    const bool few = a.n_rows * a.n_groups <= 2 * kSms;
+    if (vecs <= 32) return go<Tx, Tr, To, 1, 1>(a, stream);
+    if (vecs <= 128 && !few) return go<Tx, Tr, To, 1, 4>(a, stream);
+    if (few) {                                          // a vector a thread, as far as 1024 threads go
+        if (vecs <= 64) return go<Tx, Tr, To, 2, 1>(a, stream);
+        if (vecs <= 128) return go<Tx, Tr, To, 4, 1>(a, stream);
+        if (vecs <= 256) return go<Tx, Tr, To, 8, 1>(a, stream);
+        if (vecs <= 512) return go<Tx, Tr, To, 16, 1>(a, stream);
+        if (vecs <= 1024) return go<Tx, Tr, To, 32, 1>(a, stream);
+    } else {
+        if (vecs <= 256) return go<Tx, Tr, To, 2, 4>(a, stream);
+        if (vecs <= 512) return go<Tx, Tr, To, 4, 4>(a, stream);
+        if (vecs <= 1024) return go<Tx, Tr, To, 8, 4>(a, stream);
+    }
+    if (vecs <= 2048) return go<Tx, Tr, To, 16, 4>(a, stream);
+    go<Tx, Tr, To, 32, 4>(a, stream);
+}
+
+template <typename Tx, typename Tr>
+void launch_out(const NormArgs& a, cudaStream_t stream) {
+    if (a.out_type == SSM_I8) launch<Tx, Tr, int8_t>(a, stream);
+    else if (a.out_type == SSM_BF16) launch<Tx, Tr, __nv_bfloat16>(a, stream);
+    else launch<Tx, Tr, float>(a, stream);
 }
 
 }  // namespace
 
 int launch_norm_rms(const NormArgs& a, cudaStream_t stream, const char** why) {
-    static ContextMemo attr_memo;
-    if (!opt_in_dynamic_smem(attr_memo, k_norm_rms, 32768 * 4, why)) return -1;
-    k_norm_rms<<<(unsigned)(a.n_rows * a.n_groups), kThreads, a.width / a.n_groups * 4, stream>>>(a);
+    if (a.in_type == SSM_BF16) {
+        if (a.res_type == SSM_BF16) launch_out<__nv_bfloat16, __nv_bfloat16>(a, stream);
+        else launch_out<__nv_bfloat16, float>(a, stream);
+    } else {
+        if (a.res_type == SSM_BF16) launch_out<float, __nv_bfloat16>(a, stream);
+        else launch_out<float, float>(a, stream);
+    }
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) return 0;
     *why = cudaGetErrorString(e);

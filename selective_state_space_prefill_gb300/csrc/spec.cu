@@ -1,87 +1,226 @@
 // spec.cu -- spec_probs (probabilities of logits at a temperature) and spec_verify (drafted tokens against the
 // target's probabilities).
 //
-// First forms: a CTA per row, and a CTA per request.
+// Both read rows of the vocabulary's length, a few or hundreds of them: a row is a thread-block cluster's, cut into
+// a slice per CTA, and what the CTAs have to know of each other (a maximum, sums) goes through distributed shared
+// memory.
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "ssm.h"
+
+namespace cg = cooperative_groups;
 
 namespace ssm {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kSms = 152;
 
 // ------------------------------------------------------------------ probabilities
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_spec_probs(const ProbsArgs a) {
-    __shared__ float s_m[kWarps], s_l[kWarps];
-    __shared__ int s_i[kWarps];
-    const int64_t row = blockIdx.x;
+// The larger one; a NaN wins.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+__device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7fc00000u); }
+
+// What a row's CTAs find out together: every CTA's value in its shared memory, combined by every thread.
+enum Kind { kMax, kSum, kLeast };
+template <Kind K, typename T>
+__device__ __forceinline__ T two(T a, T b) {
+    if constexpr (K == kMax) return max_nan(a, b);
+    else if constexpr (K == kSum) return a + b;
+    else return a < b ? a : b;
+}
+template <Kind K, typename T>
+__device__ T row_wide(T v, T* s_warp, T* s_cta, int ctas) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = two<K>(v, __shfl_xor_sync(~0u, v, o));
+    if (threadIdx.x % 32 == 0) s_warp[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = s_warp[threadIdx.x % kWarps];
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) v = two<K>(v, __shfl_xor_sync(~0u, v, o));
+    if (ctas == 1) return v;
+    auto cluster = cg::this_cluster();
+    if (threadIdx.x == 0) *s_cta = v;
+    cluster.sync();
+    v = *cluster.map_shared_rank(s_cta, threadIdx.x % ctas);
+    for (int o = ctas / 2; o > 0; o >>= 1) v = two<K>(v, __shfl_xor_sync(~0u, v, o));
+    return v;
+}
+
+template <typename T> __device__ __forceinline__ void load8(const T* p, float* v);
+template <> __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+template <> __device__ __forceinline__ void load8(const float* p, float* v) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// A row stays in registers between its maximum, its sum and its output: read once, written once.  V vectors of
+// eight logits a thread, from the row's first 16-byte border on; what lies before that and behind the last whole
+// vector (up to 14 logits) is one logit each for the first CTA's first threads.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads, V <= 4 ? 2 : 1) k_spec_probs(const ProbsArgs a, int ctas) {
+    __shared__ float s_max[kWarps], s_sum[kWarps], s_max_cta, s_sum_cta;
+    __shared__ int s_at[kWarps], s_at_cta;
+    const int64_t row = blockIdx.x / (unsigned)ctas;
+    const int rank = blockIdx.x % (unsigned)ctas, vocab = (int)a.vocab;
     const T* x = reinterpret_cast<const T*>(a.logits) + row * a.ld_in;
     float* p = a.probs + row * a.ld_out;
     const float t = a.temperature ? a.temperature[row] : 1.f;
-    const bool greedy = t <= 0x1p-100f;
-    // the maximum and its first place; a NaN wins
-    float m = -INFINITY;
-    int at = 0x7fffffff;
-    for (int i = threadIdx.x; i < a.vocab; i += kThreads) {
-        const float v = to_f32(x[i]);
-        if (!(v <= m)) {
-            if (m == m) m = v, at = i;
+    int head = (int)((16 - reinterpret_cast<uintptr_t>(x) % 16) % 16 / sizeof(T));
+    if (head > vocab) head = vocab;
+    const int vecs = (vocab - head) / 8, edge = vocab - 8 * vecs;
+    const int per = (vecs + ctas - 1) / ctas, first = rank * per, mine = min(per, vecs - first);
+    float v[V][8], w = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int at = threadIdx.x + i * kThreads;
+        if (at < mine) {
+            load8(x + head + 8 * (first + at), v[i]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = -INFINITY;
         }
     }
-    for (int o = 16; o > 0; o >>= 1) {
-        const float v = __shfl_xor_sync(~0u, m, o);
-        const int j = __shfl_xor_sync(~0u, at, o);
-        if (v != v || v > m || (v == m && j < at)) m = m != m ? m : v, at = j;
+    const bool on_edge = rank == 0 && threadIdx.x < edge;
+    const int w_at = threadIdx.x < head ? threadIdx.x : threadIdx.x + 8 * vecs;
+    if (on_edge) w = to_f32(x[w_at]);
+    float m = w;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = max_nan(m, v[i][k]);
+    m = row_wide<kMax>(m, s_max, &s_max_cta, ctas);
+
+    float inv = 1.f;
+    if (!(m < INFINITY) || t != t) {                    // NaN or +inf among the logits
+        inv = quiet_nan();
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+        w = 0.f;
+    } else if (t <= 0x1p-100f || m == -INFINITY) {      // greedy: 1 at the first largest; nothing to choose from: zeros
+        int least = on_edge && w == m && m > -INFINITY ? w_at : 0x7fffffff;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+#pragma unroll
+            for (int k = 7; k >= 0; --k)
+                if (v[i][k] == m && m > -INFINITY) least = min(least, head + 8 * (first + (int)threadIdx.x + i * kThreads) + k);
+        least = row_wide<kLeast>(least, s_at, &s_at_cta, ctas);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = head + 8 * (first + (int)threadIdx.x + i * kThreads) + k == least ? 1.f : 0.f;
+        w = w_at == least ? 1.f : 0.f;
+    } else {
+        const float f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
+        float l = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = ex2((v[i][k] - m) * f), l += v[i][k];
+        w = ex2((w - m) * f);
+        l = row_wide<kSum>(l + w, s_sum, &s_sum_cta, ctas);
+        inv = __fdiv_rn(1.f, l);
     }
-    if (threadIdx.x % 32 == 0) s_m[threadIdx.x / 32] = m, s_i[threadIdx.x / 32] = at;
-    __syncthreads();
-    m = s_m[0], at = s_i[0];
-    for (int w = 1; w < kWarps; ++w) {
-        const float v = s_m[w];
-        const int j = s_i[w];
-        if (v != v || v > m || (v == m && j < at)) m = m != m ? m : v, at = j;
+    if (on_edge) p[w_at] = w * inv;
+    float* const out = p + head + 8 * first;
+    const bool whole = reinterpret_cast<uintptr_t>(out) % 16 == 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int at = threadIdx.x + i * kThreads;
+        if (at >= mine) break;
+        float* to = out + 8 * at;
+        if (whole) {
+            reinterpret_cast<float4*>(to)[0] = make_float4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
+            reinterpret_cast<float4*>(to)[1] = make_float4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) to[k] = v[i][k] * inv;
+        }
     }
-    if (!(m < INFINITY) || t != t) {                     // NaN or +inf
-        for (int i = threadIdx.x; i < a.vocab; i += kThreads) p[i] = __uint_as_float(0x7fc00000u);
-        return;
+    if (ctas > 1) cg::this_cluster().sync();            // no CTA leaves while its values are read
+}
+
+// Rows longer than a cluster's registers hold: read three times, from L2 after the first.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_spec_probs_long(const ProbsArgs a, int ctas) {
+    __shared__ float s_max[kWarps], s_sum[kWarps], s_max_cta, s_sum_cta;
+    __shared__ int s_at[kWarps], s_at_cta;
+    const int64_t row = blockIdx.x / (unsigned)ctas;
+    const int rank = blockIdx.x % (unsigned)ctas, vocab = (int)a.vocab;
+    const T* x = reinterpret_cast<const T*>(a.logits) + row * a.ld_in;
+    float* p = a.probs + row * a.ld_out;
+    const float t = a.temperature ? a.temperature[row] : 1.f;
+    const int per = (vocab + ctas - 1) / ctas, lo = rank * per, hi = min(lo + per, vocab);
+    float m = -INFINITY;
+#pragma unroll 8
+    for (int i = lo + threadIdx.x; i < hi; i += kThreads) m = max_nan(m, to_f32(x[i]));
+    m = row_wide<kMax>(m, s_max, &s_max_cta, ctas);
+    if (!(m < INFINITY) || t != t) {
+        for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = quiet_nan();
+    } else if (t <= 0x1p-100f || m == -INFINITY) {
+        int least = 0x7fffffff;
+#pragma unroll 8
+        for (int i = lo + threadIdx.x; i < hi; i += kThreads)
+            if (to_f32(x[i]) == m && m > -INFINITY) least = min(least, i);
+        least = row_wide<kLeast>(least, s_at, &s_at_cta, ctas);
+        for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = i == least ? 1.f : 0.f;
+    } else {
+        const float f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
+        float l = 0.f;
+#pragma unroll 8
+        for (int i = lo + threadIdx.x; i < hi; i += kThreads) l += ex2((to_f32(x[i]) - m) * f);
+        l = row_wide<kSum>(l, s_sum, &s_sum_cta, ctas);
+        const float inv = __fdiv_rn(1.f, l);
+#pragma unroll 8
+        for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = ex2((to_f32(x[i]) - m) * f) * inv;
     }
-    if (greedy || m == -INFINITY) {
-        for (int i = threadIdx.x; i < a.vocab; i += kThreads) p[i] = i == at && m > -INFINITY ? 1.f : 0.f;
-        return;
-    }
-    const float f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
-    float l = 0.f;
-    for (int i = threadIdx.x; i < a.vocab; i += kThreads) l += ex2((to_f32(x[i]) - m) * f);
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-    if (threadIdx.x % 32 == 0) s_l[threadIdx.x / 32] = l;
-    __syncthreads();
-    l = 0.f;
-    for (int w = 0; w < kWarps; ++w) l += s_l[w];
-    const float inv = __fdiv_rn(1.f, l);
-    for (int i = threadIdx.x; i < a.vocab; i += kThreads) p[i] = ex2((to_f32(x[i]) - m) * f) * inv;
+    if (ctas > 1) cg::this_cluster().sync();
 }
 
 // ------------------------------------------------------------------ verification
-// A probability as an integer of 2^-62; negative ones and NaN are 0.
+// A probability as an integer of 2^-62, cut off; negative ones and NaN are 0.
 __device__ __forceinline__ uint64_t fixed(float p) { return p > 0.f ? __float2ull_rz(p * 0x1p62f) : 0ull; }
+__device__ __forceinline__ float uniform(float v) { return v > 0.f ? fminf(v, 0x1.fffffep-1f) : 0.f; }
 
 // The row that the next token is drawn from, element by element.
 struct Mass {
     const float *p, *q;
-    int64_t off;
-    __device__ __forceinline__ uint64_t operator()(int64_t i) const {
-        const uint64_t a = fixed(p[i]), b = q ? fixed(q[i]) : i == off ? 1ull << 62 : 0ull;
-        return a > b ? a - b : 0ull;
+    int off;
+    __device__ __forceinline__ uint64_t less(float pv, float qv, int i) const {
+        const uint64_t x = fixed(pv), y = q ? fixed(qv) : i == off ? 1ull << 62 : 0ull;
+        return x > y ? x - y : 0ull;
     }
+    __device__ __forceinline__ uint64_t operator()(int i) const { return less(p[i], q ? q[i] : 0.f, i); }
 };
 
-__global__ void __launch_bounds__(kThreads) k_spec_verify(const VerifyArgs a) {
+__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+
+// A cluster per request.  Sums are exact integers, so that the order of their parts and the cut do not matter: a
+// warp sums a stretch of the row, and the warp in whose stretch the border falls reads that again (from L2).
+__global__ void __launch_bounds__(kThreads) k_spec_verify(const VerifyArgs a, int ctas) {
+    constexpr int kBlock = 256;                         // elements that a warp takes at a time, eight loads a lane
     __shared__ int s_kept, s_n;
-    __shared__ uint64_t s_sum[kWarps];
-    __shared__ float s_mag[kWarps];
-    const int b = blockIdx.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    __shared__ uint64_t s_sum[kWarps], s_total;
+    __shared__ float s_mag[kWarps], s_mags;
+    const int b = blockIdx.x / (unsigned)ctas, rank = blockIdx.x % (unsigned)ctas;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, vocab = (int)a.vocab;
     const int32_t* draft = a.draft + (int64_t)b * a.n_max;
     const float* u = a.u + (int64_t)b * (a.n_max + 1);
     if (warp == 0) {
@@ -94,12 +233,11 @@ __global__ void __launch_bounds__(kThreads) k_spec_verify(const VerifyArgs a) {
             bool no = false, out = false;
             if (i < n) {
                 const int d = draft[i];
-                out = d < 0 || d >= a.vocab;
-                const float v = u[i], uu = v > 0.f ? fminf(v, 0x1.fffffep-1f) : 0.f;
+                out = d < 0 || d >= vocab;
                 float pd = out ? 0.f : a.p[b * a.p_sb + i * a.p_st + d], qd = 1.f;
                 if (a.q) qd = out ? 0.f : a.q[b * a.q_sb + i * a.q_st + d];
                 pd = pd > 0.f ? pd : 0.f, qd = qd > 0.f ? qd : 0.f;
-                no = !((double)uu * qd < (double)pd);       // 24 x 24 bits: exact
+                no = !((double)uniform(u[i]) * qd < (double)pd);        // 24 x 24 bits: exact
             }
             const unsigned first = __ballot_sync(~0u, no), outs = __ballot_sync(~0u, out);
             if (first) kept = i0 + __ffs(first) - 1;
@@ -108,83 +246,161 @@ __global__ void __launch_bounds__(kThreads) k_spec_verify(const VerifyArgs a) {
         }
         if (lane == 0) {
             s_kept = kept, s_n = n;
-            if (bad) atomicOr(a.status, (unsigned)SSM_DEV_BAD_INDEX);
+            if (bad && rank == 0) atomicOr(a.status, (unsigned)SSM_DEV_BAD_INDEX);
         }
     }
     __syncthreads();
     const int kept = s_kept, n = s_n;
+    int32_t* out = a.tokens + (int64_t)b * (a.n_max + 1);
+    if (rank == 0) {
+        for (int i = threadIdx.x; i <= a.n_max; i += kThreads)
+            if (i != kept) out[i] = i < kept ? draft[i] : -1;
+        if (threadIdx.x == 0) a.n_kept[b] = kept;
+    }
     Mass w{a.p + b * a.p_sb + kept * a.p_st, nullptr, -1};
     if (kept < n) {
         if (a.q) w.q = a.q + b * a.q_sb + kept * a.q_st;
         else w.off = draft[kept];
     }
-    const int64_t per = (a.vocab + kWarps - 1) / kWarps, lo = warp * per, hi = lo + per < a.vocab ? lo + per : a.vocab;
-    uint64_t total;
-    float mag;
+    const int stretches = ctas * kWarps, per = (vocab + stretches - 1) / stretches;
+    const int lo = min(vocab, (rank * kWarps + warp) * per), hi = min(vocab, lo + per);
+    // a block's elements of this lane, all loads under way at once
+    auto block = [&](int i0, uint64_t* m, float& mag) {
+        float pv[kBlock / 32], qv[kBlock / 32];
+#pragma unroll
+        for (int k = 0; k < kBlock / 32; ++k) {
+            const int i = i0 + 32 * k + lane;
+            pv[k] = i < hi ? w.p[i] : 0.f;
+            qv[k] = w.q && i < hi ? w.q[i] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kBlock / 32; ++k) {
+            m[k] = w.less(pv[k], qv[k], i0 + 32 * k + lane);
+            mag += pv[k] > 0.f ? pv[k] : 0.f;
+        }
+    };
+    uint64_t m[kBlock / 32], total, before;
+    float mags;
     for (int turn = 0;; ++turn) {
         uint64_t sum = 0;
-        mag = 0.f;
-        for (int64_t i = lo + lane; i < hi; i += 32) {
-            const float v = w.p[i];
-            sum += w(i), mag += v > 0.f ? v : 0.f;
+        float mag = 0.f;
+        for (int i0 = lo; i0 < hi; i0 += kBlock) {
+            block(i0, m, mag);
+#pragma unroll
+            for (int k = 0; k < kBlock / 32; ++k) sum += m[k];
         }
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o), mag += __shfl_xor_sync(~0u, mag, o);
-        __syncthreads();
+        sum = warp_sum(sum);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mag += __shfl_xor_sync(~0u, mag, o);
         if (lane == 0) s_sum[warp] = sum, s_mag[warp] = mag;
         __syncthreads();
-        total = 0, mag = 0.f;
-        for (int i = 0; i < kWarps; ++i) total += s_sum[i], mag += s_mag[i];
+        total = before = 0, mags = 0.f;
+        for (int i = 0; i < kWarps; ++i) {
+            before += i < warp ? s_sum[i] : 0;
+            total += s_sum[i], mags += s_mag[i];
+        }
+        if (ctas > 1) {
+            auto cluster = cg::this_cluster();
+            if (threadIdx.x == 0) s_total = total, s_mags = mags;
+            cluster.sync();
+            total = 0, mags = 0.f;
+            for (int r = 0; r < ctas; ++r) {
+                const uint64_t v = *cluster.map_shared_rank(&s_total, r);
+                before += r < rank ? v : 0;
+                total += v, mags += *cluster.map_shared_rank(&s_mags, r);
+            }
+            cluster.sync();                             // read by all: free to be written again, or left
+        } else {
+            __syncthreads();
+        }
         if (total > 0 || turn == 1 || (!w.q && w.off < 0)) break;
         w.q = nullptr, w.off = -1;                      // nothing left of p - q: p itself
     }
-    const float v = u[a.n_max], uu = v > 0.f ? fminf(v, 0x1.fffffep-1f) : 0.f;
+    if (total == 0 || !(mags < 3.99f)) {                // no distribution
+        if (rank == 0 && threadIdx.x == 0) out[kept] = -1;
+        return;
+    }
     // the first index whose running sum exceeds floor(u * total)
-    const uint64_t border = __umul64hi(__float2ull_rz(uu * 0x1p64f), total);
-    int32_t* out = a.tokens + (int64_t)b * (a.n_max + 1);
-    uint64_t before = 0;
-    for (int i = 0; i < warp; ++i) before += s_sum[i];
-    const bool some = total > 0 && mag < 3.99f;
-    if (some && before <= border && border < before + s_sum[warp]) {
-        for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-            uint64_t c = i0 + lane < hi ? w(i0 + lane) : 0ull;
+    const uint64_t border = __umul64hi(__float2ull_rz(uniform(u[a.n_max]) * 0x1p64f), total);
+    if (before > border || border >= before + s_sum[warp]) return;
+    for (int i0 = lo; i0 < hi; i0 += kBlock) {
+        float unused = 0.f;
+        block(i0, m, unused);
+        uint64_t all = 0;
+#pragma unroll
+        for (int k = 0; k < kBlock / 32; ++k) all += m[k];
+        all = warp_sum(all);
+        if (before + all <= border) {
+            before += all;
+            continue;
+        }
+#pragma unroll
+        for (int k = 0; k < kBlock / 32; ++k) {
+            uint64_t c = m[k];
+#pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint64_t t = __shfl_up_sync(~0u, c, o);
                 if (lane >= o) c += t;
             }
             const unsigned over = __ballot_sync(~0u, before + c > border);
             if (over) {
-                if (lane == 0) out[kept] = (int32_t)(i0 + __ffs(over) - 1);
-                break;
+                if (lane == 0) out[kept] = i0 + 32 * k + __ffs(over) - 1;
+                return;
             }
             before += __shfl_sync(~0u, c, 31);
         }
     }
-    if (threadIdx.x == 0) {
-        a.n_kept[b] = kept;
-        if (!some) out[kept] = -1;
-    }
-    for (int i = threadIdx.x; i <= a.n_max; i += kThreads)
-        if (i != kept) out[i] = i < kept ? draft[i] : -1;
 }
 
-int done(const char** why) {
-    const cudaError_t e = cudaGetLastError();
+template <typename... P, typename... A>
+int launch(void (*kern)(P...), int64_t rows, int ctas, cudaStream_t stream, const char** why, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)(rows * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    if (ctas > 1) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)ctas;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args..., ctas);
+    if (e == cudaSuccess) e = cudaGetLastError();
     if (e == cudaSuccess) return 0;
     *why = cudaGetErrorString(e);
     return -1;
 }
 
+// CTAs for a row of n elements: more while a CTA has `least` of them and the rows leave SMs idle.
+int ctas_for(int64_t rows, int64_t n, int64_t least) {
+    int c = 1;
+    while (c < 8 && rows * c < kSms && n >= 2 * c * least) c *= 2;
+    return c;
+}
+
+template <typename T>
+int probs(const ProbsArgs& a, cudaStream_t stream, const char** why) {
+    constexpr int kVec = 8 * kThreads;                  // logits of a vector for each thread
+    int ctas = ctas_for(a.n_rows, a.vocab, kVec);
+    while (ctas < 8 && a.vocab > 4 * kVec * ctas) ctas *= 2;
+    const int64_t each = (a.vocab / 8 + ctas - 1) / ctas * 8;
+    if (each <= kVec) return launch(k_spec_probs<T, 1>, a.n_rows, ctas, stream, why, a);
+    if (each <= 2 * kVec) return launch(k_spec_probs<T, 2>, a.n_rows, ctas, stream, why, a);
+    if (each <= 4 * kVec) return launch(k_spec_probs<T, 4>, a.n_rows, ctas, stream, why, a);
+    if (each <= 8 * kVec) return launch(k_spec_probs<T, 8>, a.n_rows, ctas, stream, why, a);
+    return launch(k_spec_probs_long<T>, a.n_rows, ctas, stream, why, a);
+}
+
 }  // namespace
 
 int launch_spec_probs(const ProbsArgs& a, bool in_bf16, cudaStream_t stream, const char** why) {
-    if (in_bf16) k_spec_probs<__nv_bfloat16><<<(unsigned)a.n_rows, kThreads, 0, stream>>>(a);
-    else k_spec_probs<float><<<(unsigned)a.n_rows, kThreads, 0, stream>>>(a);
-    return done(why);
+    return in_bf16 ? probs<__nv_bfloat16>(a, stream, why) : probs<float>(a, stream, why);
 }
 
 int launch_spec_verify(const VerifyArgs& a, cudaStream_t stream, const char** why) {
-    k_spec_verify<<<(unsigned)a.batch, kThreads, 0, stream>>>(a);
-    return done(why);
+    return launch(k_spec_verify, a.batch, ctas_for(a.batch * 4, a.vocab, 2048), stream, why, a);
 }
 
 }  // namespace ssm

@@ -13,6 +13,8 @@
 #include "kernels.h"
 #include "ssm.h"
 
+#include <type_traits>
+
 namespace ssm {
 namespace {
 
@@ -88,6 +90,7 @@ template <int NT> struct Shape {
 // weight into a range for each walker.  A CTA is a walker's, for one slice and one group of 8 NT rows of x.
 struct W4Plan {
     int tiles, walkers, m_blocks, slices;
+    int each, more;                                     // tiles of a walker; the first `more` walkers have one more
     int groups;                                         // of a row, in a slice
     int pitch_c, pitch_s, pitch_z, stage, stages;       // bytes of a row of codes, scales, zeros; of a stage
     int smem;
@@ -111,7 +114,7 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // Two codes, 16 bits apart and at bit 3, as bf16 16 + code (16 has room for four bits below its leading one), in
@@ -170,9 +173,9 @@ __device__ __forceinline__ uint32_t ld_u16(uint32_t at) {
     asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
-__device__ __forceinline__ float ld_f32(uint32_t at) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+__device__ __forceinline__ uint32_t ld_u32(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
 __device__ __forceinline__ float2 ld_f32x2(uint32_t at) {
@@ -215,7 +218,7 @@ __device__ __forceinline__ void store_out(const W4LinearArgs& a, int m, int64_t 
 template <int NT, int PG>
 __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a, const W4Plan plan, unsigned int* status) {
     using S = Shape<NT>;
-    constexpr int KC = S::kChunks, RT = kTiles;
+    constexpr int KC = S::kChunks;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* const stages = smem;
     float* const red = reinterpret_cast<float*>(smem + plan.stages * plan.stage);          // [2][kWarps][kPart]
@@ -223,9 +226,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a,
     Bars& bars = *reinterpret_cast<Bars*>(sums + kWarps * KC * 8 * NT);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int slice = blockIdx.x % plan.slices, id = blockIdx.x / plan.slices;
-    const int m0 = id % plan.m_blocks * 8 * NT, walker = id / plan.m_blocks;
-    const int tile0 = (int)((int64_t)plan.tiles * walker / plan.walkers), tile1 = (int)((int64_t)plan.tiles * (walker + 1) / plan.walkers);
+    const int slice = blockIdx.z, m0 = blockIdx.y * 8 * NT, walker = blockIdx.x;
+    const int tile0 = walker * plan.each + min(walker, plan.more), tile1 = tile0 + plan.each + (walker < plan.more);
+    // tiles of the turn that begins at one: two, but the last two by themselves, so that little is left to do once
+    // the last data are there
+    auto turn = [&](int tile) { return tile1 - tile > 2 ? kTiles : 1; };
     // this CTA's groups of a row
     const int g0 = slice * plan.groups, gn = min(plan.groups, a.w.K / (32 * PG) - g0);
     const int es = a.w.scale_bf16 ? 2 : 4, s_skip = g0 * es % 16, z_skip = g0 % 16;
@@ -242,8 +247,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a,
     if (warp < kWarps) {
         // ---- the products
         const int g = lane / 4, t = lane % 4;
-        // this warp's groups, dealt evenly: w0 of the CTA's before them
-        const int w0 = gn * warp / kWarps, wn = gn * (warp + 1) / kWarps - w0;
+        // this warp's groups, dealt evenly over the warps and over the SM's four parts that issue for every fourth
+        const int turn_of = warp % 4 * (kWarps / 4) + warp / 4;
+        const int w0 = gn * turn_of / kWarps, wn = gn * (turn_of + 1) / kWarps - w0;
         uint32_t x[KC][NT][4];
         if (a.x_i8) load_x<uint2>(a, m0 + g, (g0 + w0) * PG * 32 + 8 * t, wn * PG, x);
         else load_x<uint4>(a, m0 + g, (g0 + w0) * PG * 32 + 8 * t, wn * PG, x);
@@ -268,56 +274,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a,
         const int s_at = off_s + g * plan.pitch_s + s_skip + w0 * es, z_at = off_z + g * plan.pitch_z + z_skip + w0;
         uint32_t full_parity = 0, part_parity = 1;
         int s = 0, buf = 0;
-        for (int tile = tile0; tile < tile1; tile += RT) {
+        auto products = [&](auto many) {
+            constexpr int RT = decltype(many)::value;
             uint32_t st[RT], done[RT];
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                if (r > 0 && tile + r >= tile1) {       // an odd tile left: taken twice, stored once
-                    st[r] = st[0], done[r] = 0;
-                    continue;
-                }
                 wait(&bars.full[s], full_parity);
                 st[r] = smem_u32(stages) + s * plan.stage, done[r] = smem_u32(&bars.empty[s]);
                 if (++s == plan.stages) s = 0, full_parity ^= 1;
             }
             float acc[RT][NT][4] = {};
-            uint32_t q[RT][4];
 #pragma unroll
             for (int j = 0; j < KC / PG; ++j) {
                 if (j >= wn) break;
+                // a group's words, scales and zeros, all under way before the first is used
+                uint32_t q[RT][(PG + 1) / 2][4], sb[RT][2], zb[RT][2] = {};
+                float2 xs[NT];
+#pragma unroll
+                for (int c = 0; c < PG; c += 2)         // two chunks' words; of a group of one chunk the first counts
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) ldmatrix4(q[r][c / 2], st[r] + row_at + (j * PG + c) * 16);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const uint32_t sp = st[r] + s_at + j * es, zp = st[r] + z_at + j;
+                    if (a.w.scale_bf16) sb[r][0] = ld_u16(sp) << 16, sb[r][1] = ld_u16(sp + 8 * plan.pitch_s) << 16;
+                    else sb[r][0] = ld_u32(sp), sb[r][1] = ld_u32(sp + 8 * plan.pitch_s);
+                    if (a.w.zeros) zb[r][0] = ld_u8(zp), zb[r][1] = ld_u8(zp + 8 * plan.pitch_z);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) xs[n] = ld_f32x2(my_sums + (j * NT + n) * 32);
                 float part[RT][NT][4] = {};
 #pragma unroll
-                for (int c = j * PG; c < (j + 1) * PG; ++c) {
-                    if (c % 2 == 0) {                   // two chunks' words
-#pragma unroll
-                        for (int r = 0; r < RT; ++r) ldmatrix4(q[r], st[r] + row_at + c * 16);
-                    }
+                for (int c = 0; c < PG; ++c)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int r = 0; r < RT; ++r) {
-                            const uint32_t u = q[r][c % 2 * 2] >> (8 * h), v = q[r][c % 2 * 2 + 1] >> (8 * h);
-                            const uint32_t a0 = two_codes(u << 3), a1 = two_codes(v << 3), a2 = two_codes(u >> 1), a3 = two_codes(v >> 1);
+                            const uint32_t u = q[r][c / 2][c % 2 * 2], v = q[r][c / 2][c % 2 * 2 + 1];
+                            const uint32_t a0 = two_codes(h ? u >> 5 : u << 3), a1 = two_codes(h ? v >> 5 : v << 3);
+                            const uint32_t a2 = two_codes(h ? u >> 9 : u >> 1), a3 = two_codes(h ? v >> 9 : v >> 1);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) mma(part[r][n], a0, a1, a2, a3, x[c][n][2 * h], x[c][n][2 * h + 1]);
+                            for (int n = 0; n < NT; ++n)
+                                mma(part[r][n], a0, a1, a2, a3, x[j * PG + c][n][2 * h], x[j * PG + c][n][2 * h + 1]);
                         }
-                }
                 // the group's sums times its scales
-                float2 xs[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) xs[n] = ld_f32x2(my_sums + (j * NT + n) * 32);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
-                    const uint32_t sp = st[r] + s_at + j * es, zp = st[r] + z_at + j;
-                    float s0, s1, z0 = 24.f, z1 = 24.f;
-                    if (a.w.scale_bf16) {
-                        s0 = __uint_as_float(ld_u16(sp) << 16), s1 = __uint_as_float(ld_u16(sp + 8 * plan.pitch_s) << 16);
-                    } else {
-                        s0 = ld_f32(sp), s1 = ld_f32(sp + 8 * plan.pitch_s);
-                    }
+                    const float s0 = __uint_as_float(sb[r][0]), s1 = __uint_as_float(sb[r][1]);
+                    float z0 = 24.f, z1 = 24.f;
                     if (a.w.zeros) {                    // 16 + zero, as the codes
-                        z0 = __uint_as_float(0x41800000u | (ld_u8(zp) & 15u) << 19);
-                        z1 = __uint_as_float(0x41800000u | (ld_u8(zp + 8 * plan.pitch_z) & 15u) << 19);
+                        z0 = __uint_as_float(0x41800000u | (zb[r][0] & 15u) << 19);
+                        z1 = __uint_as_float(0x41800000u | (zb[r][1] & 15u) << 19);
                     }
                     float(&p)[NT][4] = part[r];
 #pragma unroll
@@ -338,23 +345,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a,
             __syncwarp();
             if (lane == 0) {
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
-                    if (done[r]) arrive_at(done[r]);
+                for (int r = 0; r < RT; ++r) arrive_at(done[r]);
             }
             wait(&bars.part_empty[buf], part_parity);
-            {
-                uint32_t to = smem_u32(red + (buf * kWarps + warp) * S::kPart + 2 * t * kCol + g);
+            uint32_t to = smem_u32(red + (buf * kWarps + warp) * S::kPart + 2 * t * kCol + g);
 #pragma unroll
-                for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < RT; ++r)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n, to += 8 * kCol * 4) {
-                        st_f32(to, acc[r][n][0]), st_f32(to + kCol * 4, acc[r][n][1]);
-                        st_f32(to + 32, acc[r][n][2]), st_f32(to + kCol * 4 + 32, acc[r][n][3]);
-                    }
-            }
+                for (int n = 0; n < NT; ++n, to += 8 * kCol * 4) {
+                    st_f32(to, acc[r][n][0]), st_f32(to + kCol * 4, acc[r][n][1]);
+                    st_f32(to + 32, acc[r][n][2]), st_f32(to + kCol * 4 + 32, acc[r][n][3]);
+                }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.part_full[buf]);
             buf ^= 1, part_parity ^= buf == 0;
+        };
+        for (int tile = tile0; tile < tile1; tile += turn(tile)) {
+            if (turn(tile) == kTiles) products(std::integral_constant<int, kTiles>());
+            else products(std::integral_constant<int, 1>());
         }
     } else {
         const int me = threadIdx.x - 32 * kWarps;
@@ -389,23 +397,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a,
         uint32_t parity = 0;
         int buf = 0;
         for (int s = 0; s < plan.stages && load < tile1; ++s) fetch();
-        for (int tile = tile0; tile < tile1; tile += RT) {
+        const int columns = min(8 * NT, a.M - m0);      // rows of x
+        for (int tile = tile0; tile < tile1; tile += turn(tile)) {
             // the tiles that take this turn's stages: after its products, before its sums
-            for (int r = 0; r < RT && load < tile1; ++r) fetch();
+            for (int r = 0; r < turn(tile) && load < tile1; ++r) fetch();
             wait(&bars.part_full[buf], parity);
-            for (int e = me; e < S::kOut; e += 32 * kServe) {
-                const float* from = red + buf * kWarps * S::kPart + e / kRows * kCol + e % kRows;
-                float p[kWarps], v = 0.f;
+            const float* const parts = red + buf * kWarps * S::kPart;
+            auto finish = [&](int r, int m, int row, float v) {
+                const int64_t n = (int64_t)(tile + r) * kRows + row;
+                if (n >= a.w.N) return;
+                if (a.x_scale && a.x_blocks == 1) v *= __ldg(a.x_scale + m0 + m);
+                if (plan.slices > 1) a.parts[((int64_t)slice * a.M + m0 + m) * a.w.N + n] = v;
+                else store_out(a, m0 + m, n, v);
+            };
+            const int outs = turn(tile) * columns * kRows;
+            if (outs <= 8 * kServe) {                   // few: four threads for each
+                const int e = me / 4, col = e / kRows, r = col / columns;
+                float v = 0.f;
+                if (e < outs) {
+                    const float* from = parts + (r * 8 * NT + col - r * columns) * kCol + e % kRows;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) p[w] = from[w * S::kPart];
+                    for (int w = 0; w < kWarps / 4; ++w) v += from[(me % 4 + 4 * w) * S::kPart];
+                }
+                v += __shfl_xor_sync(~0u, v, 1);
+                v += __shfl_xor_sync(~0u, v, 2);
+                if (e < outs && me % 4 == 0) finish(r, col - r * columns, e % kRows, v);
+            } else {
+                for (int e = me; e < outs; e += 32 * kServe) {
+                    const int col = e / kRows, r = col >= columns;
+                    const float* from = parts + (r * 8 * NT + col - r * columns) * kCol + e % kRows;
+                    float p[kWarps], v = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) v += p[w];
-                const int r = e / (128 * NT), m = m0 + e / kRows % (8 * NT);
-                const int64_t n = (int64_t)(tile + r) * kRows + e % kRows;
-                if (m >= a.M || tile + r >= tile1 || n >= a.w.N) continue;
-                if (a.x_scale && a.x_blocks == 1) v *= __ldg(a.x_scale + m);
-                if (plan.slices > 1) a.parts[((int64_t)slice * a.M + m) * a.w.N + n] = v;
-                else store_out(a, m, n, v);
+                    for (int w = 0; w < kWarps; ++w) p[w] = from[w * S::kPart];
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) v += p[w];
+                    finish(r, col - r * columns, e % kRows, v);
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.part_empty[buf]);
@@ -438,6 +465,7 @@ W4Plan plan_of(int M, const W4Weight& w, int slices) {
     p.walkers = kSms / (p.slices * p.m_blocks);
     if (p.walkers < 1) p.walkers = 1;
     if (p.walkers > p.tiles) p.walkers = p.tiles;
+    p.each = p.tiles / p.walkers, p.more = p.tiles % p.walkers;
     // 16 bytes past a multiple of 128: rows of a column of words fall on different banks.  A slice may start
     // inside 16 bytes of scales or zeros, and two chunks' words are read together.
     p.pitch_c = (p.groups * w.group / 2 + 16 + 127) / 128 * 128 + 16;
@@ -473,7 +501,7 @@ int linear(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, con
     auto kern = k_w4_linear<NT, PG>;
     static ContextMemo attr_memo;
     if (!opt_in_dynamic_smem(attr_memo, kern, kMaxSmem, why)) return -1;
-    kern<<<(unsigned)(p.walkers * p.m_blocks * p.slices), kThreads, p.smem, stream>>>(a, p, status);
+    kern<<<dim3((unsigned)p.walkers, (unsigned)p.m_blocks, (unsigned)p.slices), kThreads, p.smem, stream>>>(a, p, status);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && p.slices > 1) {
         cudaLaunchConfig_t cfg = {};
