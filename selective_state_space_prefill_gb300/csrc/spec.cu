@@ -27,6 +27,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7fc00000u); }
 
+// One float, whatever stands beside it: plain stores of four neighbours, next to one of them as a float4 in the other
+// branch, came out as one 16-byte store, which faults where the row is not aligned.
+__device__ __forceinline__ void store1(float* p, float v) { asm volatile("st.global.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory"); }
+
 // What a row's CTAs find out together: every CTA's value in its shared memory, combined by every thread.
 enum Kind { kMax, kSum, kLeast };
 template <Kind K, typename T>
@@ -53,23 +57,35 @@ __device__ T row_wide(T v, T* s_warp, T* s_cta, int ctas) {
     return v;
 }
 
-template <typename T> __device__ __forceinline__ void load8(const T* p, float* v);
-template <> __device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-}
-template <> __device__ __forceinline__ void load8(const float* p, float* v) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
+// Eight logits as they came.
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+    uint4 q;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void none() { q = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }   // -inf
+    __device__ __forceinline__ float at(int k) const {
+        const uint32_t w = k / 2 == 0 ? q.x : k / 2 == 1 ? q.y : k / 2 == 2 ? q.z : q.w;
+        return __uint_as_float(k % 2 ? w & 0xffff0000u : w << 16);
+    }
+};
+template <> struct Raw<float> {
+    float4 q[2];
+    __device__ __forceinline__ void load(const float* p) {
+        q[0] = __ldg(reinterpret_cast<const float4*>(p)), q[1] = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void none() { q[0] = q[1] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
+    __device__ __forceinline__ float at(int k) const {
+        const float4& v = q[k / 4];
+        return k % 4 == 0 ? v.x : k % 4 == 1 ? v.y : k % 4 == 2 ? v.z : v.w;
+    }
+};
 
-// A row stays in registers between its maximum, its sum and its output: read once, written once.  V vectors of
-// eight logits a thread, from the row's first 16-byte border on; what lies before that and behind the last whole
-// vector (up to 14 logits) is one logit each for the first CTA's first threads.
+// A row stays in registers, as it came, between its maximum, its sum and its output: read once, written once.  (The
+// powers are taken twice: their unit would do three times as many in the time that the row's bytes take.)  V
+// vectors of eight logits a thread, from the row's first 16-byte border on; what lies before that and behind the
+// last whole vector (up to 14 logits) is one logit each for the first CTA's first threads.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, V <= 4 ? 2 : 1) k_spec_probs(const ProbsArgs a, int ctas) {
+__global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 2 : 1) k_spec_probs(const ProbsArgs a, int ctas) {
     __shared__ float s_max[kWarps], s_sum[kWarps], s_max_cta, s_sum_cta;
     __shared__ int s_at[kWarps], s_at_cta;
     const int64_t row = blockIdx.x / (unsigned)ctas;
@@ -81,73 +97,64 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 2 : 1) k_spec_probs(const P
     if (head > vocab) head = vocab;
     const int vecs = (vocab - head) / 8, edge = vocab - 8 * vecs;
     const int per = (vecs + ctas - 1) / ctas, first = rank * per, mine = min(per, vecs - first);
-    float v[V][8], w = -INFINITY;
+    Raw<T> v[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int at = threadIdx.x + i * kThreads;
-        if (at < mine) {
-            load8(x + head + 8 * (first + at), v[i]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = -INFINITY;
-        }
+        if (at < mine) v[i].load(x + head + 8 * (first + at));
+        else v[i].none();
     }
     const bool on_edge = rank == 0 && threadIdx.x < edge;
     const int w_at = threadIdx.x < head ? threadIdx.x : threadIdx.x + 8 * vecs;
-    if (on_edge) w = to_f32(x[w_at]);
+    const float w = on_edge ? to_f32(x[w_at]) : -INFINITY;
     float m = w;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m = max_nan(m, v[i][k]);
+        for (int k = 0; k < 8; ++k) m = max_nan(m, v[i].at(k));
     m = row_wide<kMax>(m, s_max, &s_max_cta, ctas);
 
-    float inv = 1.f;
-    if (!(m < INFINITY) || t != t) {                    // NaN or +inf among the logits
-        inv = quiet_nan();
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
-        w = 0.f;
+    // p = 2^((x - m) f) inv, or 1 at one place, or the same everywhere
+    float f = 0.f, inv = quiet_nan();
+    int least = -1;
+    if (!(m < INFINITY) || t != t) {                    // NaN or +inf among the logits: NaN
     } else if (t <= 0x1p-100f || m == -INFINITY) {      // greedy: 1 at the first largest; nothing to choose from: zeros
-        int least = on_edge && w == m && m > -INFINITY ? w_at : 0x7fffffff;
+        inv = 0.f;
+        least = 0x7fffffff;
+        if (m > -INFINITY) {
+            if (on_edge && w == m) least = w_at;
 #pragma unroll
-        for (int i = V - 1; i >= 0; --i)
+            for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int k = 7; k >= 0; --k)
-                if (v[i][k] == m && m > -INFINITY) least = min(least, head + 8 * (first + (int)threadIdx.x + i * kThreads) + k);
+                for (int k = 0; k < 8; ++k)
+                    if (v[i].at(k) == m) least = min(least, head + 8 * (first + (int)threadIdx.x + i * kThreads) + k);
+        }
         least = row_wide<kLeast>(least, s_at, &s_at_cta, ctas);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = head + 8 * (first + (int)threadIdx.x + i * kThreads) + k == least ? 1.f : 0.f;
-        w = w_at == least ? 1.f : 0.f;
     } else {
-        const float f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
-        float l = 0.f;
+        f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
+        float l = ex2((w - m) * f);
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = ex2((v[i][k] - m) * f), l += v[i][k];
-        w = ex2((w - m) * f);
-        l = row_wide<kSum>(l + w, s_sum, &s_sum_cta, ctas);
-        inv = __fdiv_rn(1.f, l);
+            for (int k = 0; k < 8; ++k) l += ex2((v[i].at(k) - m) * f);
+        inv = __fdiv_rn(1.f, row_wide<kSum>(l, s_sum, &s_sum_cta, ctas));
     }
-    if (on_edge) p[w_at] = w * inv;
-    float* const out = p + head + 8 * first;
-    const bool whole = reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    const bool powers = f > 0.f;                        // else inv everywhere, but 1 at `least`
+    auto prob = [&](float x, int at) { return powers ? ex2((x - m) * f) * inv : at == least ? 1.f : inv; };
+    if (on_edge) p[w_at] = prob(w, w_at);
+    const int start = head + 8 * first;
+    const bool whole = reinterpret_cast<uintptr_t>(p + start) % 16 == 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int at = threadIdx.x + i * kThreads;
         if (at >= mine) break;
-        float* to = out + 8 * at;
-        if (whole) {
-            reinterpret_cast<float4*>(to)[0] = make_float4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-            reinterpret_cast<float4*>(to)[1] = make_float4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv);
-        } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) to[k] = v[i][k] * inv;
+        for (int k = 0; k < 8; k += 4) {
+            float* to = p + start + 8 * at + k;
+            const float4 o = make_float4(prob(v[i].at(k), start + 8 * at + k), prob(v[i].at(k + 1), start + 8 * at + k + 1),
+                                         prob(v[i].at(k + 2), start + 8 * at + k + 2), prob(v[i].at(k + 3), start + 8 * at + k + 3));
+            if (whole) *reinterpret_cast<float4*>(to) = o;
+            else store1(to, o.x), store1(to + 1, o.y), store1(to + 2, o.z), store1(to + 3, o.w);
         }
     }
     if (ctas > 1) cg::this_cluster().sync();            // no CTA leaves while its values are read
@@ -223,7 +230,9 @@ __global__ void __launch_bounds__(kThreads) k_spec_verify(const VerifyArgs a, in
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, vocab = (int)a.vocab;
     const int32_t* draft = a.draft + (int64_t)b * a.n_max;
     const float* u = a.u + (int64_t)b * (a.n_max + 1);
+    const float draw = uniform(u[a.n_max]);             // asked for now, used at the end
     if (warp == 0) {
+        const int d0 = lane < a.n_max ? draft[lane] : 0;                // as n_draft, not after it
         int n = a.n_draft ? a.n_draft[b] : a.n_max;
         bool bad = n < 0 || n > a.n_max;
         n = n < 0 ? 0 : n > a.n_max ? a.n_max : n;
@@ -232,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) k_spec_verify(const VerifyArgs a, in
             const int i = i0 + lane;
             bool no = false, out = false;
             if (i < n) {
-                const int d = draft[i];
+                const int d = i0 == 0 ? d0 : draft[i];
                 out = d < 0 || d >= vocab;
                 float pd = out ? 0.f : a.p[b * a.p_sb + i * a.p_st + d], qd = 1.f;
                 if (a.q) qd = out ? 0.f : a.q[b * a.q_sb + i * a.q_st + d];
@@ -321,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) k_spec_verify(const VerifyArgs a, in
         return;
     }
     // the first index whose running sum exceeds floor(u * total)
-    const uint64_t border = __umul64hi(__float2ull_rz(uniform(u[a.n_max]) * 0x1p64f), total);
+    const uint64_t border = __umul64hi(__float2ull_rz(draw * 0x1p64f), total);
     if (before > border || border >= before + s_sum[warp]) return;
     for (int i0 = lo; i0 < hi; i0 += kBlock) {
         float unused = 0.f;
@@ -383,8 +392,9 @@ int ctas_for(int64_t rows, int64_t n, int64_t least) {
 template <typename T>
 int probs(const ProbsArgs& a, cudaStream_t stream, const char** why) {
     constexpr int kVec = 8 * kThreads;                  // logits of a vector for each thread
+    constexpr int kMost = sizeof(T) == 2 ? 8 : 4;       // vectors with which two CTAs fit an SM
     int ctas = ctas_for(a.n_rows, a.vocab, kVec);
-    while (ctas < 8 && a.vocab > 4 * kVec * ctas) ctas *= 2;
+    while (ctas < 8 && a.vocab > (int64_t)kMost * kVec * ctas) ctas *= 2;
     const int64_t each = (a.vocab / 8 + ctas - 1) / ctas * 8;
     if (each <= kVec) return launch(k_spec_probs<T, 1>, a.n_rows, ctas, stream, why, a);
     if (each <= 2 * kVec) return launch(k_spec_probs<T, 2>, a.n_rows, ctas, stream, why, a);
@@ -400,7 +410,8 @@ int launch_spec_probs(const ProbsArgs& a, bool in_bf16, cudaStream_t stream, con
 }
 
 int launch_spec_verify(const VerifyArgs& a, cudaStream_t stream, const char** why) {
-    return launch(k_spec_verify, a.batch, ctas_for(a.batch * 4, a.vocab, 2048), stream, why, a);
+    // three CTAs fit an SM: up to four clusters' worth of requests before a row goes to fewer CTAs
+    return launch(k_spec_verify, a.batch, ctas_for((a.batch + 3) / 4, a.vocab, 2048), stream, why, a);
 }
 
 }  // namespace ssm
