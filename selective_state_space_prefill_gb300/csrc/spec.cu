@@ -63,6 +63,15 @@ template <> struct Raw<__nv_bfloat16> {
     uint4 q;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = __ldg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void none() { q = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }   // -inf
+    __device__ __forceinline__ float most() const {     // of the eight; a NaN wins
+        const uint32_t m = max2(max2(q.x, q.y), max2(q.z, q.w));
+        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t m;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+        return m;
+    }
     __device__ __forceinline__ float at(int k) const {
         const uint32_t w = k / 2 == 0 ? q.x : k / 2 == 1 ? q.y : k / 2 == 2 ? q.z : q.w;
         return __uint_as_float(k % 2 ? w & 0xffff0000u : w << 16);
@@ -74,6 +83,12 @@ template <> struct Raw<float> {
         q[0] = __ldg(reinterpret_cast<const float4*>(p)), q[1] = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
     __device__ __forceinline__ void none() { q[0] = q[1] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
+    __device__ __forceinline__ float most() const {
+        float m = at(0);
+#pragma unroll
+        for (int k = 1; k < 8; ++k) m = max_nan(m, at(k));
+        return m;
+    }
     __device__ __forceinline__ float at(int k) const {
         const float4& v = q[k / 4];
         return k % 4 == 0 ? v.x : k % 4 == 1 ? v.y : k % 4 == 2 ? v.z : v.w;
@@ -109,9 +124,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 2 : 1) k_spec_
     const float w = on_edge ? to_f32(x[w_at]) : -INFINITY;
     float m = w;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m = max_nan(m, v[i].at(k));
+    for (int i = 0; i < V; ++i) m = max_nan(m, v[i].most());
     m = row_wide<kMax>(m, s_max, &s_max_cta, ctas);
 
     // p = 2^((x - m) f) inv, or 1 at one place, or the same everywhere
@@ -139,24 +152,26 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 2 : 1) k_spec_
             for (int k = 0; k < 8; ++k) l += ex2((v[i].at(k) - m) * f);
         inv = __fdiv_rn(1.f, row_wide<kSum>(l, s_sum, &s_sum_cta, ctas));
     }
-    const bool powers = f > 0.f;                        // else inv everywhere, but 1 at `least`
-    auto prob = [&](float x, int at) { return powers ? ex2((x - m) * f) * inv : at == least ? 1.f : inv; };
-    if (on_edge) p[w_at] = prob(w, w_at);
     const int start = head + 8 * first;
     const bool whole = reinterpret_cast<uintptr_t>(p + start) % 16 == 0;
+    auto write = [&](auto prob) {
+        if (on_edge) p[w_at] = prob(w, w_at);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int at = threadIdx.x + i * kThreads;
-        if (at >= mine) break;
+        for (int i = 0; i < V; ++i) {
+            const int at = threadIdx.x + i * kThreads;
+            if (at >= mine) break;
 #pragma unroll
-        for (int k = 0; k < 8; k += 4) {
-            float* to = p + start + 8 * at + k;
-            const float4 o = make_float4(prob(v[i].at(k), start + 8 * at + k), prob(v[i].at(k + 1), start + 8 * at + k + 1),
-                                         prob(v[i].at(k + 2), start + 8 * at + k + 2), prob(v[i].at(k + 3), start + 8 * at + k + 3));
-            if (whole) *reinterpret_cast<float4*>(to) = o;
-            else store1(to, o.x), store1(to + 1, o.y), store1(to + 2, o.z), store1(to + 3, o.w);
+            for (int k = 0; k < 8; k += 4) {
+                const int n = start + 8 * at + k;
+                const float4 o = make_float4(prob(v[i].at(k), n), prob(v[i].at(k + 1), n + 1), prob(v[i].at(k + 2), n + 2),
+                                             prob(v[i].at(k + 3), n + 3));
+                if (whole) *reinterpret_cast<float4*>(p + n) = o;
+                else store1(p + n, o.x), store1(p + n + 1, o.y), store1(p + n + 2, o.z), store1(p + n + 3, o.w);
+            }
         }
-    }
+    };
+    if (f > 0.f) write([&](float x, int) { return ex2((x - m) * f) * inv; });
+    else write([&](float, int at) { return at == least ? 1.f : inv; });
     if (ctas > 1) cg::this_cluster().sync();            // no CTA leaves while its values are read
 }
 
@@ -198,8 +213,16 @@ __global__ void __launch_bounds__(kThreads) k_spec_probs_long(const ProbsArgs a,
 }
 
 // ------------------------------------------------------------------ verification
-// A probability as an integer of 2^-62, cut off; negative ones and NaN are 0.
-__device__ __forceinline__ uint64_t fixed(float p) { return p > 0.f ? __float2ull_rz(p * 0x1p62f) : 0ull; }
+// A probability as an integer of 2^-62, cut off: the mantissa with its leading one at the top of 64 bits, which is
+// right for [2, 4), shifted down by what the exponent is below that.  Negative ones and NaN shift by more than 64
+// and are 0, as is what is too small.  (A conversion to 64 bits is an instruction, but one that this GPU does at
+// a few elements a clock.)
+__device__ __forceinline__ uint64_t fixed(float p) {
+    const uint32_t bits = __float_as_uint(p);
+    uint64_t v;
+    asm("shr.u64 %0, %1, %2;" : "=l"(v) : "l"((uint64_t)(bits << 8 | 0x80000000u) << 32), "r"(128u - (bits >> 23)));
+    return v;
+}
 __device__ __forceinline__ float uniform(float v) { return v > 0.f ? fminf(v, 0x1.fffffep-1f) : 0.f; }
 
 // The row that the next token is drawn from, element by element.
@@ -382,10 +405,10 @@ int launch(void (*kern)(P...), int64_t rows, int ctas, cudaStream_t stream, cons
     return -1;
 }
 
-// CTAs for a row of n elements: more while a CTA has `least` of them and the rows leave SMs idle.
-int ctas_for(int64_t rows, int64_t n, int64_t least) {
+// CTAs for a row of n elements: more while each still has `least` of them and `each` fit an SM.
+int ctas_for(int64_t rows, int64_t n, int64_t least, int each) {
     int c = 1;
-    while (c < 8 && rows * c < kSms && n >= 2 * c * least) c *= 2;
+    while (c < 8 && rows * 2 * c <= each * kSms && n >= 2 * c * least) c *= 2;
     return c;
 }
 
@@ -393,7 +416,7 @@ template <typename T>
 int probs(const ProbsArgs& a, cudaStream_t stream, const char** why) {
     constexpr int kVec = 8 * kThreads;                  // logits of a vector for each thread
     constexpr int kMost = sizeof(T) == 2 ? 8 : 4;       // vectors with which two CTAs fit an SM
-    int ctas = ctas_for(a.n_rows, a.vocab, kVec);
+    int ctas = ctas_for(a.n_rows, a.vocab, kVec, 2);
     while (ctas < 8 && a.vocab > (int64_t)kMost * kVec * ctas) ctas *= 2;
     const int64_t each = (a.vocab / 8 + ctas - 1) / ctas * 8;
     if (each <= kVec) return launch(k_spec_probs<T, 1>, a.n_rows, ctas, stream, why, a);
@@ -410,8 +433,7 @@ int launch_spec_probs(const ProbsArgs& a, bool in_bf16, cudaStream_t stream, con
 }
 
 int launch_spec_verify(const VerifyArgs& a, cudaStream_t stream, const char** why) {
-    // three CTAs fit an SM: up to four clusters' worth of requests before a row goes to fewer CTAs
-    return launch(k_spec_verify, a.batch, ctas_for((a.batch + 3) / 4, a.vocab, 2048), stream, why, a);
+    return launch(k_spec_verify, a.batch, ctas_for(a.batch, a.vocab, 2048, 3), stream, why, a);
 }
 
 }  // namespace ssm
