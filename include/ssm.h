@@ -669,7 +669,7 @@ size_t w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);
 /*
  * w4_linear -- out[m][n] = sum_k x[m][k] W[n][k] with a 4-bit W, for the few rows of a decode step.  Products
  * of x and codes are exact and are summed in fp32 within a group, the groups' sums times their scales in fp32, in
- * an order that the sizes alone choose.  An infinity or NaN in a row of x makes that row's outputs NaN.
+ * an order that the sizes alone choose.  With an infinity or NaN in a row of x none of that row's outputs is finite.
  *
  *   M                    0 .. 256 (0 does nothing); more return SSM_ERR_UNSUPPORTED: they belong to a product with
  *                        the whole weight

@@ -9,11 +9,12 @@
 // being held in the same order), and become bf16 numbers 16 + code in two operations for two codes.  The group's
 // sum is multiplied by its scale in fp32.  The warps' sums of a block meet in shared memory; where a row of x is
 // more than 16 warps hold, slices of the rows go to different CTAs and a second kernel adds their sums.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "ssm.h"
-
-#include <type_traits>
+#include "w4.cuh"
 
 namespace ssm {
 namespace {
@@ -124,21 +125,6 @@ __device__ __forceinline__ uint32_t two_codes(uint32_t w) {
     asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w), "r"(0x00780078u), "r"(0x41804180u));
     return v;
 }
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float i8_at(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
-
-// Eight consecutive elements of x as the pairs (0, 4), (1, 5), (2, 6), (3, 7), as the codes come out of a word.
-__device__ __forceinline__ void x_pairs(uint4 q, uint32_t (&r)[4]) {
-    r[0] = __byte_perm(q.x, q.z, 0x5410), r[1] = __byte_perm(q.x, q.z, 0x7632);
-    r[2] = __byte_perm(q.y, q.w, 0x5410), r[3] = __byte_perm(q.y, q.w, 0x7632);
-}
-__device__ __forceinline__ void x_pairs(uint2 q, uint32_t (&r)[4]) {    // whole numbers up to 128: exact in bf16
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = bf16_pair(i8_at(q.x, i), i8_at(q.y, i));
-}
 // A warp's slice of x: elements k .. of rows m, m + 8, ..., all loads in flight at once.  What is not there (rows
 // from M on, chunks from n on) is loaded from the first place and counts as 0.
 template <typename Q, int KC, int NT>
@@ -186,32 +172,6 @@ __device__ __forceinline__ float2 ld_f32x2(uint32_t at) {
 __device__ __forceinline__ void st_f32(uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); }
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Waits that give up after two seconds, report it and are not waited for again: every loop still ends.  The timer
-// takes longer to read than most waits, so it is not looked at before 4096 tries.
-struct Waiter {
-    unsigned int* status;
-    bool dead = false;
-    __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-        if (dead) return;
-        uint64_t t0 = 0;
-        for (uint32_t spin = 0; !mbar_try_wait(bar, parity); ++spin)
-            if ((spin & 4095u) == 4095u) {
-                const uint64_t now = globaltimer_ns();
-                if (t0 == 0) t0 = now;
-                if (now - t0 > 2000000000ull) {
-                    dead = true;
-                    atomicOr(status, (unsigned)SSM_DEV_WAIT_TIMEOUT);
-                    return;
-                }
-            }
-    }
-};
-
-__device__ __forceinline__ void store_out(const W4LinearArgs& a, int m, int64_t n, float v) {
-    if (a.out_bf16) reinterpret_cast<__nv_bfloat16*>(a.out)[(int64_t)m * a.ldo + n] = __float2bfloat16_rn(v);
-    else reinterpret_cast<float*>(a.out)[(int64_t)m * a.ldo + n] = v;
 }
 
 // PG: chunks in a group.
@@ -408,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a,
                 if (n >= a.w.N) return;
                 if (a.x_scale && a.x_blocks == 1) v *= __ldg(a.x_scale + m0 + m);
                 if (plan.slices > 1) a.parts[((int64_t)slice * a.M + m0 + m) * a.w.N + n] = v;
-                else store_out(a, m0 + m, n, v);
+                else w4_store(a, m0 + m, n, v);
             };
             const int outs = turn(tile) * columns * kRows;
             if (outs <= 8 * kServe) {                   // few: four threads for each
@@ -446,11 +406,10 @@ __global__ void __launch_bounds__(256) k_w4_join(const W4LinearArgs a, int slice
     cudaGridDependencySynchronize();                    // launched while the products still run
     const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (n >= a.w.N) return;
-    for (int m = blockIdx.y; m < a.M; m += gridDim.y) {
-        float v = 0.f;
-        for (int s = 0; s < slices; ++s) v += a.parts[((int64_t)s * a.M + m) * a.w.N + n];
-        store_out(a, m, n, v);
-    }
+    const int m = blockIdx.y;
+    float v = 0.f;
+    for (int s = 0; s < slices; ++s) v += a.parts[((int64_t)s * a.M + m) * a.w.N + n];
+    w4_store(a, m, n, v);
 }
 
 template <int NT>
@@ -502,21 +461,8 @@ int linear(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, con
     static ContextMemo attr_memo;
     if (!opt_in_dynamic_smem(attr_memo, kern, kMaxSmem, why)) return -1;
     kern<<<dim3((unsigned)p.walkers, (unsigned)p.m_blocks, (unsigned)p.slices), kThreads, p.smem, stream>>>(a, p, status);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess && p.slices > 1) {
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        cfg.gridDim = dim3((unsigned)((a.w.N + 255) / 256), (unsigned)(a.M < 1024 ? a.M : 1024));
-        cfg.blockDim = dim3(256);
-        cfg.stream = stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        e = cudaLaunchKernelEx(&cfg, k_w4_join, a, p.slices);
-        if (e == cudaSuccess) e = cudaGetLastError();
-    }
-    if (e == cudaSuccess) return 0;
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) return p.slices > 1 ? launch_w4_join(a, p.slices, stream, why) : 0;
     *why = cudaGetErrorString(e);
     return -1;
 }
@@ -555,12 +501,31 @@ int launch_w4_quantize(const W4Weight& w, const void* W, int64_t ldw, bool in_bf
                    : quantize(w, static_cast<const float*>(W), ldw, stream, why);
 }
 
+int launch_w4_join(const W4LinearArgs& a, int slices, cudaStream_t stream, const char** why) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)((a.w.N + 255) / 256), (unsigned)a.M);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k_w4_join, a, slices);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e == cudaSuccess) return 0;
+    *why = cudaGetErrorString(e);
+    return -1;
+}
+
 size_t w4_linear_workspace(int M, const W4Weight& w) {
+    if (M > 16) return w4_tiles_workspace(M, w);
     const int slices = M <= 8 ? best_plan<1>(M, w).slices : best_plan<2>(M, w).slices;
     return slices == 1 ? 0 : (size_t)slices * M * w.N * sizeof(float);
 }
 
 int launch_w4_linear(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, const char** why) {
+    if (a.M > 16) return launch_w4_tiles(a, status, stream, why);
     return a.M <= 8 ? linear_of<1>(a, status, stream, why) : linear_of<2>(a, status, stream, why);
 }
 

@@ -1,0 +1,400 @@
+// w4_tiles.cu -- w4_linear for more rows of x than a matrix instruction of a warp takes: tiles of 128 rows of the
+// 4-bit weight against up to 64 rows of x on the 5th-generation tensor cores.
+//
+// With 64 rows the product costs a warp's matrix instructions several times what the weight's bytes take, and the
+// codes would be unpacked once for every 16 rows of x.  Here they are unpacked once for 64: a thread has a row of
+// the weight, turns its codes into bf16 whole numbers code - zero (exact) and writes them to TMEM, where they are
+// the A operand; x, in the order in which a word's codes come out, is B in shared memory.  A group's sums are an
+// accumulator of their own (four of them in turn), which other threads, a row each, multiply by the group's
+// scale and add up in fp32 registers.  Eight warps unpack (56 integer operations and 32 subtractions for 64 codes of
+// 32 rows), four scale, one lane each issues copies and products.
+#include <type_traits>
+
+#include "kernels.h"
+#include "ssm.h"
+#include "tcgen05.cuh"
+#include "w4.cuh"
+
+namespace ssm {
+namespace {
+
+constexpr int kRows = 128;                              // of the weight: an MMA's M
+constexpr int kStep = 64;                               // elements that are unpacked together: 32 TMEM columns
+constexpr int kStageK = 256;                            // elements in a stage of codes: rows of 128 bytes
+constexpr int kStageC = kRows * kStageK / 2;
+constexpr int kCodeStages = 6, kXStages = 8;
+constexpr int kA = 4, kD = 4;                           // A operands and accumulators in TMEM
+constexpr int kUnpack = 8, kScale = 4;                  // warps
+constexpr int kThreads = 32 * (kUnpack + kScale + 2);
+
+template <int MP> struct Geo {                          // rows of x: 32 or 64
+    static constexpr int kStageX = MP * kStep * 2;
+    static constexpr int kOffX = kCodeStages * kStageC;
+    static constexpr int kOffBar = kOffX + kXStages * kStageX;
+    static constexpr int kSmem = kOffBar + (2 * kCodeStages + 2 * kXStages + 2 * kA + 2 * kD) * 8 + 16 + 1024;    // + to align
+    static constexpr uint32_t kColD = 32 * kA;          // TMEM: A operands, then accumulators
+    // fp32 accumulator, bf16 operands, M = 128, N = MP, both K-major
+    static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(MP >> 3) << 17) | (8u << 24);
+};
+
+__device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+          "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+          "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint4 ld_u128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+// bf16 128 + zero twice, of a group's zero
+__device__ __forceinline__ uint32_t zero_pair(uint32_t z) { return (0x4300u | (z & 15u)) * 0x10001u; }
+// Two codes, 16 bits apart, as bf16 128 + code (its last place is 1 there), less 128 + zero: exact.
+__device__ __forceinline__ uint32_t less_zero(uint32_t w, uint32_t zero) {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w), "r"(0x000f000fu), "r"(0x43004300u));
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&zero));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// A position in a ring of stages and the parity of its turn.
+template <int N> struct Ring {
+    int at = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) at = 0, parity ^= 1;
+    }
+};
+
+struct Cut {                    // of a call
+    int tiles, slices, m_blocks;
+    int slice_k;                // elements of a row in a slice: a multiple of a stage's
+};
+
+template <int MP>
+__global__ void __launch_bounds__(kThreads, 1)
+k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_x, const W4LinearArgs a,
+           const Cut cut, unsigned int* status) {
+    using G = Geo<MP>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* const c_full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
+    uint64_t *const c_empty = c_full + kCodeStages, *const x_full = c_empty + kCodeStages, *const x_empty = x_full + kXStages;
+    uint64_t *const a_full = x_empty + kXStages, *const a_empty = a_full + kA, *const d_full = a_empty + kA, *const d_empty = d_full + kD;
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(d_empty + kD);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int m0 = blockIdx.y * MP, slice = blockIdx.z;
+    const int k0 = slice * cut.slice_k, kn = min(cut.slice_k, a.w.K - k0);
+    const int steps = (kn + kStep - 1) / kStep, group = a.w.group, groups = kn / group, j0 = k0 / group;
+    const int per_step = group == 32 ? 2 : 1;           // groups in a step
+    const int steps_per_group = group == 128 ? 2 : 1;
+    Waiter wait{status};
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kCodeStages; ++i) mbar_init(&c_full[i], 1), mbar_init(&c_empty[i], kUnpack);
+        for (int i = 0; i < kXStages; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_empty[i], 1);
+        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], kUnpack / 2), mbar_init(&a_empty[i], 1);
+        for (int i = 0; i < kD; ++i) mbar_init(&d_full[i], 1), mbar_init(&d_empty[i], kScale);
+        fence_barrier_init();
+        prefetch_tmap(&tm_codes);
+        prefetch_tmap(&tm_x);
+    }
+    if (warp == kUnpack + kScale) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < kUnpack) {
+        // ---- codes to operands: a row of the weight each; every second step is one half of the warps'
+        const int half = warp / 4, row = 32 * (warp % 4) + lane;
+        const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
+        Ring<kCodeStages> cs;
+        uint32_t turns[kA / 2] = {1, 1};                // parities of this half's operands
+        int mine = 0;                                   // which of them is next
+        for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x) {
+            const int64_t n = min((int64_t)tile * kRows + row, (int64_t)a.w.N - 1);
+            const uint8_t* const zeros = a.w.zeros ? a.w.zeros + n * a.w.ldz + j0 : nullptr;
+            for (int s0 = 0; s0 < steps; s0 += kStageK / kStep, cs.next()) {
+                wait(&c_full[cs.at], cs.parity);
+                const uint32_t at = smem_u32(smem) + cs.at * kStageC + row * 128;
+                for (int i = 0; i < kStageK / kStep; ++i) {
+                    const int s = s0 + i;
+                    if (s >= steps) break;
+                    // operands go round by steps of the tile's own count, so a half's turns alternate with it
+                    if ((s & 1) != half) continue;
+                    uint32_t z0 = 0x43084308u, z1 = z0;
+                    if (zeros) {
+                        const int j = group == 32 ? 2 * s : s / steps_per_group;
+                        z0 = z1 = zero_pair(__ldg(zeros + j));
+                        if (group == 32 && j + 1 < groups) z1 = zero_pair(__ldg(zeros + j + 1));
+                    }
+                    // 32 bytes of the row: two 16-byte pieces, where the 128-byte swizzle put them
+                    const uint4 p = ld_u128(at + (((2 * i) ^ (row & 7)) << 4)), q = ld_u128(at + (((2 * i + 1) ^ (row & 7)) << 4));
+                    const uint32_t words[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+                    uint32_t v[32];
+#pragma unroll
+                    for (int w = 0; w < 8; ++w)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[4 * w + k] = less_zero(words[w] >> (4 * k), w < 4 ? z0 : z1);
+                    const int buf = half + 2 * mine;
+                    wait(&a_empty[buf], turns[mine]);
+                    turns[mine] ^= 1;
+                    mine ^= 1;
+                    tc_fence_after();
+                    __syncwarp();
+                    tmem_st32(tmem + lanes + 32u * buf, v);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&a_full[buf]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c_empty[cs.at]);
+            }
+        }
+    } else if (warp < kUnpack + kScale) {
+        // ---- a group's sums times its scale, and the outputs
+        const int row = 32 * (warp % 4) + lane;
+        const uint32_t from = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + G::kColD;
+        Ring<kD> ds;
+        const int x_block = a.w.K / group / a.x_blocks;     // groups
+        for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x) {
+            const int64_t n = (int64_t)tile * kRows + row, n_in = min(n, (int64_t)a.w.N - 1);
+            const int64_t s_at = n_in * a.w.lds + j0;
+            auto scale_at = [&](int j) {
+                return a.w.scale_bf16 ? __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(a.w.scales) + s_at + j))
+                                      : __ldg(reinterpret_cast<const float*>(a.w.scales) + s_at + j);
+            };
+            float acc[MP] = {}, ahead = scale_at(0);
+            for (int j = 0; j < groups; ++j, ds.next()) {
+                const float scale = ahead;
+                if (j + 1 < groups) ahead = scale_at(j + 1);
+                wait(&d_full[ds.at], ds.parity);
+                tc_fence_after();
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < MP; c += 32) {
+                    float d[32];
+                    tmem_ld32(from + MP * ds.at + c, d);
+                    if (c + 32 >= MP) {                     // all read: the accumulator is free again
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&d_empty[ds.at]);
+                    }
+                    if (a.x_blocks > 1) {
+                        const float* xs = a.x_scale + (j0 + j) / x_block;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (m0 + c + i < a.M) d[i] *= __ldg(xs + (int64_t)(m0 + c + i) * a.x_blocks);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(d[i], scale, acc[c + i]);
+                }
+            }
+            if (n < a.w.N) {
+#pragma unroll
+                for (int i = 0; i < MP; ++i) {
+                    const int m = m0 + i;
+                    if (m >= a.M) break;
+                    float v = acc[i];
+                    if (a.x_scale && a.x_blocks == 1) v *= __ldg(a.x_scale + m);
+                    if (cut.slices > 1) a.parts[((int64_t)slice * a.M + m) * a.w.N + n] = v;
+                    else w4_store(a, m, n, v);
+                }
+            }
+        }
+    } else if (warp == kUnpack + kScale) {
+        if (lane == 0) {
+            // ---- copies: stages of codes ahead of the steps of x
+            Ring<kCodeStages> cs;
+            Ring<kXStages> xs;
+            const int stages = (steps + kStageK / kStep - 1) / (kStageK / kStep);
+            // (tile, stage) of the next codes
+            int tile_c = blockIdx.x, stage_c = 0;
+            auto codes = [&]() {
+                if (tile_c >= cut.tiles) return;
+                wait(&c_empty[cs.at], cs.parity ^ 1);
+                mbar_arrive_expect_tx(&c_full[cs.at], kStageC);
+                tma_load_2d(smem + cs.at * kStageC, &tm_codes, &c_full[cs.at], k0 / 2 + stage_c * (kStageK / 2), tile_c * kRows);
+                cs.next();
+                if (++stage_c == stages) stage_c = 0, tile_c += gridDim.x;
+            };
+            for (int i = 0; i < kCodeStages - 1; ++i) codes();
+            asm volatile("griddepcontrol.wait;" ::: "memory");      // x in its order comes from the kernel before
+            for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
+                for (int s = 0; s < steps; ++s, xs.next()) {
+                    if (s % (kStageK / kStep) == 0) codes();
+                    wait(&x_empty[xs.at], xs.parity ^ 1);
+                    mbar_arrive_expect_tx(&x_full[xs.at], G::kStageX);
+                    tma_load_2d(smem + G::kOffX + xs.at * G::kStageX, &tm_x, &x_full[xs.at], k0 + s * kStep, m0);
+                }
+        }
+    } else if (lane == 0) {
+        // ---- products
+        Ring<kXStages> xs;
+        Ring<kD> ds;
+        uint32_t a_turn[kA] = {0, 0, 0, 0};
+        int pick[2] = {0, 0};
+        for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x) {
+            int done = 0;                                   // groups
+            for (int s = 0; s < steps; ++s, xs.next()) {
+                const int half = s & 1, buf = half + 2 * pick[half];
+                pick[half] ^= 1;
+                wait(&a_full[buf], a_turn[buf]);
+                a_turn[buf] ^= 1;
+                wait(&x_full[xs.at], xs.parity);
+                const uint64_t b = smem_desc_sw128(smem_u32(smem) + G::kOffX + xs.at * G::kStageX);
+                const uint32_t a_at = tmem + 32u * buf;
+                for (int h = 0; h < per_step && done < groups; ++h) {
+                    const bool opens = group != 128 || half == 0, closes = group != 128 || half == 1;
+                    if (opens) wait(&d_empty[ds.at], ds.parity ^ 1);
+                    tc_fence_after();
+                    const int from = per_step == 2 ? 2 * h : 0, to = per_step == 2 ? 2 * h + 2 : 4;
+                    for (int k = from; k < to; ++k)
+                        mma_from_tmem(tmem + G::kColD + MP * ds.at, a_at + 8u * k, b + 2u * k, G::kIdesc, !(opens && k == from));
+                    if (closes) {
+                        mma_commit(&d_full[ds.at]);
+                        ds.next();
+                        ++done;
+                    }
+                }
+                mma_commit(&a_empty[buf]);
+                mma_commit(&x_empty[xs.at]);
+            }
+        }
+        // the last commits have arrived before the CTA ends
+        if (cut.tiles > (int)blockIdx.x) {
+            const int at = (xs.at + kXStages - 1) % kXStages, last = (steps - 1) & 1, buf = last + 2 * (pick[last] ^ 1);
+            wait(&x_empty[at], xs.at == 0 ? xs.parity ^ 1 : xs.parity);
+            wait(&a_empty[buf], a_turn[buf] ^ 1);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kUnpack + kScale) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// x as bf16, every eight elements in the order 0 4 1 5 2 6 3 7 in which a word's codes come out; rows from M on are 0.
+__global__ void __launch_bounds__(256) k_w4_order(const W4LinearArgs a, uint4* to, int64_t vecs) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= vecs) return;
+    const int per_row = a.w.K / 8, m = (int)(i / per_row), k = (int)(i % per_row) * 8;
+    uint32_t r[4] = {};
+    if (m < a.M) {
+        if (a.x_i8) x_pairs(*reinterpret_cast<const uint2*>(reinterpret_cast<const int8_t*>(a.x) + m * a.ldx + k), r);
+        else x_pairs(*reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.x) + m * a.ldx + k), r);
+    }
+    to[i] = make_uint4(r[0], r[1], r[2], r[3]);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+bool encode(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base, uint64_t inner, uint64_t rows, uint64_t stride,
+            uint32_t box_inner, uint32_t box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {inner, rows}, strides[1] = {stride * size};
+    cuuint32_t box[2] = {box_inner, box_rows}, one[2] = {1, 1};
+    return enc(m, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kSms = 152;
+
+int rows_of(int M) { return M <= 32 ? 32 : 64; }
+
+// Slices of the rows where the tiles alone leave SMs idle: as for the kernel of few rows, by the CTA with most work
+// at an SM's share of the copy rate, and two microseconds for the second kernel.
+Cut cut_of(int M, const W4Weight& w) {
+    Cut best{};
+    int64_t least = 0;
+    const int stages = (w.K + kStageK - 1) / kStageK;
+    for (int s = 1; s <= 8 && s <= stages; ++s) {
+        Cut c;
+        c.tiles = (w.N + kRows - 1) / kRows;
+        c.m_blocks = (M + rows_of(M) - 1) / rows_of(M);
+        c.slice_k = (stages + s - 1) / s * kStageK;
+        c.slices = (w.K + c.slice_k - 1) / c.slice_k;
+        int walkers = kSms / (c.m_blocks * c.slices);
+        walkers = walkers < 1 ? 1 : walkers > c.tiles ? c.tiles : walkers;
+        const int64_t bytes = (int64_t)((c.tiles + walkers - 1) / walkers) * c.slice_k * (kRows / 2);
+        const int64_t ns = bytes / 44 + (c.slices > 1 ? 2000 : 0);
+        if (s == 1 || ns < least) best = c, least = ns;
+    }
+    return best;
+}
+
+int64_t padded(int M) { return (int64_t)(M + rows_of(M) - 1) / rows_of(M) * rows_of(M); }
+
+template <int MP>
+int launch(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, const char** why) {
+    using G = Geo<MP>;
+    const Cut cut = cut_of(a.M, a.w);
+    uint4* const x = reinterpret_cast<uint4*>(a.parts);         // x in its order, then the slices' sums
+    W4LinearArgs b = a;
+    b.parts = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(a.parts) + padded(a.M) * a.w.K * 2);
+    CUtensorMap mc, mx;
+    if (!encode(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.w.codes, a.w.K / 2, a.w.N, a.w.ldc, kStageK / 2, kRows) ||
+        !encode(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, a.w.K, padded(a.M), a.w.K, kStep, MP)) {
+        *why = "cuTensorMapEncodeTiled failed (driver entry point missing or layout rejected)";
+        return -1;
+    }
+    auto kern = k_w4_tiles<MP>;
+    static ContextMemo attr_memo;
+    if (!opt_in_dynamic_smem(attr_memo, kern, G::kSmem, why)) return -1;
+    const int64_t vecs = padded(a.M) * a.w.K / 8;
+    k_w4_order<<<(unsigned)((vecs + 255) / 256), 256, 0, stream>>>(a, x, vecs);
+    cudaError_t e = cudaGetLastError();
+    int walkers = kSms / (cut.m_blocks * cut.slices);
+    walkers = walkers < 1 ? 1 : walkers > cut.tiles ? cut.tiles : walkers;
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        cfg.gridDim = dim3((unsigned)walkers, (unsigned)cut.m_blocks, (unsigned)cut.slices);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = G::kSmem;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        e = cudaLaunchKernelEx(&cfg, kern, mc, mx, b, cut, status);
+        if (e == cudaSuccess) e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) {
+        *why = cudaGetErrorString(e);
+        return -1;
+    }
+    return cut.slices > 1 ? launch_w4_join(b, cut.slices, stream, why) : 0;
+}
+
+}  // namespace
+
+size_t w4_tiles_workspace(int M, const W4Weight& w) {
+    const Cut c = cut_of(M, w);
+    return (size_t)padded(M) * w.K * 2 + (c.slices > 1 ? (size_t)c.slices * M * w.N * sizeof(float) : 0);
+}
+
+int launch_w4_tiles(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, const char** why) {
+    return rows_of(a.M) == 32 ? launch<32>(a, status, stream, why) : launch<64>(a, status, stream, why);
+}
+
+}  // namespace ssm
