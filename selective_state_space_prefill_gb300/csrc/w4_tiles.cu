@@ -22,21 +22,27 @@ constexpr int kRows = 128;                              // of the weight: an MMA
 constexpr int kStep = 64;                               // elements that are unpacked together: 32 TMEM columns
 constexpr int kStageK = 256;                            // elements in a stage of codes: rows of 128 bytes
 constexpr int kStageC = kRows * kStageK / 2;
-constexpr int kCodeStages = 6, kXStages = 8;
-constexpr int kA = 4, kD = 4;                           // A operands and accumulators in TMEM
-constexpr int kUnpack = 8, kScale = 4;                  // warps
-constexpr int kThreads = 32 * (kUnpack + kScale + 2);
+constexpr int kCodeStages = 6;
+constexpr int kSteps = 8;                               // under way: A operands in TMEM and x in shared memory
+constexpr int kD = 4;                                   // accumulators in TMEM
+constexpr int kUnpack = 8, kScale = 4;                  // warps; then one each for codes, x and products
+constexpr int kThreads = 32 * (kUnpack + kScale + 3);
 
 template <int MP> struct Geo {                          // rows of x: 32 or 64
     static constexpr int kStageX = MP * kStep * 2;
     static constexpr int kOffX = kCodeStages * kStageC;
-    static constexpr int kOffBar = kOffX + kXStages * kStageX;
-    static constexpr int kSmem = kOffBar + (2 * kCodeStages + 2 * kXStages + 2 * kA + 2 * kD) * 8 + 16 + 1024;    // + to align
-    static constexpr uint32_t kColD = 32 * kA;          // TMEM: A operands, then accumulators
+    static constexpr int kOffBar = kOffX + kSteps * kStageX;
+    static constexpr int kSmem = kOffBar + (2 * kCodeStages + 3 * kSteps + 2 * kD) * 8 + 16 + 1024;    // + to align
+    static constexpr uint32_t kColD = 32 * kSteps;          // TMEM: A operands, then accumulators
     // fp32 accumulator, bf16 operands, M = 128, N = MP, both K-major
     static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(MP >> 3) << 17) | (8u << 24);
 };
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, bool accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -73,11 +79,11 @@ __device__ __forceinline__ uint32_t less_zero(uint32_t w, uint32_t zero) {
 }
 
 // A position in a ring of stages and the parity of its turn.
-template <int N> struct Ring {
+struct Ring {
     int at = 0;
     uint32_t parity = 0;
     __device__ __forceinline__ void next() {
-        if (++at == N) at = 0, parity ^= 1;
+        if (++at == kCodeStages) at = 0, parity ^= 1;
     }
 };
 
@@ -86,7 +92,9 @@ struct Cut {                    // of a call
     int slice_k;                // elements of a row in a slice: a multiple of a stage's
 };
 
-template <int MP>
+// Steps, groups and stages are counted over all the tiles of a CTA: step r has A operand and x stage r % kSteps, in
+// the turn r / kSteps; group q accumulator q % kD.
+template <int MP, int GK>                               // rows of x, elements of a group
 __global__ void __launch_bounds__(kThreads, 1)
 k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_x, const W4LinearArgs a,
            const Cut cut, unsigned int* status) {
@@ -94,22 +102,19 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
     extern __shared__ unsigned char smem_raw[];
     unsigned char* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* const c_full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
-    uint64_t *const c_empty = c_full + kCodeStages, *const x_full = c_empty + kCodeStages, *const x_empty = x_full + kXStages;
-    uint64_t *const a_full = x_empty + kXStages, *const a_empty = a_full + kA, *const d_full = a_empty + kA, *const d_empty = d_full + kD;
+    uint64_t *const c_empty = c_full + kCodeStages, *const x_full = c_empty + kCodeStages, *const a_full = x_full + kSteps;
+    uint64_t *const used = a_full + kSteps, *const d_full = used + kSteps, *const d_empty = d_full + kD;
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(d_empty + kD);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int m0 = blockIdx.y * MP, slice = blockIdx.z;
     const int k0 = slice * cut.slice_k, kn = min(cut.slice_k, a.w.K - k0);
-    const int steps = (kn + kStep - 1) / kStep, group = a.w.group, groups = kn / group, j0 = k0 / group;
-    const int per_step = group == 32 ? 2 : 1;           // groups in a step
-    const int steps_per_group = group == 128 ? 2 : 1;
+    const int steps = (kn + kStep - 1) / kStep, groups = kn / GK, j0 = k0 / GK;
     Waiter wait{status};
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kCodeStages; ++i) mbar_init(&c_full[i], 1), mbar_init(&c_empty[i], kUnpack);
-        for (int i = 0; i < kXStages; ++i) mbar_init(&x_full[i], 1), mbar_init(&x_empty[i], 1);
-        for (int i = 0; i < kA; ++i) mbar_init(&a_full[i], kUnpack / 2), mbar_init(&a_empty[i], 1);
+        for (int i = 0; i < kSteps; ++i) mbar_init(&x_full[i], 1), mbar_init(&a_full[i], kUnpack / 2), mbar_init(&used[i], 1);
         for (int i = 0; i < kD; ++i) mbar_init(&d_full[i], 1), mbar_init(&d_empty[i], kScale);
         fence_barrier_init();
         prefetch_tmap(&tm_codes);
@@ -125,25 +130,21 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
         // ---- codes to operands: a row of the weight each; every second step is one half of the warps'
         const int half = warp / 4, row = 32 * (warp % 4) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
-        Ring<kCodeStages> cs;
-        uint32_t turns[kA / 2] = {1, 1};                // parities of this half's operands
-        int mine = 0;                                   // which of them is next
+        Ring cs;
+        uint32_t r = 0;
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x) {
             const int64_t n = min((int64_t)tile * kRows + row, (int64_t)a.w.N - 1);
             const uint8_t* const zeros = a.w.zeros ? a.w.zeros + n * a.w.ldz + j0 : nullptr;
             for (int s0 = 0; s0 < steps; s0 += kStageK / kStep, cs.next()) {
                 wait(&c_full[cs.at], cs.parity);
                 const uint32_t at = smem_u32(smem) + cs.at * kStageC + row * 128;
-                for (int i = 0; i < kStageK / kStep; ++i) {
-                    const int s = s0 + i;
-                    if (s >= steps) break;
-                    // operands go round by steps of the tile's own count, so a half's turns alternate with it
-                    if ((s & 1) != half) continue;
+                for (int i = 0; i < kStageK / kStep && s0 + i < steps; ++i, ++r) {
+                    if ((r & 1) != half) continue;
                     uint32_t z0 = 0x43084308u, z1 = z0;
                     if (zeros) {
-                        const int j = group == 32 ? 2 * s : s / steps_per_group;
+                        const int j = (s0 + i) * kStep / GK;
                         z0 = z1 = zero_pair(__ldg(zeros + j));
-                        if (group == 32 && j + 1 < groups) z1 = zero_pair(__ldg(zeros + j + 1));
+                        if (GK == 32 && j + 1 < groups) z1 = zero_pair(__ldg(zeros + j + 1));
                     }
                     // 32 bytes of the row: two 16-byte pieces, where the 128-byte swizzle put them
                     const uint4 p = ld_u128(at + (((2 * i) ^ (row & 7)) << 4)), q = ld_u128(at + (((2 * i + 1) ^ (row & 7)) << 4));
@@ -153,10 +154,8 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                     for (int w = 0; w < 8; ++w)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) v[4 * w + k] = less_zero(words[w] >> (4 * k), w < 4 ? z0 : z1);
-                    const int buf = half + 2 * mine;
-                    wait(&a_empty[buf], turns[mine]);
-                    turns[mine] ^= 1;
-                    mine ^= 1;
+                    const uint32_t buf = r % kSteps;
+                    wait(&used[buf], r / kSteps & 1 ^ 1);
                     tc_fence_after();
                     __syncwarp();
                     tmem_st32(tmem + lanes + 32u * buf, v);
@@ -172,8 +171,8 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
         // ---- a group's sums times its scale, and the outputs
         const int row = 32 * (warp % 4) + lane;
         const uint32_t from = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + G::kColD;
-        Ring<kD> ds;
-        const int x_block = a.w.K / group / a.x_blocks;     // groups
+        uint32_t q = 0;
+        const int x_block = a.w.K / GK / a.x_blocks;    // groups
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x) {
             const int64_t n = (int64_t)tile * kRows + row, n_in = min(n, (int64_t)a.w.N - 1);
             const int64_t s_at = n_in * a.w.lds + j0;
@@ -182,20 +181,21 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                                       : __ldg(reinterpret_cast<const float*>(a.w.scales) + s_at + j);
             };
             float acc[MP] = {}, ahead = scale_at(0);
-            for (int j = 0; j < groups; ++j, ds.next()) {
+            for (int j = 0; j < groups; ++j, ++q) {
                 const float scale = ahead;
                 if (j + 1 < groups) ahead = scale_at(j + 1);
-                wait(&d_full[ds.at], ds.parity);
+                const uint32_t buf = q % kD;
+                wait(&d_full[buf], q / kD & 1);
                 tc_fence_after();
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < MP; c += 32) {
                     float d[32];
-                    tmem_ld32(from + MP * ds.at + c, d);
+                    tmem_ld32(from + MP * buf + c, d);
                     if (c + 32 >= MP) {                     // all read: the accumulator is free again
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&d_empty[ds.at]);
+                        if (lane == 0) mbar_arrive(&d_empty[buf]);
                     }
                     if (a.x_blocks > 1) {
                         const float* xs = a.x_scale + (j0 + j) / x_block;
@@ -220,70 +220,72 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
             }
         }
     } else if (warp == kUnpack + kScale) {
-        if (lane == 0) {
-            // ---- copies: stages of codes ahead of the steps of x
-            Ring<kCodeStages> cs;
-            Ring<kXStages> xs;
-            const int stages = (steps + kStageK / kStep - 1) / (kStageK / kStep);
-            // (tile, stage) of the next codes
-            int tile_c = blockIdx.x, stage_c = 0;
-            auto codes = [&]() {
-                if (tile_c >= cut.tiles) return;
+        // ---- copies of codes.  Here and below the whole warp walks the loop, so that what an instruction wants in
+        // uniform registers stays there, and one elected lane issues.
+        Ring cs;
+        const int stages = (steps + kStageK / kStep - 1) / (kStageK / kStep);
+        for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
+            for (int i = 0; i < stages; ++i, cs.next()) {
                 wait(&c_empty[cs.at], cs.parity ^ 1);
-                mbar_arrive_expect_tx(&c_full[cs.at], kStageC);
-                tma_load_2d(smem + cs.at * kStageC, &tm_codes, &c_full[cs.at], k0 / 2 + stage_c * (kStageK / 2), tile_c * kRows);
-                cs.next();
-                if (++stage_c == stages) stage_c = 0, tile_c += gridDim.x;
-            };
-            for (int i = 0; i < kCodeStages - 1; ++i) codes();
-            asm volatile("griddepcontrol.wait;" ::: "memory");      // x in its order comes from the kernel before
-            for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
-                for (int s = 0; s < steps; ++s, xs.next()) {
-                    if (s % (kStageK / kStep) == 0) codes();
-                    wait(&x_empty[xs.at], xs.parity ^ 1);
-                    mbar_arrive_expect_tx(&x_full[xs.at], G::kStageX);
-                    tma_load_2d(smem + G::kOffX + xs.at * G::kStageX, &tm_x, &x_full[xs.at], k0 + s * kStep, m0);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&c_full[cs.at], kStageC);
+                    tma_load_2d(smem + cs.at * kStageC, &tm_codes, &c_full[cs.at], k0 / 2 + i * (kStageK / 2), tile * kRows);
                 }
-        }
-    } else if (lane == 0) {
-        // ---- products
-        Ring<kXStages> xs;
-        Ring<kD> ds;
-        uint32_t a_turn[kA] = {0, 0, 0, 0};
-        int pick[2] = {0, 0};
-        for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x) {
-            int done = 0;                                   // groups
-            for (int s = 0; s < steps; ++s, xs.next()) {
-                const int half = s & 1, buf = half + 2 * pick[half];
-                pick[half] ^= 1;
-                wait(&a_full[buf], a_turn[buf]);
-                a_turn[buf] ^= 1;
-                wait(&x_full[xs.at], xs.parity);
-                const uint64_t b = smem_desc_sw128(smem_u32(smem) + G::kOffX + xs.at * G::kStageX);
-                const uint32_t a_at = tmem + 32u * buf;
-                for (int h = 0; h < per_step && done < groups; ++h) {
-                    const bool opens = group != 128 || half == 0, closes = group != 128 || half == 1;
-                    if (opens) wait(&d_empty[ds.at], ds.parity ^ 1);
-                    tc_fence_after();
-                    const int from = per_step == 2 ? 2 * h : 0, to = per_step == 2 ? 2 * h + 2 : 4;
-                    for (int k = from; k < to; ++k)
-                        mma_from_tmem(tmem + G::kColD + MP * ds.at, a_at + 8u * k, b + 2u * k, G::kIdesc, !(opens && k == from));
-                    if (closes) {
-                        mma_commit(&d_full[ds.at]);
-                        ds.next();
-                        ++done;
-                    }
-                }
-                mma_commit(&a_empty[buf]);
-                mma_commit(&x_empty[xs.at]);
+                __syncwarp();
             }
-        }
+    } else if (warp == kUnpack + kScale + 1) {
+        // ---- copies of x
+        asm volatile("griddepcontrol.wait;" ::: "memory");          // x in its order comes from the kernel before
+        uint32_t r = 0;
+        for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
+            for (int s = 0; s < steps; ++s, ++r) {
+                const uint32_t buf = r % kSteps;
+                wait(&used[buf], r / kSteps & 1 ^ 1);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&x_full[buf], G::kStageX);
+                    tma_load_2d(smem + G::kOffX + buf * G::kStageX, &tm_x, &x_full[buf], k0 + s * kStep, m0);
+                }
+                __syncwarp();
+            }
+    } else {
+        // ---- products
+        const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+        const uint64_t xd = smem_desc_sw128(__shfl_sync(~0u, smem_u32(smem), 0) + G::kOffX);
+        uint32_t r = 0, q = 0;
+        for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
+            for (int s = 0; s < steps; ++s, ++r) {
+                const uint32_t buf = r % kSteps;
+                wait(&a_full[buf], r / kSteps & 1);
+                wait(&x_full[buf], r / kSteps & 1);
+                const uint64_t b = xd + (uint64_t)(buf * (G::kStageX >> 4));
+                // a group's 16-element products, the first of which starts its accumulator
+                auto products = [&](auto first, auto count, bool opens, bool closes) {
+                    constexpr int kFirst = decltype(first)::value, kCount = decltype(count)::value;
+                    if (opens) wait(&d_empty[q % kD], q / kD & 1 ^ 1);
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = kFirst; k < kFirst + kCount; ++k)
+                            mma_from_tmem(tm + G::kColD + MP * (q % kD), tm + 32u * buf + 8u * k, b + 2u * k, G::kIdesc,
+                                          k != kFirst || !opens);
+                        if (closes) mma_commit(&d_full[q % kD]);
+                    }
+                    __syncwarp();
+                    if (closes) ++q;
+                };
+                using std::integral_constant;
+                if constexpr (GK == 32) {
+                    products(integral_constant<int, 0>(), integral_constant<int, 2>(), true, true);
+                    if (2 * s + 1 < groups) products(integral_constant<int, 2>(), integral_constant<int, 2>(), true, true);
+                } else {
+                    const bool opens = GK == 64 || s % 2 == 0;
+                    products(integral_constant<int, 0>(), integral_constant<int, 4>(), opens, GK == 64 || !opens);
+                }
+                if (elect_one()) mma_commit(&used[buf]);
+                __syncwarp();
+            }
         // the last commits have arrived before the CTA ends
-        if (cut.tiles > (int)blockIdx.x) {
-            const int at = (xs.at + kXStages - 1) % kXStages, last = (steps - 1) & 1, buf = last + 2 * (pick[last] ^ 1);
-            wait(&x_empty[at], xs.at == 0 ? xs.parity ^ 1 : xs.parity);
-            wait(&a_empty[buf], a_turn[buf] ^ 1);
-        }
+        for (uint32_t i = r < kSteps ? 0 : r - kSteps; i < r; ++i) wait(&used[i % kSteps], i / kSteps & 1);
     }
     tc_fence_before();
     __syncthreads();
@@ -344,7 +346,7 @@ Cut cut_of(int M, const W4Weight& w) {
 
 int64_t padded(int M) { return (int64_t)(M + rows_of(M) - 1) / rows_of(M) * rows_of(M); }
 
-template <int MP>
+template <int MP, int GK>
 int launch(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, const char** why) {
     using G = Geo<MP>;
     const Cut cut = cut_of(a.M, a.w);
@@ -357,7 +359,7 @@ int launch(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, con
         *why = "cuTensorMapEncodeTiled failed (driver entry point missing or layout rejected)";
         return -1;
     }
-    auto kern = k_w4_tiles<MP>;
+    auto kern = k_w4_tiles<MP, GK>;
     static ContextMemo attr_memo;
     if (!opt_in_dynamic_smem(attr_memo, kern, G::kSmem, why)) return -1;
     const int64_t vecs = padded(a.M) * a.w.K / 8;
@@ -394,7 +396,10 @@ size_t w4_tiles_workspace(int M, const W4Weight& w) {
 }
 
 int launch_w4_tiles(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, const char** why) {
-    return rows_of(a.M) == 32 ? launch<32>(a, status, stream, why) : launch<64>(a, status, stream, why);
+    const bool few = rows_of(a.M) == 32;
+    if (a.w.group == 32) return few ? launch<32, 32>(a, status, stream, why) : launch<64, 32>(a, status, stream, why);
+    if (a.w.group == 64) return few ? launch<32, 64>(a, status, stream, why) : launch<64, 64>(a, status, stream, why);
+    return few ? launch<32, 128>(a, status, stream, why) : launch<64, 128>(a, status, stream, why);
 }
 
 }  // namespace ssm
