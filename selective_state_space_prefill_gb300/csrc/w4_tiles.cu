@@ -7,7 +7,7 @@
 // the A operand; x, in the order in which a word's codes come out, is B in shared memory.  A group's sums are an
 // accumulator of their own (four of them in turn), which other threads, a row each, multiply by the group's
 // scale and add up in fp32 registers.  Eight warps unpack (56 integer operations and 32 subtractions for 64 codes of
-// 32 rows), four scale, one lane each issues copies and products.
+// 32 rows), eight scale, one each issues copies of codes, copies of x and products.
 #include <type_traits>
 
 #include "kernels.h"
@@ -19,21 +19,21 @@ namespace ssm {
 namespace {
 
 constexpr int kRows = 128;                              // of the weight: an MMA's M
-constexpr int kStep = 64;                               // elements that are unpacked together: 32 TMEM columns
+constexpr int kStep = 128;                              // elements of a step: 64 TMEM columns, two tiles of x
 constexpr int kStageK = 256;                            // elements in a stage of codes: rows of 128 bytes
 constexpr int kStageC = kRows * kStageK / 2;
 constexpr int kCodeStages = 6;
-constexpr int kSteps = 8;                               // under way: A operands in TMEM and x in shared memory
+constexpr int kSteps = 4;                               // under way: A operands in TMEM and x in shared memory
 constexpr int kD = 4;                                   // accumulators in TMEM
-constexpr int kUnpack = 8, kScale = 4;                  // warps; then one each for codes, x and products
+constexpr int kUnpack = 8, kScale = 8;                  // warps; then one each for codes, x and products
 constexpr int kThreads = 32 * (kUnpack + kScale + 3);
 
 template <int MP> struct Geo {                          // rows of x: 32 or 64
     static constexpr int kStageX = MP * kStep * 2;
     static constexpr int kOffX = kCodeStages * kStageC;
     static constexpr int kOffBar = kOffX + kSteps * kStageX;
-    static constexpr int kSmem = kOffBar + (2 * kCodeStages + 3 * kSteps + 2 * kD) * 8 + 16 + 1024;    // + to align
-    static constexpr uint32_t kColD = 32 * kSteps;          // TMEM: A operands, then accumulators
+    static constexpr int kSmem = kOffBar + (2 * kCodeStages + 2 * kSteps + 2 * kD) * 8 + 16 + 1024;    // + to align
+    static constexpr uint32_t kColD = kStep / 2 * kSteps;          // TMEM: A operands, then accumulators
     // fp32 accumulator, bf16 operands, M = 128, N = MP, both K-major
     static constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(MP >> 3) << 17) | (8u << 24);
 };
@@ -61,7 +61,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint4 ld_u128(uint32_t at) {
     uint4 v;
@@ -92,6 +91,11 @@ struct Cut {                    // of a call
     int slice_k;                // elements of a row in a slice: a multiple of a stage's
 };
 
+template <int N> __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+    if constexpr (N == 32) tmem_ld32(taddr, v);
+    else tmem_ld16(taddr, v);
+}
+
 // Steps, groups and stages are counted over all the tiles of a CTA: step r has A operand and x stage r % kSteps, in
 // the turn r / kSteps; group q accumulator q % kD.
 template <int MP, int GK>                               // rows of x, elements of a group
@@ -102,8 +106,8 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
     extern __shared__ unsigned char smem_raw[];
     unsigned char* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* const c_full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
-    uint64_t *const c_empty = c_full + kCodeStages, *const x_full = c_empty + kCodeStages, *const a_full = x_full + kSteps;
-    uint64_t *const used = a_full + kSteps, *const d_full = used + kSteps, *const d_empty = d_full + kD;
+    uint64_t *const c_empty = c_full + kCodeStages, *const full = c_empty + kCodeStages;
+    uint64_t *const used = full + kSteps, *const d_full = used + kSteps, *const d_empty = d_full + kD;
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(d_empty + kD);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -114,7 +118,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kCodeStages; ++i) mbar_init(&c_full[i], 1), mbar_init(&c_empty[i], kUnpack);
-        for (int i = 0; i < kSteps; ++i) mbar_init(&x_full[i], 1), mbar_init(&a_full[i], kUnpack / 2), mbar_init(&used[i], 1);
+        for (int i = 0; i < kSteps; ++i) mbar_init(&full[i], kUnpack / 2 + 1), mbar_init(&used[i], 1);      // operand and x
         for (int i = 0; i < kD; ++i) mbar_init(&d_full[i], 1), mbar_init(&d_empty[i], kScale);
         fence_barrier_init();
         prefetch_tmap(&tm_codes);
@@ -140,37 +144,43 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                 const uint32_t at = smem_u32(smem) + cs.at * kStageC + row * 128;
                 for (int i = 0; i < kStageK / kStep && s0 + i < steps; ++i, ++r) {
                     if ((r & 1) != half) continue;
-                    uint32_t z0 = 0x43084308u, z1 = z0;
-                    if (zeros) {
-                        const int j = (s0 + i) * kStep / GK;
-                        z0 = z1 = zero_pair(__ldg(zeros + j));
-                        if (GK == 32 && j + 1 < groups) z1 = zero_pair(__ldg(zeros + j + 1));
-                    }
-                    // 32 bytes of the row: two 16-byte pieces, where the 128-byte swizzle put them
-                    const uint4 p = ld_u128(at + (((2 * i) ^ (row & 7)) << 4)), q = ld_u128(at + (((2 * i + 1) ^ (row & 7)) << 4));
-                    const uint32_t words[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
-                    uint32_t v[32];
-#pragma unroll
-                    for (int w = 0; w < 8; ++w)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) v[4 * w + k] = less_zero(words[w] >> (4 * k), w < 4 ? z0 : z1);
                     const uint32_t buf = r % kSteps;
                     wait(&used[buf], r / kSteps & 1 ^ 1);
                     tc_fence_after();
-                    __syncwarp();
-                    tmem_st32(tmem + lanes + 32u * buf, v);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {           // 64 elements at a time
+                        uint32_t z0 = 0x43084308u, z1 = z0;
+                        if (zeros) {
+                            const int j = ((s0 + i) * kStep + 64 * h) / GK;
+                            if (j < groups) z0 = z1 = zero_pair(__ldg(zeros + j));
+                            if (GK == 32 && j + 1 < groups) z1 = zero_pair(__ldg(zeros + j + 1));
+                        }
+                        // 32 bytes of the row: two 16-byte pieces, where the 128-byte swizzle put them
+                        const uint4 p = ld_u128(at + (((4 * i + 2 * h) ^ (row & 7)) << 4));
+                        const uint4 q = ld_u128(at + (((4 * i + 2 * h + 1) ^ (row & 7)) << 4));
+                        const uint32_t words[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+                        uint32_t v[32];
+#pragma unroll
+                        for (int w = 0; w < 8; ++w)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) v[4 * w + k] = less_zero(words[w] >> (4 * k), w < 4 ? z0 : z1);
+                        __syncwarp();
+                        tmem_st32(tmem + lanes + (uint32_t)(kStep / 2) * buf + 32u * h, v);
+                    }
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&a_full[buf]);
+                    if (lane == 0) mbar_arrive(&full[buf]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c_empty[cs.at]);
             }
         }
     } else if (warp < kUnpack + kScale) {
-        // ---- a group's sums times its scale, and the outputs
-        const int row = 32 * (warp % 4) + lane;
-        const uint32_t from = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + G::kColD;
+        // ---- a group's sums times its scale, and the outputs: a row of the weight and half of x's rows each
+        constexpr int kMine = MP / 2;
+        const int row = 32 * (warp % 4) + lane, c0 = (warp - kUnpack) / 4 * kMine;
+        const uint32_t from = tmem + ((uint32_t)(32 * (warp % 4)) << 16) + G::kColD + c0;
         uint32_t q = 0;
         const int x_block = a.w.K / GK / a.x_blocks;    // groups
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x) {
@@ -180,37 +190,33 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                 return a.w.scale_bf16 ? __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(a.w.scales) + s_at + j))
                                       : __ldg(reinterpret_cast<const float*>(a.w.scales) + s_at + j);
             };
-            float acc[MP] = {}, ahead = scale_at(0);
+            float acc[kMine] = {}, ahead[2] = {scale_at(0), groups > 1 ? scale_at(1) : 0.f};
             for (int j = 0; j < groups; ++j, ++q) {
-                const float scale = ahead;
-                if (j + 1 < groups) ahead = scale_at(j + 1);
+                const float scale = ahead[0];
+                ahead[0] = ahead[1];
+                if (j + 2 < groups) ahead[1] = scale_at(j + 2);
                 const uint32_t buf = q % kD;
                 wait(&d_full[buf], q / kD & 1);
                 tc_fence_after();
                 __syncwarp();
+                float d[kMine];
+                tmem_ld(from + MP * buf, d);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&d_empty[buf]);
+                if (a.x_blocks > 1) {
+                    const float* xs = a.x_scale + (j0 + j) / x_block;
 #pragma unroll
-                for (int c = 0; c < MP; c += 32) {
-                    float d[32];
-                    tmem_ld32(from + MP * buf + c, d);
-                    if (c + 32 >= MP) {                     // all read: the accumulator is free again
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&d_empty[buf]);
-                    }
-                    if (a.x_blocks > 1) {
-                        const float* xs = a.x_scale + (j0 + j) / x_block;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (m0 + c + i < a.M) d[i] *= __ldg(xs + (int64_t)(m0 + c + i) * a.x_blocks);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(d[i], scale, acc[c + i]);
+                    for (int i = 0; i < kMine; ++i)
+                        if (m0 + c0 + i < a.M) d[i] *= __ldg(xs + (int64_t)(m0 + c0 + i) * a.x_blocks);
                 }
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) acc[i] = fmaf(d[i], scale, acc[i]);
             }
             if (n < a.w.N) {
 #pragma unroll
-                for (int i = 0; i < MP; ++i) {
-                    const int m = m0 + i;
+                for (int i = 0; i < kMine; ++i) {
+                    const int m = m0 + c0 + i;
                     if (m >= a.M) break;
                     float v = acc[i];
                     if (a.x_scale && a.x_blocks == 1) v *= __ldg(a.x_scale + m);
@@ -242,8 +248,9 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                 const uint32_t buf = r % kSteps;
                 wait(&used[buf], r / kSteps & 1 ^ 1);
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&x_full[buf], G::kStageX);
-                    tma_load_2d(smem + G::kOffX + buf * G::kStageX, &tm_x, &x_full[buf], k0 + s * kStep, m0);
+                    mbar_arrive_expect_tx(&full[buf], G::kStageX);
+                    for (int h = 0; h < 2; ++h)
+                        tma_load_2d(smem + G::kOffX + buf * G::kStageX + h * (G::kStageX / 2), &tm_x, &full[buf], k0 + s * kStep + 64 * h, m0);
                 }
                 __syncwarp();
             }
@@ -255,31 +262,24 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
             for (int s = 0; s < steps; ++s, ++r) {
                 const uint32_t buf = r % kSteps;
-                wait(&a_full[buf], r / kSteps & 1);
-                wait(&x_full[buf], r / kSteps & 1);
+                wait(&full[buf], r / kSteps & 1);
                 const uint64_t b = xd + (uint64_t)(buf * (G::kStageX >> 4));
-                // a group's 16-element products, the first of which starts its accumulator
-                auto products = [&](auto first, auto count, bool opens, bool closes) {
-                    constexpr int kFirst = decltype(first)::value, kCount = decltype(count)::value;
-                    if (opens) wait(&d_empty[q % kD], q / kD & 1 ^ 1);
+                // the step's groups, each an accumulator's: products of 16 elements, the first of which starts it
+                constexpr int kGroups = kStep / GK, kCount = GK / 16;
+#pragma unroll
+                for (int h = 0; h < kGroups; ++h) {
+                    if (kGroups > 1 && s * kGroups + h >= groups) break;
+                    wait(&d_empty[q % kD], q / kD & 1 ^ 1);
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = kFirst; k < kFirst + kCount; ++k)
-                            mma_from_tmem(tm + G::kColD + MP * (q % kD), tm + 32u * buf + 8u * k, b + 2u * k, G::kIdesc,
-                                          k != kFirst || !opens);
-                        if (closes) mma_commit(&d_full[q % kD]);
+                        for (int k = h * kCount; k < (h + 1) * kCount; ++k)
+                            mma_from_tmem(tm + G::kColD + MP * (q % kD), tm + (uint32_t)(kStep / 2) * buf + 8u * k,
+                                          b + (uint64_t)(k / 4 * (G::kStageX >> 5) + 2 * (k % 4)), G::kIdesc, k != h * kCount);
+                        mma_commit(&d_full[q % kD]);
                     }
                     __syncwarp();
-                    if (closes) ++q;
-                };
-                using std::integral_constant;
-                if constexpr (GK == 32) {
-                    products(integral_constant<int, 0>(), integral_constant<int, 2>(), true, true);
-                    if (2 * s + 1 < groups) products(integral_constant<int, 2>(), integral_constant<int, 2>(), true, true);
-                } else {
-                    const bool opens = GK == 64 || s % 2 == 0;
-                    products(integral_constant<int, 0>(), integral_constant<int, 4>(), opens, GK == 64 || !opens);
+                    ++q;
                 }
                 if (elect_one()) mma_commit(&used[buf]);
                 __syncwarp();
@@ -355,7 +355,7 @@ int launch(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, con
     b.parts = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(a.parts) + padded(a.M) * a.w.K * 2);
     CUtensorMap mc, mx;
     if (!encode(&mc, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.w.codes, a.w.K / 2, a.w.N, a.w.ldc, kStageK / 2, kRows) ||
-        !encode(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, a.w.K, padded(a.M), a.w.K, kStep, MP)) {
+        !encode(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, x, a.w.K, padded(a.M), a.w.K, kStep / 2, MP)) {
         *why = "cuTensorMapEncodeTiled failed (driver entry point missing or layout rejected)";
         return -1;
     }
