@@ -25,8 +25,9 @@ constexpr int kStageC = kRows * kStageK / 2;
 constexpr int kCodeStages = 6;
 constexpr int kSteps = 4;                               // under way: A operands in TMEM and x in shared memory
 constexpr int kD = 4;                                   // accumulators in TMEM
-constexpr int kUnpack = 8, kScale = 8;                  // warps; then one each for codes, x and products
+constexpr int kSets = 2, kUnpack = 4 * kSets, kScale = 8;       // warps; then one each for codes, x and products
 constexpr int kThreads = 32 * (kUnpack + kScale + 3);
+static_assert(kSteps == kD, "a step that is a group has one barrier for both");
 
 template <int MP> struct Geo {                          // rows of x: 32 or 64
     static constexpr int kStageX = MP * kStep * 2;
@@ -91,11 +92,6 @@ struct Cut {                    // of a call
     int slice_k;                // elements of a row in a slice: a multiple of a stage's
 };
 
-template <int N> __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
-    if constexpr (N == 32) tmem_ld32(taddr, v);
-    else tmem_ld16(taddr, v);
-}
-
 // Steps, groups and stages are counted over all the tiles of a CTA: step r has A operand and x stage r % kSteps, in
 // the turn r / kSteps; group q accumulator q % kD.
 template <int MP, int GK>                               // rows of x, elements of a group
@@ -107,7 +103,8 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
     unsigned char* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* const c_full = reinterpret_cast<uint64_t*>(smem + G::kOffBar);
     uint64_t *const c_empty = c_full + kCodeStages, *const full = c_empty + kCodeStages;
-    uint64_t *const used = full + kSteps, *const d_full = used + kSteps, *const d_empty = d_full + kD;
+    // where a step is a group, one commit tells both that its operands are used and that its sums are there
+    uint64_t *const d_full = full + kSteps, *const used = GK == kStep ? d_full : d_full + kD, *const d_empty = d_full + kD + kSteps;
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(d_empty + kD);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -118,8 +115,11 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kCodeStages; ++i) mbar_init(&c_full[i], 1), mbar_init(&c_empty[i], kUnpack);
-        for (int i = 0; i < kSteps; ++i) mbar_init(&full[i], kUnpack / 2 + 1), mbar_init(&used[i], 1);      // operand and x
-        for (int i = 0; i < kD; ++i) mbar_init(&d_full[i], 1), mbar_init(&d_empty[i], kScale);
+        for (int i = 0; i < kSteps; ++i) mbar_init(&full[i], 4 + 1), mbar_init(&used[i], 1);      // operand and x
+        for (int i = 0; i < kD; ++i) {
+            if (GK != kStep) mbar_init(&d_full[i], 1);
+            mbar_init(&d_empty[i], kScale);
+        }
         fence_barrier_init();
         prefetch_tmap(&tm_codes);
         prefetch_tmap(&tm_x);
@@ -131,33 +131,44 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
     const uint32_t tmem = *tmem_slot;
 
     if (warp < kUnpack) {
-        // ---- codes to operands: a row of the weight each; every second step is one half of the warps'
-        const int half = warp / 4, row = 32 * (warp % 4) + lane;
+        // ---- codes to operands: a row of the weight each; the sets of four warps take the steps in turn
+        const uint32_t set = warp / 4, row = 32 * (warp % 4) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
         Ring cs;
         uint32_t r = 0;
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x) {
             const int64_t n = min((int64_t)tile * kRows + row, (int64_t)a.w.N - 1);
-            const uint8_t* const zeros = a.w.zeros ? a.w.zeros + n * a.w.ldz + j0 : nullptr;
+            // a row's zeros, 16 groups at a time, the next ones under way: one byte of a row at a time would be a
+            // load of 32 sectors, and its wait, for every step
+            const uint4* const zeros = reinterpret_cast<const uint4*>(a.w.zeros + n * a.w.ldz);
+            auto zeros_at = [&](int block) { return a.w.zeros && block * 16 < a.w.K / GK ? __ldg(zeros + block) : make_uint4(0, 0, 0, 0); };
+            int z_block = j0 / 16;
+            uint4 z_now = zeros_at(z_block), z_next = zeros_at(z_block + 1);
+            auto zero_of = [&](int j) {
+                const uint32_t w = j % 16 < 4 ? z_now.x : j % 16 < 8 ? z_now.y : j % 16 < 12 ? z_now.z : z_now.w;
+                return zero_pair(w >> (j % 4 * 8));
+            };
             for (int s0 = 0; s0 < steps; s0 += kStageK / kStep, cs.next()) {
                 wait(&c_full[cs.at], cs.parity);
                 const uint32_t at = smem_u32(smem) + cs.at * kStageC + row * 128;
                 for (int i = 0; i < kStageK / kStep && s0 + i < steps; ++i, ++r) {
-                    if ((r & 1) != half) continue;
+                    if (r % kSets != set) continue;
                     const uint32_t buf = r % kSteps;
                     wait(&used[buf], r / kSteps & 1 ^ 1);
                     tc_fence_after();
+                    // 64 bytes of the row: four 16-byte pieces, where the 128-byte swizzle put them
+                    uint4 pieces[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) pieces[h] = ld_u128(at + (((4 * i + h) ^ (row & 7)) << 4));
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {           // 64 elements at a time
                         uint32_t z0 = 0x43084308u, z1 = z0;
-                        if (zeros) {
-                            const int j = ((s0 + i) * kStep + 64 * h) / GK;
-                            if (j < groups) z0 = z1 = zero_pair(__ldg(zeros + j));
-                            if (GK == 32 && j + 1 < groups) z1 = zero_pair(__ldg(zeros + j + 1));
+                        if (a.w.zeros) {                    // a step's groups are of one block of 16
+                            const int j = j0 + ((s0 + i) * kStep + 64 * h) / GK;
+                            if (j / 16 != z_block) z_block = j / 16, z_now = z_next, z_next = zeros_at(z_block + 1);
+                            z0 = zero_of(j), z1 = GK == 32 ? zero_of(j + 1) : z0;
                         }
-                        // 32 bytes of the row: two 16-byte pieces, where the 128-byte swizzle put them
-                        const uint4 p = ld_u128(at + (((4 * i + 2 * h) ^ (row & 7)) << 4));
-                        const uint4 q = ld_u128(at + (((4 * i + 2 * h + 1) ^ (row & 7)) << 4));
+                        const uint4 p = pieces[2 * h], q = pieces[2 * h + 1];
                         const uint32_t words[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
                         uint32_t v[32];
 #pragma unroll
@@ -185,44 +196,68 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
         const int x_block = a.w.K / GK / a.x_blocks;    // groups
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x) {
             const int64_t n = (int64_t)tile * kRows + row, n_in = min(n, (int64_t)a.w.N - 1);
-            const int64_t s_at = n_in * a.w.lds + j0;
-            auto scale_at = [&](int j) {
-                return a.w.scale_bf16 ? __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(a.w.scales) + s_at + j))
-                                      : __ldg(reinterpret_cast<const float*>(a.w.scales) + s_at + j);
-            };
-            float acc[kMine] = {}, ahead[2] = {scale_at(0), groups > 1 ? scale_at(1) : 0.f};
-            for (int j = 0; j < groups; ++j, ++q) {
-                const float scale = ahead[0];
-                ahead[0] = ahead[1];
-                if (j + 2 < groups) ahead[1] = scale_at(j + 2);
-                const uint32_t buf = q % kD;
-                wait(&d_full[buf], q / kD & 1);
-                tc_fence_after();
-                __syncwarp();
-                float d[kMine];
-                tmem_ld(from + MP * buf, d);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&d_empty[buf]);
-                if (a.x_blocks > 1) {
-                    const float* xs = a.x_scale + (j0 + j) / x_block;
-#pragma unroll
-                    for (int i = 0; i < kMine; ++i)
-                        if (m0 + c0 + i < a.M) d[i] *= __ldg(xs + (int64_t)(m0 + c0 + i) * a.x_blocks);
+            // a row's scales, eight groups at a time, the next ones under way: one at a time would be a load of 32
+            // sectors, and its wait, for every group (that took twice the time of all the rest)
+            const uint4* const scales = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.w.scales) + n_in * a.w.lds * (a.w.scale_bf16 ? 2 : 4));
+            auto scales_at = [&](int block, uint4 (&q)[2]) {
+                if (block * 8 >= a.w.K / GK) return;
+                if (a.w.scale_bf16) {
+                    q[0] = __ldg(scales + block);
+                } else {
+                    q[0] = __ldg(scales + 2 * block);
+                    if (block * 8 + 4 < a.w.K / GK) q[1] = __ldg(scales + 2 * block + 1);
                 }
+            };
+            uint4 next[2] = {};
+            scales_at(j0 / 8, next);
+            float acc[kMine] = {};
+            for (int block = j0 / 8; block * 8 < j0 + groups; ++block) {
+                const uint32_t w[8] = {next[0].x, next[0].y, next[0].z, next[0].w, next[1].x, next[1].y, next[1].z, next[1].w};
+                scales_at(block + 1, next);
 #pragma unroll
-                for (int i = 0; i < kMine; ++i) acc[i] = fmaf(d[i], scale, acc[i]);
+                for (int k = 0; k < 8; ++k) {
+                    if (block * 8 + k < j0 || block * 8 + k >= j0 + groups) continue;
+                    const float scale = __uint_as_float(a.w.scale_bf16 ? k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16 : w[k]);
+                    const uint32_t buf = q % kD;
+                    wait(&d_full[buf], q / kD & 1);
+                    tc_fence_after();
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < kMine; c += 16) {
+                        float d[16];
+                        tmem_ld16(from + MP * buf + c, d);
+                        if (c + 16 == kMine) {              // all read: the accumulator is free again
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&d_empty[buf]);
+                        }
+                        if (a.x_blocks > 1) {
+                            const float* xs = a.x_scale + (block * 8 + k) / x_block;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (m0 + c0 + c + i < a.M) d[i] *= __ldg(xs + (int64_t)(m0 + c0 + c + i) * a.x_blocks);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(d[i], scale, acc[c + i]);
+                    }
+                    ++q;
+                }
             }
             if (n < a.w.N) {
+                const int rows = min(kMine, a.M - m0 - c0);
+                if (a.x_scale && a.x_blocks == 1) {
 #pragma unroll
-                for (int i = 0; i < kMine; ++i) {
-                    const int m = m0 + c0 + i;
-                    if (m >= a.M) break;
-                    float v = acc[i];
-                    if (a.x_scale && a.x_blocks == 1) v *= __ldg(a.x_scale + m);
-                    if (cut.slices > 1) a.parts[((int64_t)slice * a.M + m) * a.w.N + n] = v;
-                    else w4_store(a, m, n, v);
+                    for (int i = 0; i < kMine; ++i)
+                        if (i < rows) acc[i] *= __ldg(a.x_scale + m0 + c0 + i);
                 }
+                auto put = [&](auto* to, int64_t stride) {
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i, to += stride)
+                        if (i < rows) *to = from_f32<std::remove_pointer_t<decltype(to)>>(acc[i]);
+                };
+                if (cut.slices > 1) put(a.parts + ((int64_t)slice * a.M + m0 + c0) * a.w.N + n, a.w.N);
+                else if (a.out_bf16) put(reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(m0 + c0) * a.ldo + n, a.ldo);
+                else put(reinterpret_cast<float*>(a.out) + (int64_t)(m0 + c0) * a.ldo + n, a.ldo);
             }
         }
     } else if (warp == kUnpack + kScale) {
@@ -281,8 +316,10 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                     __syncwarp();
                     ++q;
                 }
-                if (elect_one()) mma_commit(&used[buf]);
-                __syncwarp();
+                if (GK != kStep) {
+                    if (elect_one()) mma_commit(&used[buf]);
+                    __syncwarp();
+                }
             }
         // the last commits have arrived before the CTA ends
         for (uint32_t i = r < kSteps ? 0 : r - kSteps; i < r; ++i) wait(&used[i % kSteps], i / kSteps & 1);
