@@ -154,8 +154,6 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                 for (int i = 0; i < kStageK / kStep && s0 + i < steps; ++i, ++r) {
                     if (r % kSets != set) continue;
                     const uint32_t buf = r % kSteps;
-                    wait(&used[buf], r / kSteps & 1 ^ 1);
-                    tc_fence_after();
                     // 64 bytes of the row: four 16-byte pieces, where the 128-byte swizzle put them
                     uint4 pieces[4];
 #pragma unroll
@@ -175,6 +173,10 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                         for (int w = 0; w < 8; ++w)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) v[4 * w + k] = less_zero(words[w] >> (4 * k), w < 4 ? z0 : z1);
+                        if (h == 0) {                       // half of the step is ready before its operand is free
+                            wait(&used[buf], r / kSteps & 1 ^ 1);
+                            tc_fence_after();
+                        }
                         __syncwarp();
                         tmem_st32(tmem + lanes + (uint32_t)(kStep / 2) * buf + 32u * h, v);
                     }
@@ -196,28 +198,22 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
         const int x_block = a.w.K / GK / a.x_blocks;    // groups
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x) {
             const int64_t n = (int64_t)tile * kRows + row, n_in = min(n, (int64_t)a.w.N - 1);
-            // a row's scales, eight groups at a time, the next ones under way: one at a time would be a load of 32
+            // a row's scales, 16 bytes at a time, the next ones under way: one at a time would be a load of 32
             // sectors, and its wait, for every group (that took twice the time of all the rest)
             const uint4* const scales = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.w.scales) + n_in * a.w.lds * (a.w.scale_bf16 ? 2 : 4));
-            auto scales_at = [&](int block, uint4 (&q)[2]) {
-                if (block * 8 >= a.w.K / GK) return;
-                if (a.w.scale_bf16) {
-                    q[0] = __ldg(scales + block);
-                } else {
-                    q[0] = __ldg(scales + 2 * block);
-                    if (block * 8 + 4 < a.w.K / GK) q[1] = __ldg(scales + 2 * block + 1);
-                }
-            };
-            uint4 next[2] = {};
-            scales_at(j0 / 8, next);
+            const int shift = a.w.scale_bf16 ? 3 : 2, per = 1 << shift;     // scales in 16 bytes
+            auto scales_at = [&](int block) { return block << shift < a.w.K / GK ? __ldg(scales + block) : make_uint4(0, 0, 0, 0); };
+            uint4 next = scales_at(j0 >> shift);
             float acc[kMine] = {};
-            for (int block = j0 / 8; block * 8 < j0 + groups; ++block) {
-                const uint32_t w[8] = {next[0].x, next[0].y, next[0].z, next[0].w, next[1].x, next[1].y, next[1].z, next[1].w};
-                scales_at(block + 1, next);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (block * 8 + k < j0 || block * 8 + k >= j0 + groups) continue;
-                    const float scale = __uint_as_float(a.w.scale_bf16 ? k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16 : w[k]);
+            for (int block = j0 >> shift; block << shift < j0 + groups; ++block) {
+                const uint4 now = next;
+                next = scales_at(block + 1);
+                const int to_k = min(j0 + groups - (block << shift), per);
+#pragma unroll 1
+                for (int k = max(j0 - (block << shift), 0); k < to_k; ++k, ++q) {
+                    const int i = a.w.scale_bf16 ? k / 2 : k;               // the same for all threads
+                    const uint32_t word = i & 2 ? (i & 1 ? now.w : now.z) : (i & 1 ? now.y : now.x);
+                    const float scale = __uint_as_float(!a.w.scale_bf16 ? word : k % 2 ? word & 0xffff0000u : word << 16);
                     const uint32_t buf = q % kD;
                     wait(&d_full[buf], q / kD & 1);
                     tc_fence_after();
@@ -232,7 +228,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                             if (lane == 0) mbar_arrive(&d_empty[buf]);
                         }
                         if (a.x_blocks > 1) {
-                            const float* xs = a.x_scale + (block * 8 + k) / x_block;
+                            const float* xs = a.x_scale + ((block << shift) + k) / x_block;
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 if (m0 + c0 + c + i < a.M) d[i] *= __ldg(xs + (int64_t)(m0 + c0 + c + i) * a.x_blocks);
@@ -240,7 +236,6 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
 #pragma unroll
                         for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(d[i], scale, acc[c + i]);
                     }
-                    ++q;
                 }
             }
             if (n < a.w.N) {
