@@ -15,7 +15,6 @@ namespace cg = cooperative_groups;
 namespace ssm {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kSms = 152;
 
 // ------------------------------------------------------------------ probabilities
@@ -39,7 +38,7 @@ __device__ __forceinline__ T two(T a, T b) {
     else if constexpr (K == kSum) return a + b;
     else return a < b ? a : b;
 }
-template <Kind K, typename T>
+template <Kind K, int kWarps, typename T>
 __device__ T row_wide(T v, T* s_warp, T* s_cta, int ctas) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = two<K>(v, __shfl_xor_sync(~0u, v, o));
@@ -99,8 +98,9 @@ template <> struct Raw<float> {
 // powers are taken twice: their unit would do three times as many in the time that the row's bytes take.)  V
 // vectors of eight logits a thread, from the row's first 16-byte border on; what lies before that and behind the
 // last whole vector (up to 14 logits) is one logit each for the first CTA's first threads.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 2 : 1) k_spec_probs(const ProbsArgs a, int ctas) {
+template <typename T, int V, int kThreads>
+__global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThreads : 1) k_spec_probs(const ProbsArgs a, int ctas) {
+    constexpr int kWarps = kThreads / 32;
     __shared__ float s_max[kWarps], s_sum[kWarps], s_max_cta, s_sum_cta;
     __shared__ int s_at[kWarps], s_at_cta;
     const int64_t row = blockIdx.x / (unsigned)ctas;
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 2 : 1) k_spec_
     float m = w;
 #pragma unroll
     for (int i = 0; i < V; ++i) m = max_nan(m, v[i].most());
-    m = row_wide<kMax>(m, s_max, &s_max_cta, ctas);
+    m = row_wide<kMax, kWarps>(m, s_max, &s_max_cta, ctas);
 
     // p = 2^((x - m) f) inv, or 1 at one place, or the same everywhere
     float f = 0.f, inv = quiet_nan();
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 2 : 1) k_spec_
                 for (int k = 0; k < 8; ++k)
                     if (v[i].at(k) == m) least = min(least, head + 8 * (first + (int)threadIdx.x + i * kThreads) + k);
         }
-        least = row_wide<kLeast>(least, s_at, &s_at_cta, ctas);
+        least = row_wide<kLeast, kWarps>(least, s_at, &s_at_cta, ctas);
     } else {
         f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
         float l = ex2((w - m) * f);
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 2 : 1) k_spec_
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int k = 0; k < 8; ++k) l += ex2((v[i].at(k) - m) * f);
-        inv = __fdiv_rn(1.f, row_wide<kSum>(l, s_sum, &s_sum_cta, ctas));
+        inv = __fdiv_rn(1.f, row_wide<kSum, kWarps>(l, s_sum, &s_sum_cta, ctas));
     }
     const int start = head + 8 * first;
     const bool whole = reinterpret_cast<uintptr_t>(p + start) % 16 == 0;
@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 2 : 1) k_spec_
 
 // Rows longer than a cluster's registers hold: read three times, from L2 after the first.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_spec_probs_long(const ProbsArgs a, int ctas) {
+__global__ void __launch_bounds__(512) k_spec_probs_long(const ProbsArgs a, int ctas) {
+    constexpr int kThreads = 512, kWarps = kThreads / 32;
     __shared__ float s_max[kWarps], s_sum[kWarps], s_max_cta, s_sum_cta;
     __shared__ int s_at[kWarps], s_at_cta;
     const int64_t row = blockIdx.x / (unsigned)ctas;
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) k_spec_probs_long(const ProbsArgs a,
     float m = -INFINITY;
 #pragma unroll 8
     for (int i = lo + threadIdx.x; i < hi; i += kThreads) m = max_nan(m, to_f32(x[i]));
-    m = row_wide<kMax>(m, s_max, &s_max_cta, ctas);
+    m = row_wide<kMax, kWarps>(m, s_max, &s_max_cta, ctas);
     if (!(m < INFINITY) || t != t) {
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = quiet_nan();
     } else if (t <= 0x1p-100f || m == -INFINITY) {
@@ -197,14 +198,14 @@ __global__ void __launch_bounds__(kThreads) k_spec_probs_long(const ProbsArgs a,
 #pragma unroll 8
         for (int i = lo + threadIdx.x; i < hi; i += kThreads)
             if (to_f32(x[i]) == m && m > -INFINITY) least = min(least, i);
-        least = row_wide<kLeast>(least, s_at, &s_at_cta, ctas);
+        least = row_wide<kLeast, kWarps>(least, s_at, &s_at_cta, ctas);
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = i == least ? 1.f : 0.f;
     } else {
         const float f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
         float l = 0.f;
 #pragma unroll 8
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) l += ex2((to_f32(x[i]) - m) * f);
-        l = row_wide<kSum>(l, s_sum, &s_sum_cta, ctas);
+        l = row_wide<kSum, kWarps>(l, s_sum, &s_sum_cta, ctas);
         const float inv = __fdiv_rn(1.f, l);
 #pragma unroll 8
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = ex2((to_f32(x[i]) - m) * f) * inv;
@@ -233,7 +234,6 @@ struct Mass {
         const uint64_t x = fixed(pv), y = q ? fixed(qv) : i == off ? 1ull << 62 : 0ull;
         return x > y ? x - y : 0ull;
     }
-    __device__ __forceinline__ uint64_t operator()(int i) const { return less(p[i], q ? q[i] : 0.f, i); }
 };
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
@@ -244,7 +244,9 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 
 // A cluster per request.  Sums are exact integers, so that the order of their parts and the cut do not matter: a
 // warp sums a stretch of the row, and the warp in whose stretch the border falls reads that again (from L2).
-__global__ void __launch_bounds__(kThreads) k_spec_verify(const VerifyArgs a, int ctas) {
+constexpr int kVerifyThreads = 256;
+__global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyArgs a, int ctas) {
+    constexpr int kThreads = kVerifyThreads, kWarps = kThreads / 32;
     constexpr int kBlock = 256;                         // elements that a warp takes at a time, eight loads a lane
     __shared__ int s_kept, s_n;
     __shared__ uint64_t s_sum[kWarps], s_total;
@@ -297,29 +299,31 @@ __global__ void __launch_bounds__(kThreads) k_spec_verify(const VerifyArgs a, in
     const int stretches = ctas * kWarps, per = (vocab + stretches - 1) / stretches;
     const int lo = min(vocab, (rank * kWarps + warp) * per), hi = min(vocab, lo + per);
     // a block's elements of this lane, all loads under way at once
-    auto block = [&](int i0, uint64_t* m, float& mag) {
-        float pv[kBlock / 32], qv[kBlock / 32];
+    constexpr int kEach = kBlock / 32;
+    auto load = [&](int i0, float (&pv)[kEach], float (&qv)[kEach]) {
 #pragma unroll
-        for (int k = 0; k < kBlock / 32; ++k) {
+        for (int k = 0; k < kEach; ++k) {
             const int i = i0 + 32 * k + lane;
             pv[k] = i < hi ? w.p[i] : 0.f;
             qv[k] = w.q && i < hi ? w.q[i] : 0.f;
         }
-#pragma unroll
-        for (int k = 0; k < kBlock / 32; ++k) {
-            m[k] = w.less(pv[k], qv[k], i0 + 32 * k + lane);
-            mag += pv[k] > 0.f ? pv[k] : 0.f;
-        }
     };
-    uint64_t m[kBlock / 32], total, before;
+    float pv[kEach], qv[kEach];
+    uint64_t total, before;
     float mags;
     for (int turn = 0;; ++turn) {
         uint64_t sum = 0;
         float mag = 0.f;
-        for (int i0 = lo; i0 < hi; i0 += kBlock) {
-            block(i0, m, mag);
+        load(lo, pv, qv);
+        for (int i0 = lo; i0 < hi; i0 += kBlock) {      // the next block comes while this one is summed
+            float pn[kEach], qn[kEach];
+            load(i0 + kBlock, pn, qn);
 #pragma unroll
-            for (int k = 0; k < kBlock / 32; ++k) sum += m[k];
+            for (int k = 0; k < kEach; ++k) {
+                sum += w.less(pv[k], qv[k], i0 + 32 * k + lane);
+                mag += pv[k] > 0.f ? pv[k] : 0.f;
+                pv[k] = pn[k], qv[k] = qn[k];
+            }
         }
         sum = warp_sum(sum);
 #pragma unroll
@@ -356,18 +360,17 @@ __global__ void __launch_bounds__(kThreads) k_spec_verify(const VerifyArgs a, in
     const uint64_t border = __umul64hi(__float2ull_rz(draw * 0x1p64f), total);
     if (before > border || border >= before + s_sum[warp]) return;
     for (int i0 = lo; i0 < hi; i0 += kBlock) {
-        float unused = 0.f;
-        block(i0, m, unused);
-        uint64_t all = 0;
+        load(i0, pv, qv);
+        uint64_t m[kEach], all = 0;
 #pragma unroll
-        for (int k = 0; k < kBlock / 32; ++k) all += m[k];
+        for (int k = 0; k < kEach; ++k) m[k] = w.less(pv[k], qv[k], i0 + 32 * k + lane), all += m[k];
         all = warp_sum(all);
         if (before + all <= border) {
             before += all;
             continue;
         }
 #pragma unroll
-        for (int k = 0; k < kBlock / 32; ++k) {
+        for (int k = 0; k < kEach; ++k) {
             uint64_t c = m[k];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -385,11 +388,11 @@ __global__ void __launch_bounds__(kThreads) k_spec_verify(const VerifyArgs a, in
 }
 
 template <typename... P, typename... A>
-int launch(void (*kern)(P...), int64_t rows, int ctas, cudaStream_t stream, const char** why, const A&... args) {
+int launch(void (*kern)(P...), int threads, int64_t rows, int ctas, cudaStream_t stream, const char** why, const A&... args) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3((unsigned)(rows * ctas));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = stream;
     if (ctas > 1) {
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -405,35 +408,41 @@ int launch(void (*kern)(P...), int64_t rows, int ctas, cudaStream_t stream, cons
     return -1;
 }
 
-// CTAs for a row of n elements: more while each still has `least` of them and `each` fit an SM.
-int ctas_for(int64_t rows, int64_t n, int64_t least, int each) {
-    int c = 1;
-    while (c < 8 && rows * 2 * c <= each * kSms && n >= 2 * c * least) c *= 2;
-    return c;
-}
-
-template <typename T>
+// A row's CTAs: the fewest powers of two that hold it with kMost vectors a thread (up to eight CTAs), more while each
+// still has a vector for every thread and all rows' CTAs are on the GPU at once.
+template <typename T, int kThreads>
 int probs(const ProbsArgs& a, cudaStream_t stream, const char** why) {
     constexpr int kVec = 8 * kThreads;                  // logits of a vector for each thread
-    constexpr int kMost = sizeof(T) == 2 ? 8 : 4;       // vectors with which two CTAs fit an SM
-    int ctas = ctas_for(a.n_rows, a.vocab, kVec, 2);
-    while (ctas < 8 && a.vocab > (int64_t)kMost * kVec * ctas) ctas *= 2;
+    constexpr int kMost = sizeof(T) == 2 ? 8 : 4;       // vectors with which 1024 threads fit an SM
+    int ctas = 1;
+    while (ctas < 8 && (a.vocab > (int64_t)kMost * kVec * ctas || (a.n_rows * 2 * ctas <= 1024 / kThreads * kSms && a.vocab >= 2 * ctas * kVec)))
+        ctas *= 2;
     const int64_t each = (a.vocab / 8 + ctas - 1) / ctas * 8;
-    if (each <= kVec) return launch(k_spec_probs<T, 1>, a.n_rows, ctas, stream, why, a);
-    if (each <= 2 * kVec) return launch(k_spec_probs<T, 2>, a.n_rows, ctas, stream, why, a);
-    if (each <= 4 * kVec) return launch(k_spec_probs<T, 4>, a.n_rows, ctas, stream, why, a);
-    if (each <= 8 * kVec) return launch(k_spec_probs<T, 8>, a.n_rows, ctas, stream, why, a);
-    return launch(k_spec_probs_long<T>, a.n_rows, ctas, stream, why, a);
+    if (each <= kVec) return launch(k_spec_probs<T, 1, kThreads>, kThreads, a.n_rows, ctas, stream, why, a);
+    if (each <= 2 * kVec) return launch(k_spec_probs<T, 2, kThreads>, kThreads, a.n_rows, ctas, stream, why, a);
+    if (each <= 4 * kVec) return launch(k_spec_probs<T, 4, kThreads>, kThreads, a.n_rows, ctas, stream, why, a);
+    if (each <= 8 * kVec) return launch(k_spec_probs<T, 8, kThreads>, kThreads, a.n_rows, ctas, stream, why, a);
+    return launch(k_spec_probs_long<T>, 512, a.n_rows, ctas, stream, why, a);
+}
+
+// 256 threads where a cluster of eight such CTAs holds the row: four to an SM, in different phases.
+template <typename T>
+int probs_of(const ProbsArgs& a, cudaStream_t stream, const char** why) {
+    return a.vocab <= 8 * 8 * 256 * (sizeof(T) == 2 ? 8 : 4) ? probs<T, 256>(a, stream, why) : probs<T, 512>(a, stream, why);
 }
 
 }  // namespace
 
 int launch_spec_probs(const ProbsArgs& a, bool in_bf16, cudaStream_t stream, const char** why) {
-    return in_bf16 ? probs<__nv_bfloat16>(a, stream, why) : probs<float>(a, stream, why);
+    return in_bf16 ? probs_of<__nv_bfloat16>(a, stream, why) : probs_of<float>(a, stream, why);
 }
 
 int launch_spec_verify(const VerifyArgs& a, cudaStream_t stream, const char** why) {
-    return launch(k_spec_verify, a.batch, ctas_for(a.batch, a.vocab, 2048, 3), stream, why, a);
+    // up to eight CTAs a request, each with 2048 elements at least, as many as are on the GPU at once, four to an SM
+    // (64 requests of 131072: eight CTAs of 256 threads 25 us, four 31; seven of 512 threads 30, four 26)
+    int ctas = 1;
+    while (ctas < 8 && (int64_t)a.batch * 2 * ctas <= 4 * kSms && a.vocab >= 2 * ctas * 2048) ctas *= 2;
+    return launch(k_spec_verify, kVerifyThreads, a.batch, ctas, stream, why, a);
 }
 
 }  // namespace ssm
