@@ -131,7 +131,7 @@ def main():
     x = torch.randn(3, 512, device="cuda").to(torch.bfloat16)
     for _ in range(8):
         x = layer.decode(x)
-        x = x / x.float().square().mean(-1, keepdim=True).sqrt().to(x.dtype)
+        x = ssm.norm_rms(x)[0]
     torch.cuda.synchronize()
     status = ssm.device_status()
     print(f"cached tokens {layer.lens}, last output RMS {float(x.float().square().mean().sqrt()):.3f}, status {status}")

@@ -408,6 +408,7 @@ __global__ void __launch_bounds__(256) k_w4_join(const W4LinearArgs a, int slice
     if (n >= a.w.N) return;
     const int m = blockIdx.y;
     float v = 0.f;
+#pragma unroll 8
     for (int s = 0; s < slices; ++s) v += a.parts[((int64_t)s * a.M + m) * a.w.N + n];
     w4_store(a, m, n, v);
 }
@@ -518,14 +519,24 @@ int launch_w4_join(const W4LinearArgs& a, int slices, cudaStream_t stream, const
     return -1;
 }
 
+// Whether a call goes to the tiles of w4_tiles.cu: from nine rows of x on where the weight is large.  They unpack it
+// once for 64 rows and cost two or three kernels; here it is unpacked for every 16 rows, and sums of 16 columns
+// are what a turn waits for.  Measured (us, here / tiles, groups of 128): 16 rows x 4096 x 4096 10.0 / 10.4, 8192 x
+// 4096 12.2 / 14.3, 16384 x 4096 28 / 20, 50021 x 2560 81 / 33; 17 rows x 2048 x 2048 5.6 / 6.6, 4096 x 4096 11.9 / 10.3;
+// 64 rows x 768 x 1536 5.2 / 9.2, 2048 x 2048 7.9 / 7.9, 4096 x 4096 19.6 / 11.4.
+static bool in_tiles(int M, const W4Weight& w) {
+    const int64_t work = (int64_t)((M + 15) / 16) * w.N * w.K;
+    return M > 16 ? work > (1 << 24) : M > 8 && work > 3 * (1 << 24);
+}
+
 size_t w4_linear_workspace(int M, const W4Weight& w) {
-    if (M > 16) return w4_tiles_workspace(M, w);
+    if (in_tiles(M, w)) return w4_tiles_workspace(M, w);
     const int slices = M <= 8 ? best_plan<1>(M, w).slices : best_plan<2>(M, w).slices;
     return slices == 1 ? 0 : (size_t)slices * M * w.N * sizeof(float);
 }
 
 int launch_w4_linear(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, const char** why) {
-    if (a.M > 16) return launch_w4_tiles(a, status, stream, why);
+    if (in_tiles(a.M, a.w)) return launch_w4_tiles(a, status, stream, why);
     return a.M <= 8 ? linear_of<1>(a, status, stream, why) : linear_of<2>(a, status, stream, why);
 }
 

@@ -1,4 +1,4 @@
-// w4_tiles.cu -- w4_linear for more rows of x than a matrix instruction of a warp takes: tiles of 128 rows of the
+// w4_tiles.cu -- w4_linear for more than a few rows of x and a large weight: tiles of 128 rows of the
 // 4-bit weight against up to 64 rows of x on the 5th-generation tensor cores.
 //
 // With 64 rows the product costs a warp's matrix instructions several times what the weight's bytes take, and the
@@ -356,12 +356,12 @@ constexpr int kSms = 152;
 int rows_of(int M) { return M <= 32 ? 32 : 64; }
 
 // Slices of the rows where the tiles alone leave SMs idle: as for the kernel of few rows, by the CTA with most work
-// at an SM's share of the copy rate, and two microseconds for the second kernel.
+// at an SM's share of the copy rate, and for the second kernel two microseconds and the slices' sums at 4 TB/s.
 Cut cut_of(int M, const W4Weight& w) {
     Cut best{};
     int64_t least = 0;
     const int stages = (w.K + kStageK - 1) / kStageK;
-    for (int s = 1; s <= 8 && s <= stages; ++s) {
+    for (int s = 1; s <= 32 && s <= stages; ++s) {
         Cut c;
         c.tiles = (w.N + kRows - 1) / kRows;
         c.m_blocks = (M + rows_of(M) - 1) / rows_of(M);
@@ -370,7 +370,7 @@ Cut cut_of(int M, const W4Weight& w) {
         int walkers = kSms / (c.m_blocks * c.slices);
         walkers = walkers < 1 ? 1 : walkers > c.tiles ? c.tiles : walkers;
         const int64_t bytes = (int64_t)((c.tiles + walkers - 1) / walkers) * c.slice_k * (kRows / 2);
-        const int64_t ns = bytes / 44 + (c.slices > 1 ? 2000 : 0);
+        const int64_t ns = bytes / 44 + (c.slices > 1 ? 2000 + (int64_t)c.slices * M * w.N * 8 / 4000 : 0);
         if (s == 1 || ns < least) best = c, least = ns;
     }
     return best;

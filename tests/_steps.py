@@ -101,12 +101,14 @@ def activations64(x, x_scale):
 
 def check_linear(out, x, codes, scales, zeros, x_scale):
     """Products are exact.  Their sum goes through no more than 128 steps in sequence (a matrix instruction's own
-    sum counted as two), each cut off (2 U) or rounded at the size of sum |x w|; the scales' products add 4 U."""
+    sum counted as two), each cut off (2 U) or rounded at the size of sum |x w|; the scales' products add 4 U.
+    Where a thread adds all groups of a row one after another, each addition is rounded (U): that many U, at most
+    16 steps (2 U) inside a group, 8 U for the sum of slices and 4 U."""
     xv, w = activations64(x, x_scale), weight64(codes, scales, zeros)
     ref, mag = xv @ w.T, np.abs(xv) @ np.abs(w).T
     got = to64(out)
     assert got.shape == ref.shape
-    bad = np.abs(got - ref) > mag * (260 * U) + np.abs(ref) * half_step(out.dtype) * 1.01 + 2.0 ** -126
+    bad = np.abs(got - ref) > mag * (max(260, scales.shape[1] + 44) * U) + np.abs(ref) * half_step(out.dtype) * 1.01 + 2.0 ** -126
     assert not bad.any(), (np.argwhere(bad)[0], got[bad][0], ref[bad][0], mag[bad][0])
 
 

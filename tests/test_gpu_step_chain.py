@@ -26,6 +26,11 @@ class Setup:
         self.p, self.q = p.to(DEV), torch.softmax(2 * torch.randn(m, drafts, n, generator=g), -1).to(DEV)
         self.draft = torch.randint(0, n, (m, drafts), generator=g, dtype=torch.int32).to(DEV)
         self.u = torch.rand(m, drafts + 1, generator=g).to(DEV)
+        # rows split into slices: few rows of x, and many of them against a larger weight
+        self.xs = torch.randn(m, 8192, generator=g).to(torch.bfloat16).to(DEV)
+        self.ws = ssm.w4_quantize((torch.randn(n, 8192, generator=g) / 90).to(DEV), 128)[:2]
+        self.xm = torch.randn(150, 4096, generator=g).to(torch.bfloat16).to(DEV)
+        self.wm = ssm.w4_quantize((torch.randn(600, 4096, generator=g) / 64).to(DEV), 64, True)
         torch.cuda.synchronize()
 
     def norm(self, **kw):
@@ -37,6 +42,12 @@ class Setup:
     def linear(self, **kw):
         return (ssm.w4_linear(self.x, *self.w, out_dtype=torch.float32, **kw),)
 
+    def slices(self, **kw):
+        return (ssm.w4_linear(self.xs, *self.ws, out_dtype=torch.float32, **kw),)
+
+    def tiles(self, **kw):
+        return (ssm.w4_linear(self.xm, *self.wm, out_dtype=torch.float32, **kw),)
+
     def probs(self, **kw):
         return (ssm.spec_probs(self.logits, self.t, **kw),)
 
@@ -44,7 +55,12 @@ class Setup:
         return ssm.spec_verify(self.draft, self.p, self.u, self.q, **kw)
 
 
-CALLS = ["norm", "quantize", "linear", "probs", "verify"]
+CALLS = ["norm", "quantize", "linear", "slices", "tiles", "probs", "verify"]
+
+
+def test_the_calls_split_rows_as_meant():
+    assert ssm.w4_linear_workspace_bytes(6, 700, 8192, 128) >= 2 * 6 * 700 * 4
+    assert ssm.w4_linear_workspace_bytes(150, 600, 4096, 64) >= 192 * 4096 * 2 + 2 * 150 * 600 * 4
 
 
 @pytest.mark.parametrize("call", CALLS)
@@ -97,9 +113,9 @@ def test_captured_calls_replay_on_new_inputs(call):
         outs = getattr(a, call)()
     for turn in range(3):
         if turn == 1:
-            for name in ("x", "res", "W", "logits", "t", "p", "q", "draft", "u"):
+            for name in ("x", "res", "W", "logits", "t", "p", "q", "draft", "u", "xs", "xm"):
                 getattr(a, name).copy_(getattr(b, name))
-            for mine, other in zip(a.w, b.w):
+            for mine, other in zip(a.w + a.ws + a.wm, b.w + b.ws + b.wm):
                 mine.copy_(other)
         for o in outs:
             o.zero_()

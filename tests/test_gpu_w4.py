@@ -75,6 +75,64 @@ def test_types_of_scales_and_outputs(m, scales, out):
     run(m, 77, 768, 64, BF16, 1, scales, False, out)
 
 
+# many rows of x and a weight large enough for its tiles: sixteen rows and more times 2^24 products, or nine and a
+# weight of three times that; rows at the borders of 16, 32 and 64, K from one group on and to the longest
+@pytest.mark.parametrize("m,n,k,group", [(256, 33001, 32, 32), (250, 11001, 96, 32), (256, 6601, 160, 32), (241, 5501, 192, 64),
+                                         (255, 16500, 64, 64), (200, 2703, 480, 32), (129, 1901, 992, 32), (65, 3301, 1024, 64),
+                                         (64, 4099, 1152, 128), (33, 2803, 2048, 128), (32, 8300, 1024, 64), (17, 16700, 512, 128),
+                                         (64, 257, 16512, 128), (33, 201, 28160, 64), (64, 130, 32768, 32), (24, 300, 28160, 128),
+                                         (9, 12400, 4096, 128), (16, 1601, 32768, 64), (12, 50001, 1024, 32)])
+@pytest.mark.parametrize("x,zeros", [(BF16, False), (I8, True)])
+def test_tiles(m, n, k, group, x, zeros):
+    run(m, n, k, group, x, 1, BF16 if zeros else F32, zeros, F32)
+
+
+@pytest.mark.parametrize("blocks,k,group", [(2, 1024, 128), (32, 1024, 32), (3, 1152, 128), (8, 2560, 64)])
+@pytest.mark.parametrize("m,scales,out", [(68, BF16, F32), (256, F32, BF16)])
+def test_tiles_with_blocks_of_activation_scales(m, scales, out, blocks, k, group):
+    run(m, 3701, k, group, I8, blocks, scales, True, out, pad=1)
+
+
+def test_tiles_keep_to_their_rows_and_outputs():
+    """Infinities, NaN and bad scales stay where they are; strided x; outputs inside a wider tensor; workspaces of
+    exactly the asked size; the border between the two ways of a call agrees."""
+    g = torch.Generator().manual_seed(17)
+    m, n, k = 70, 901, 4096
+    x = torch.randn(2 * m, k + 64, generator=g).to(BF16).to(DEV)[::2, 64:]
+    codes, scales, zeros = weight(g, n, k, 64, F32, True, pad=1)
+    clean = ssm.w4_linear(x, codes, scales, zeros, out_dtype=F32)
+    check_linear(clean, x, codes, scales, zeros, None)
+    need = ssm.w4_linear_workspace_bytes(m, n, k, 64)
+    assert need > 128 * k * 2                          # x in its order, and the sums of slices
+    for out in (BF16, F32):
+        big = torch.full((m + 2, n + 20), 9.0, device=DEV, dtype=out)
+        work = torch.full((need + 256,), 77, device=DEV, dtype=U8)
+        got = ssm.w4_linear(x, codes, scales, zeros, out=big[1:-1, 7:7 + n], workspace=work[:need])
+        assert torch.equal(got, clean.to(out)) and (work[need:] == 77).all()
+        assert (big[:, :7] == 9).all() and (big[:, 7 + n:] == 9).all() and (big[0] == 9).all() and (big[-1] == 9).all()
+    x[1, 5], x[4, 200], x[66, 1023] = float("inf"), float("nan"), float("-inf")
+    scales[17, 3] = float("nan")
+    got = ssm.w4_linear(x, codes, scales, zeros, out_dtype=F32)
+    rows, cols = torch.ones(m, dtype=torch.bool, device=DEV), torch.ones(n, dtype=torch.bool, device=DEV)
+    rows[[1, 4, 66]] = False
+    cols[17] = False
+    assert torch.equal(got[rows][:, cols], clean[rows][:, cols])
+    assert not torch.isfinite(got[~rows]).any() and torch.isnan(got[:, 17]).all()
+
+
+def test_slices_of_few_rows_with_a_given_workspace():
+    g = torch.Generator().manual_seed(19)
+    for m, n, k in ((1, 700, 16384), (8, 1000, 8192), (16, 700, 16384), (20, 300, 16384)):
+        x = torch.randn(m, k, generator=g).to(BF16).to(DEV)
+        codes, scales, _ = weight(g, n, k, 128, BF16)
+        need = ssm.w4_linear_workspace_bytes(m, n, k, 128)
+        assert need >= 2 * m * n * 4 and need % (m * n * 4) == 0
+        work = torch.full((need + 64,), 77, device=DEV, dtype=U8)
+        got = ssm.w4_linear(x, codes, scales, out_dtype=F32, workspace=work[:need])
+        check_linear(got, x, codes, scales, None, None)
+        assert (work[need:] == 77).all()
+
+
 def test_strides_and_neighbours():
     """Slices of wider tensors; outputs in place, at odd offsets, and nothing around them touched."""
     g = torch.Generator().manual_seed(11)
@@ -141,7 +199,7 @@ def test_zeros_count_by_their_low_half():
 def test_repeats_agree_bit_by_bit():
     g = torch.Generator().manual_seed(16)
     w = weight(g, 1000, 3328, 128, BF16, True)
-    for m in (1, 8, 30, 64):
+    for m in (1, 8, 30, 64, 100):
         x = torch.randn(m, 3328, generator=g).to(BF16).to(DEV)
         a = ssm.w4_linear(x, *w, out_dtype=F32)
         for _ in range(4):
