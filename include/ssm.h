@@ -723,8 +723,8 @@ int spec_probs(int64_t n_rows, int64_t vocab, ssm_dtype_t in_dtype, const void* 
  *   u                    [batch][n_max + 1] float32 in [0, 1); below 0 or NaN counts as 0, 1 and more as 1 - 2^-24
  *   tokens               [batch][n_max + 1] int32: the kept tokens, the next one, then -1
  *   n_kept               [batch] int32
- * Probabilities are >= 0 and sum up to about 1: a negative one or a NaN counts as 0, and a row that is drawn from
- * and sums up to 0 or to 4 or more gives token -1.
+ * Probabilities are >= 0 and sum up to about 1: a negative one or a NaN counts as 0, and a row p that is
+ * drawn from and sums up to 0 or to 3.99 or more gives token -1.
  */
 int spec_verify(int batch, int n_max, int64_t vocab, const int32_t* draft, const int32_t* n_draft,
                 const float* target_probs, int64_t tp_stride_b, int64_t tp_stride_t,

@@ -226,29 +226,56 @@ __device__ __forceinline__ uint64_t fixed(float p) {
 }
 __device__ __forceinline__ float uniform(float v) { return v > 0.f ? fminf(v, 0x1.fffffep-1f) : 0.f; }
 
-// The row that the next token is drawn from, element by element.
-struct Mass {
-    const float *p, *q;
-    int off;
-    __device__ __forceinline__ uint64_t less(float pv, float qv, int i) const {
-        const uint64_t x = fixed(pv), y = q ? fixed(qv) : i == off ? 1ull << 62 : 0ull;
-        return x > y ? x - y : 0ull;
+// What is left of p without q, both >= 0, in those integers.
+__device__ __forceinline__ uint64_t less(float p, float q) { return p > q ? fixed(p) - fixed(q) : 0ull; }
+
+// Sums of the same, without shifts of 64 bits (64 requests x 131072 21.5 us, with shifts 23.0).  A value below 4 is cut into three: added to 8 towards 0 its places down to 2^-20 are the sum's last bits,
+// the rest, exact, added to 2^-20 gives those down to 2^-43, and what is left of that, added to 2^-39, those down to
+// 2^-62.  The constants' bits go out in the differences of p's parts and q's.
+struct Parts {
+    uint32_t a = 0, b = 0, c = 0;
+    __device__ __forceinline__ void add(float p, float q) {
+        const float pa = __fadd_rz(p, 8.f), qa = __fadd_rz(q, 8.f);
+        const float pr = p - (pa - 8.f), qr = q - (qa - 8.f);
+        const float pb = __fadd_rz(pr, 0x1p-20f), qb = __fadd_rz(qr, 0x1p-20f);
+        const float pc = __fadd_rz(pr - (pb - 0x1p-20f), 0x1p-39f), qc = __fadd_rz(qr - (qb - 0x1p-20f), 0x1p-39f);
+        if (p > q) {
+            a += __float_as_uint(pa) - __float_as_uint(qa);
+            b += __float_as_uint(pb) - __float_as_uint(qb);
+            c += __float_as_uint(pc) - __float_as_uint(qc);
+        }
+    }
+    // of up to 256 values: the parts, below 2^22, 2^23 and 2^19, stay in 32 bits, the lower two with their signs
+    __device__ __forceinline__ uint64_t sum() const {
+        return ((uint64_t)a << 42) + ((uint64_t)(int64_t)(int32_t)b << 19) + (uint64_t)(int64_t)(int32_t)c;
     }
 };
 
-__device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
+// The row that the next token is drawn from.
+struct Mass {
+    const float *p, *q;
+    int off;
+};
+
+template <typename T> __device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
     return v;
 }
 
 // A cluster per request.  Sums are exact integers, so that the order of their parts and the cut do not matter: a
-// warp sums a stretch of the row, and the warp in whose stretch the border falls reads that again (from L2).
+// warp sums a stretch of the row, its lanes note their sums up to eight times on the way, and the warp in whose
+// stretch the border falls reads again (from L2) what lies between two notes.  Without notes it read its stretch
+// from the start, block by block.  Of the 21.5 us of 64 requests x 131072 (67 MB, 9.9 us at the copy rate) the checks of the
+// drafted tokens take 2 (three reads, each waiting for the one before), the sums 9, the cluster's exchange and
+// its slowest CTA 3, the search 2, starting and ending the rest.  One request: 7 us, the same chain of waits.
 constexpr int kVerifyThreads = 256;
 __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyArgs a, int ctas) {
     constexpr int kThreads = kVerifyThreads, kWarps = kThreads / 32;
-    constexpr int kBlock = 256;                         // elements that a warp takes at a time, eight loads a lane
+    constexpr int kEach = 8, kBlock = 32 * kEach;       // elements that a warp takes at a time
+    constexpr int kNotes = 8;                           // of a lane's sum on the way
     __shared__ int s_kept, s_n;
+    __shared__ uint64_t s_note[kWarps][kNotes][32];
     __shared__ uint64_t s_sum[kWarps], s_total;
     __shared__ float s_mag[kWarps], s_mags;
     const int b = blockIdx.x / (unsigned)ctas, rank = blockIdx.x % (unsigned)ctas;
@@ -298,36 +325,48 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
     }
     const int stretches = ctas * kWarps, per = (vocab + stretches - 1) / stretches;
     const int lo = min(vocab, (rank * kWarps + warp) * per), hi = min(vocab, lo + per);
-    // a block's elements of this lane, all loads under way at once
-    constexpr int kEach = kBlock / 32;
-    auto load = [&](int i0, float (&pv)[kEach], float (&qv)[kEach]) {
+    const int step = ((per + kBlock - 1) / kBlock + kNotes - 1) / kNotes * kBlock;      // elements between two notes
+    // a lane's elements of a block, `apart` from each other, all loads under way at once; negative ones and NaN are 0
+    auto load = [&](int i0, int apart, float (&pv)[kEach], float (&qv)[kEach]) {
+        const bool whole = i0 + kBlock <= hi;
+        i0 += apart == 1 ? lane * kEach : lane;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const int i = i0 + 32 * k + lane;
-            pv[k] = i < hi ? w.p[i] : 0.f;
-            qv[k] = w.q && i < hi ? w.q[i] : 0.f;
+            const int i = i0 + apart * k;
+            pv[k] = whole || i < hi ? w.p[i] : 0.f;
+            qv[k] = w.q && (whole || i < hi) ? w.q[i] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) pv[k] = fmaxf(pv[k], 0.f), qv[k] = fmaxf(qv[k], 0.f);
+        if (w.off >= 0) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k)
+                if (i0 + apart * k == w.off) qv[k] = 1.f;
         }
     };
     float pv[kEach], qv[kEach];
     uint64_t total, before;
     float mags;
+    int notes;
     for (int turn = 0;; ++turn) {
         uint64_t sum = 0;
         float mag = 0.f;
-        load(lo, pv, qv);
-        for (int i0 = lo; i0 < hi; i0 += kBlock) {      // the next block comes while this one is summed
-            float pn[kEach], qn[kEach];
-            load(i0 + kBlock, pn, qn);
+        notes = 0;
+        for (int i0 = lo; i0 < hi; ++notes) {
+            for (const int to = min(i0 + step, hi); i0 < to; i0 += kBlock) {
+                load(i0, 32, pv, qv);
+                Parts parts;
 #pragma unroll
-            for (int k = 0; k < kEach; ++k) {
-                sum += w.less(pv[k], qv[k], i0 + 32 * k + lane);
-                mag += pv[k] > 0.f ? pv[k] : 0.f;
-                pv[k] = pn[k], qv[k] = qn[k];
+                for (int k = 0; k < kEach; ++k) {
+                    parts.add(pv[k], qv[k]);
+                    mag += pv[k];
+                }
+                sum += parts.sum();
             }
+            s_note[warp][notes][lane] = sum;
         }
         sum = warp_sum(sum);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mag += __shfl_xor_sync(~0u, mag, o);
+        mag = warp_sum(mag);
         if (lane == 0) s_sum[warp] = sum, s_mag[warp] = mag;
         __syncthreads();
         total = before = 0, mags = 0.f;
@@ -339,52 +378,61 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
             auto cluster = cg::this_cluster();
             if (threadIdx.x == 0) s_total = total, s_mags = mags;
             cluster.sync();
-            total = 0, mags = 0.f;
-            for (int r = 0; r < ctas; ++r) {
-                const uint64_t v = *cluster.map_shared_rank(&s_total, r);
-                before += r < rank ? v : 0;
-                total += v, mags += *cluster.map_shared_rank(&s_mags, r);
-            }
-            cluster.sync();                             // read by all: free to be written again, or left
+            const uint64_t v = lane < ctas ? *cluster.map_shared_rank(&s_total, lane) : 0;
+            mags = warp_sum(lane < ctas ? *cluster.map_shared_rank(&s_mags, lane) : 0.f);
+            total = warp_sum(v);
+            before += warp_sum(lane < rank ? v : 0);
+            asm volatile("barrier.cluster.arrive.release;" ::: "memory");       // read
         } else {
             __syncthreads();
         }
         if (total > 0 || turn == 1 || (!w.q && w.off < 0)) break;
         w.q = nullptr, w.off = -1;                      // nothing left of p - q: p itself
-    }
-    if (total == 0 || !(mags < 3.99f)) {                // no distribution
-        if (rank == 0 && threadIdx.x == 0) out[kept] = -1;
-        return;
+        if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     }
     // the first index whose running sum exceeds floor(u * total)
     const uint64_t border = __umul64hi(__float2ull_rz(draw * 0x1p64f), total);
-    if (before > border || border >= before + s_sum[warp]) return;
-    for (int i0 = lo; i0 < hi; i0 += kBlock) {
-        load(i0, pv, qv);
-        uint64_t m[kEach], all = 0;
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) m[k] = w.less(pv[k], qv[k], i0 + 32 * k + lane), all += m[k];
-        all = warp_sum(all);
-        if (before + all <= border) {
-            before += all;
-            continue;
+    if (total == 0 || !(mags < 3.99f)) {                // no distribution
+        if (rank == 0 && threadIdx.x == 0) out[kept] = -1;
+    } else if (before <= border && border < before + s_sum[warp]) {
+        // the notes say between which two of them; that is read again (from L2)
+        uint64_t at = 0;
+        if (lane < notes) {
+#pragma unroll 8
+            for (int k = 0; k < 32; ++k) at += s_note[warp][lane][(k + lane) % 32];
         }
+        const int note = __ffs(__ballot_sync(~0u, lane < notes && before + at > border)) - 1;
+        if (note > 0) before += __shfl_sync(~0u, at, note - 1);
+        for (int i0 = lo + note * step; i0 < hi; i0 += kBlock) {
+            load(i0, 1, pv, qv);
+            uint64_t m[kEach], mine = 0;
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            uint64_t c = m[k];
+            for (int k = 0; k < kEach; ++k) m[k] = less(pv[k], qv[k]), mine += m[k];
+            uint64_t to = mine;                         // of the lanes up to this one
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const uint64_t t = __shfl_up_sync(~0u, c, o);
-                if (lane >= o) c += t;
+                const uint64_t t = __shfl_up_sync(~0u, to, o);
+                if (lane >= o) to += t;
             }
-            const unsigned over = __ballot_sync(~0u, before + c > border);
+            const unsigned over = __ballot_sync(~0u, before + to > border);
             if (over) {
-                if (lane == 0) out[kept] = i0 + 32 * k + __ffs(over) - 1;
-                return;
+                if (lane == __ffs(over) - 1) {
+                    before += to - mine;
+                    int k = 0;
+#pragma unroll
+                    for (int j = 0; j + 1 < kEach; ++j) {
+                        before += m[j];
+                        k += before <= border;
+                    }
+                    out[kept] = i0 + kEach * lane + k;
+                }
+                break;
             }
-            before += __shfl_sync(~0u, c, 31);
+            before += __shfl_sync(~0u, to, 31);
         }
     }
+    __syncwarp();
+    if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");   // all have read: free to leave
 }
 
 template <typename... P, typename... A>
@@ -439,7 +487,7 @@ int launch_spec_probs(const ProbsArgs& a, bool in_bf16, cudaStream_t stream, con
 
 int launch_spec_verify(const VerifyArgs& a, cudaStream_t stream, const char** why) {
     // up to eight CTAs a request, each with 2048 elements at least, as many as are on the GPU at once, four to an SM
-    // (64 requests of 131072: eight CTAs of 256 threads 25 us, four 31; seven of 512 threads 30, four 26)
+    // (64 requests of 131072: eight CTAs of 256 threads 22 us, four of 512 23, eight of 512 28)
     int ctas = 1;
     while (ctas < 8 && (int64_t)a.batch * 2 * ctas <= 4 * kSms && a.vocab >= 2 * ctas * 2048) ctas *= 2;
     return launch(k_spec_verify, kVerifyThreads, a.batch, ctas, stream, why, a);

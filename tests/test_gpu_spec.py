@@ -157,6 +157,28 @@ def test_rows_without_mass_and_values_that_are_none():
     assert tokens[0, 0] == -1 and kept[0] == 0
 
 
+def test_draft_probabilities_above_one_leave_nothing_there():
+    draft, p, u, q, _ = case(6, 2, 300, 5, near=1.0)
+    u[:, 0] = 0.97
+    for b, v in enumerate((1.5, 2.0, 3.99, 4.0, 7.0, INF)):
+        q[b, :, 1::2] = v
+    same(draft, p, u, q)
+
+
+def test_masses_of_every_size():
+    """Probabilities from 1 down to below 2^-62, and residuals that are the last bits of what they come from."""
+    g = torch.Generator().manual_seed(6)
+    p = (2.0 ** -torch.randint(0, 80, (40, 2, 700), generator=g).double() * (1 + torch.rand(40, 2, 700, generator=g, dtype=torch.float64)))
+    p = (p / p.sum(-1, keepdim=True) * (0.5 + torch.rand(40, 2, 1, generator=g, dtype=torch.float64))).float()
+    up, down = torch.nextafter(p[:, :1], torch.tensor(INF)), torch.nextafter(p[:, :1], torch.tensor(0.0))
+    q = torch.where(torch.rand(40, 1, 700, generator=g) < 0.5, up, down)
+    draft = torch.randint(0, 700, (40, 1), generator=g).to(I32)
+    q[torch.arange(40), 0, draft[:, 0].long()] *= 2                  # refused for u from a half on
+    u = 0.6 + 0.4 * torch.rand(40, 2, generator=g)
+    same(draft, p, u, q)
+    same(draft, p, u)
+
+
 @pytest.mark.parametrize("q", [True, False])
 def test_uniform_numbers_out_of_range(q):
     draft, p, u, qs, _ = case(6, 2, 64, 3, q=q)
