@@ -663,13 +663,15 @@ int w4_quantize(int64_t N, int64_t K, int group, ssm_dtype_t in_dtype, const voi
                 uint8_t* zeros, int64_t ldz, void* cuda_stream);
 
 /* Bytes of device workspace w4_linear needs for these sizes (0 on a bad size): the sums of the slices into which
- * long rows are cut. */
+ * long rows are cut, and, where many rows of x meet a large weight, x in the order in which codes come out of words. */
 size_t w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);
 
 /*
  * w4_linear -- out[m][n] = sum_k x[m][k] W[n][k] with a 4-bit W, for the few rows of a decode step.  Products
  * of x and codes are exact and are summed in fp32 within a group, the groups' sums times their scales in fp32, in
- * an order that the sizes alone choose.  With an infinity or NaN in a row of x none of that row's outputs is finite.
+ * an order that the sizes alone choose.  A group's sum may be taken as that of x (16 + code), less (16 + zero) times
+ * that of x: errors are those of sums of 31 |x|, whatever the codes, and elements from 2^115 on can overflow.
+ * With an infinity or NaN in a row of x none of that row's outputs is finite.
  *
  *   M                    0 .. 256 (0 does nothing); more return SSM_ERR_UNSUPPORTED: they belong to a product with
  *                        the whole weight

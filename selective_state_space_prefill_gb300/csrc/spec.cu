@@ -56,6 +56,15 @@ __device__ T row_wide(T v, T* s_warp, T* s_cta, int ctas) {
     return v;
 }
 
+// The end of a cluster's exchanges, in two parts: all read; no CTA leaves while its values are read.  Outputs are
+// written between them, and nothing waits for those.
+__device__ __forceinline__ void all_read(int ctas) {
+    if (ctas > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void leave(int ctas) {
+    if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // Eight logits as they came.
 template <typename T> struct Raw;
 template <> struct Raw<__nv_bfloat16> {
@@ -152,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
             for (int k = 0; k < 8; ++k) l += ex2((v[i].at(k) - m) * f);
         inv = __fdiv_rn(1.f, row_wide<kSum, kWarps>(l, s_sum, &s_sum_cta, ctas));
     }
+    all_read(ctas);
     const int start = head + 8 * first;
     const bool whole = reinterpret_cast<uintptr_t>(p + start) % 16 == 0;
     auto write = [&](auto prob) {
@@ -172,7 +182,8 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
     };
     if (f > 0.f) write([&](float x, int) { return ex2((x - m) * f) * inv; });
     else write([&](float, int at) { return at == least ? 1.f : inv; });
-    if (ctas > 1) cg::this_cluster().sync();            // no CTA leaves while its values are read
+    __syncwarp();
+    leave(ctas);
 }
 
 // Rows longer than a cluster's registers hold: read three times, from L2 after the first.
@@ -192,6 +203,7 @@ __global__ void __launch_bounds__(512) k_spec_probs_long(const ProbsArgs a, int 
     for (int i = lo + threadIdx.x; i < hi; i += kThreads) m = max_nan(m, to_f32(x[i]));
     m = row_wide<kMax, kWarps>(m, s_max, &s_max_cta, ctas);
     if (!(m < INFINITY) || t != t) {
+        all_read(ctas);
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = quiet_nan();
     } else if (t <= 0x1p-100f || m == -INFINITY) {
         int least = 0x7fffffff;
@@ -199,6 +211,7 @@ __global__ void __launch_bounds__(512) k_spec_probs_long(const ProbsArgs a, int 
         for (int i = lo + threadIdx.x; i < hi; i += kThreads)
             if (to_f32(x[i]) == m && m > -INFINITY) least = min(least, i);
         least = row_wide<kLeast, kWarps>(least, s_at, &s_at_cta, ctas);
+        all_read(ctas);
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = i == least ? 1.f : 0.f;
     } else {
         const float f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
@@ -206,11 +219,13 @@ __global__ void __launch_bounds__(512) k_spec_probs_long(const ProbsArgs a, int 
 #pragma unroll 8
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) l += ex2((to_f32(x[i]) - m) * f);
         l = row_wide<kSum, kWarps>(l, s_sum, &s_sum_cta, ctas);
+        all_read(ctas);
         const float inv = __fdiv_rn(1.f, l);
 #pragma unroll 8
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = ex2((to_f32(x[i]) - m) * f) * inv;
     }
-    if (ctas > 1) cg::this_cluster().sync();
+    __syncwarp();
+    leave(ctas);
 }
 
 // ------------------------------------------------------------------ verification
@@ -382,13 +397,13 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
             mags = warp_sum(lane < ctas ? *cluster.map_shared_rank(&s_mags, lane) : 0.f);
             total = warp_sum(v);
             before += warp_sum(lane < rank ? v : 0);
-            asm volatile("barrier.cluster.arrive.release;" ::: "memory");       // read
+            all_read(ctas);
         } else {
             __syncthreads();
         }
         if (total > 0 || turn == 1 || (!w.q && w.off < 0)) break;
         w.q = nullptr, w.off = -1;                      // nothing left of p - q: p itself
-        if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        leave(ctas);
     }
     // the first index whose running sum exceeds floor(u * total)
     const uint64_t border = __umul64hi(__float2ull_rz(draw * 0x1p64f), total);
@@ -432,7 +447,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
         }
     }
     __syncwarp();
-    if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");   // all have read: free to leave
+    leave(ctas);
 }
 
 template <typename... P, typename... A>

@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a,
             if (lane == 0) mbar_arrive(&bars.part_empty[buf]);
             buf ^= 1, parity ^= buf == 0;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");            // also after a wait that expired
     }
 }
 

@@ -257,13 +257,14 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
         }
     } else if (warp == kUnpack + kScale) {
         // ---- copies of codes.  Here and below the whole warp walks the loop, so that what an instruction wants in
-        // uniform registers stays there, and one elected lane issues.
+        // uniform registers stays there, and one elected lane issues (nothing more after a wait that expired: by the
+        // end of the CTA what it issued before is long done).
         Ring cs;
         const int stages = (steps + kStageK / kStep - 1) / (kStageK / kStep);
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
             for (int i = 0; i < stages; ++i, cs.next()) {
                 wait(&c_empty[cs.at], cs.parity ^ 1);
-                if (elect_one()) {
+                if (elect_one() && !wait.dead) {
                     mbar_arrive_expect_tx(&c_full[cs.at], kStageC);
                     tma_load_2d(smem + cs.at * kStageC, &tm_codes, &c_full[cs.at], k0 / 2 + i * (kStageK / 2), tile * kRows);
                 }
@@ -277,7 +278,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
             for (int s = 0; s < steps; ++s, ++r) {
                 const uint32_t buf = r % kSteps;
                 wait(&used[buf], r / kSteps & 1 ^ 1);
-                if (elect_one()) {
+                if (elect_one() && !wait.dead) {
                     mbar_arrive_expect_tx(&full[buf], G::kStageX);
                     for (int h = 0; h < 2; ++h)
                         tma_load_2d(smem + G::kOffX + buf * G::kStageX + h * (G::kStageX / 2), &tm_x, &full[buf], k0 + s * kStep + 64 * h, m0);
@@ -301,7 +302,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                     if (kGroups > 1 && s * kGroups + h >= groups) break;
                     wait(&d_empty[q % kD], q / kD & 1 ^ 1);
                     tc_fence_after();
-                    if (elect_one()) {
+                    if (elect_one() && !wait.dead) {
 #pragma unroll
                         for (int k = h * kCount; k < (h + 1) * kCount; ++k)
                             mma_from_tmem(tm + G::kColD + MP * (q % kD), tm + (uint32_t)(kStep / 2) * buf + 8u * k,
@@ -312,7 +313,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                     ++q;
                 }
                 if (GK != kStep) {
-                    if (elect_one()) mma_commit(&used[buf]);
+                    if (elect_one() && !wait.dead) mma_commit(&used[buf]);
                     __syncwarp();
                 }
             }

@@ -188,6 +188,28 @@ def test_a_bad_scale_reaches_its_own_output_only():
     assert torch.equal(got[:, keep], clean[:, keep])
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 60, 1024), (8, 33, 640), (16, 70, 2048), (40, 24, 1024), (70, 901, 4096)])
+@pytest.mark.parametrize("group", [32, 128])
+def test_weights_that_are_mostly_zero(m, n, k, group):
+    """One element of a group and the rest at its zero: the result is that element's, the errors those of the sums of
+    x (16 + code) and x (16 + zero): at most 128 steps of 2 U and 4 U on sum 31 |x| scale, for each of the two."""
+    g = torch.Generator().manual_seed(m + n)
+    groups = k // group
+    z = torch.randint(0, 16, (n, groups), generator=g, dtype=U8)
+    c = z.repeat_interleave(group, 1)
+    at = torch.arange(groups) * group + torch.randint(0, group, (n, groups), generator=g)
+    c.scatter_(1, at, torch.randint(0, 16, (n, groups), generator=g, dtype=U8))
+    codes = (c[:, ::2] | c[:, 1::2] << 4).to(DEV)
+    zeros = torch.nn.functional.pad(z, (0, -groups % 16)).to(DEV)[:, :groups]
+    scales = torch.nn.functional.pad(0.02 * torch.randn(n, groups, generator=g), (0, -groups % 4)).to(DEV)[:, :groups]
+    x = torch.randn(m, k, generator=g).to(BF16).to(DEV)
+    got = ssm.w4_linear(x, codes, scales, zeros, out_dtype=F32)
+    w = ((c.double() - z.double().repeat_interleave(group, 1)) * scales.cpu().double().repeat_interleave(group, 1))
+    ref = x.cpu().double() @ w.T
+    mag = x.cpu().double().abs() @ (31 * scales.cpu().double().abs()).repeat_interleave(group, 1).T
+    assert ((got.cpu().double() - ref).abs() <= 2 * 260 * 2.0 ** -24 * mag).all()
+
+
 def test_zeros_count_by_their_low_half():
     g = torch.Generator().manual_seed(15)
     codes, scales, zeros = weight(g, 33, 256, 32, BF16, True)
