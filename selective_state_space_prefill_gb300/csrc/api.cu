@@ -4,7 +4,8 @@
 // status (with a message for ssm_last_error) before launching anything when they
 // are wrong, and otherwise enqueues its kernels on the caller's stream (one
 // kernel; three for a prefill cut into several sequence segments; two for the
-// SSD prefill and decode).
+// SSD prefill and decode; up to three for w4_linear: x put in order, products,
+// the sums of slices).
 // No entry point allocates memory or keeps per-call state.
 #include <stdarg.h>
 #include <stdio.h>
