@@ -204,7 +204,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
             const int shift = a.w.scale_bf16 ? 3 : 2, per = 1 << shift;     // scales in 16 bytes
             auto scales_at = [&](int block) { return block << shift < a.w.K / GK ? __ldg(scales + block) : make_uint4(0, 0, 0, 0); };
             uint4 next = scales_at(j0 >> shift);
-            float acc[kMine] = {};
+            float2 acc[kMine / 2] = {};                 // of two columns
             for (int block = j0 >> shift; block << shift < j0 + groups; ++block) {
                 const uint4 now = next;
                 next = scales_at(block + 1);
@@ -234,7 +234,8 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                                 if (m0 + c0 + c + i < a.M) d[i] *= __ldg(xs + (int64_t)(m0 + c0 + c + i) * a.x_blocks);
                         }
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[c + i] = fmaf(d[i], scale, acc[c + i]);
+                        for (int i = 0; i < 16; i += 2)
+                            acc[(c + i) / 2] = __ffma2_rn(make_float2(d[i], d[i + 1]), make_float2(scale, scale), acc[(c + i) / 2]);
                     }
                 }
             }
@@ -243,12 +244,12 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                 if (a.x_scale && a.x_blocks == 1) {
 #pragma unroll
                     for (int i = 0; i < kMine; ++i)
-                        if (i < rows) acc[i] *= __ldg(a.x_scale + m0 + c0 + i);
+                        if (i < rows) (i % 2 ? acc[i / 2].y : acc[i / 2].x) *= __ldg(a.x_scale + m0 + c0 + i);
                 }
                 auto put = [&](auto* to, int64_t stride) {
 #pragma unroll
                     for (int i = 0; i < kMine; ++i, to += stride)
-                        if (i < rows) *to = from_f32<std::remove_pointer_t<decltype(to)>>(acc[i]);
+                        if (i < rows) *to = from_f32<std::remove_pointer_t<decltype(to)>>(i % 2 ? acc[i / 2].y : acc[i / 2].x);
                 };
                 if (cut.slices > 1) put(a.parts + ((int64_t)slice * a.M + m0 + c0) * a.w.N + n, a.w.N);
                 else if (a.out_bf16) put(reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(m0 + c0) * a.ldo + n, a.ldo);
@@ -356,8 +357,9 @@ constexpr int kSms = 152;
 
 int rows_of(int M) { return M <= 32 ? 32 : 64; }
 
-// Slices of the rows where the tiles alone leave SMs idle: as for the kernel of few rows, by the CTA with most work
-// at an SM's share of the copy rate, and for the second kernel two microseconds and the slices' sums at 4 TB/s.
+// Slices of the rows where the tiles alone leave SMs idle, by the CTA with most work at 24 bytes of codes a nanosecond
+// (0.35 us a step), and for the second kernel two microseconds and the slices' sums at 4 TB/s.  64 x 4096 -> 8192: one
+// slice 19.4 us, two 16.
 Cut cut_of(int M, const W4Weight& w) {
     Cut best{};
     int64_t least = 0;
@@ -371,7 +373,7 @@ Cut cut_of(int M, const W4Weight& w) {
         int walkers = kSms / (c.m_blocks * c.slices);
         walkers = walkers < 1 ? 1 : walkers > c.tiles ? c.tiles : walkers;
         const int64_t bytes = (int64_t)((c.tiles + walkers - 1) / walkers) * c.slice_k * (kRows / 2);
-        const int64_t ns = bytes / 44 + (c.slices > 1 ? 2000 + (int64_t)c.slices * M * w.N * 8 / 4000 : 0);
+        const int64_t ns = bytes / 24 + (c.slices > 1 ? 2000 + (int64_t)c.slices * M * w.N * 8 / 4000 : 0);
         if (s == 1 || ns < least) best = c, least = ns;
     }
     return best;
