@@ -68,6 +68,32 @@ bool opt_in_dynamic_smem(ContextMemo& memo, K* kern, int bytes, const char** why
     return true;
 }
 
+// Launches a kernel that may start while the one before it in the stream still runs, so that its launch and first
+// instructions cost no time of their own.  Every thread of it that touches memory calls after_previous() first
+// (common.cuh); a kernel that was not launched so waits for all before it as ever.  `cluster` CTAs form a cluster.
+template <typename... P, typename... A>
+int launch_in_turn(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, const char** why,
+                   const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e == cudaSuccess) return 0;
+    *why = cudaGetErrorString(e);
+    return -1;
+}
+
 // Kernel-side arguments of the prefill (everything except the TMA maps).
 struct PrefillArgs {
     int seqlen, d_inner;

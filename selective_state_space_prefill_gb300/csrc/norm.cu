@@ -87,6 +87,8 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) k_norm_rms(const NormAr
     const unsigned row = unit / (unsigned)a.n_groups, group = unit - row * (unsigned)a.n_groups;
     if (W == 1 && row >= a.n_rows) return;
     const int c0 = group * n, first = 8 * tid;
+    after_previous();
+    next_may_start();
     Vec<Tx> x[V];
     Vec<Tr> r[V];
 #pragma unroll
@@ -144,53 +146,46 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) k_norm_rms(const NormAr
 }
 
 template <typename Tx, typename Tr, typename To, int W, int V>
-void go(const NormArgs& a, cudaStream_t stream) {
+int go(const NormArgs& a, cudaStream_t stream, const char** why) {
     const int64_t units = a.n_rows * a.n_groups;
-    k_norm_rms<Tx, Tr, To, W, V><<<(unsigned)(W == 1 ? (units + 3) / 4 : units), W == 1 ? 128 : 32 * W, 0, stream>>>(a);
+    return launch_in_turn(k_norm_rms<Tx, Tr, To, W, V>, dim3((unsigned)(W == 1 ? (units + 3) / 4 : units)), W == 1 ? 128 : 32 * W, 0, 1,
+                          stream, why, a);
 }
 
 template <typename Tx, typename Tr, typename To>
-void launch(const NormArgs& a, cudaStream_t stream) {
+int launch(const NormArgs& a, cudaStream_t stream, const char** why) {
     const int vecs = a.width / a.n_groups / 8;
     const bool few = a.n_rows * a.n_groups <= 2 * kSms;
-    if (vecs <= 32) return go<Tx, Tr, To, 1, 1>(a, stream);
-    if (vecs <= 128 && !few) return go<Tx, Tr, To, 1, 4>(a, stream);
+    if (vecs <= 32) return go<Tx, Tr, To, 1, 1>(a, stream, why);
+    if (vecs <= 128 && !few) return go<Tx, Tr, To, 1, 4>(a, stream, why);
     if (few) {                                          // a vector a thread, as far as 1024 threads go
-        if (vecs <= 64) return go<Tx, Tr, To, 2, 1>(a, stream);
-        if (vecs <= 128) return go<Tx, Tr, To, 4, 1>(a, stream);
-        if (vecs <= 256) return go<Tx, Tr, To, 8, 1>(a, stream);
-        if (vecs <= 512) return go<Tx, Tr, To, 16, 1>(a, stream);
-        if (vecs <= 1024) return go<Tx, Tr, To, 32, 1>(a, stream);
+        if (vecs <= 64) return go<Tx, Tr, To, 2, 1>(a, stream, why);
+        if (vecs <= 128) return go<Tx, Tr, To, 4, 1>(a, stream, why);
+        if (vecs <= 256) return go<Tx, Tr, To, 8, 1>(a, stream, why);
+        if (vecs <= 512) return go<Tx, Tr, To, 16, 1>(a, stream, why);
+        if (vecs <= 1024) return go<Tx, Tr, To, 32, 1>(a, stream, why);
     } else {
-        if (vecs <= 256) return go<Tx, Tr, To, 2, 4>(a, stream);
-        if (vecs <= 512) return go<Tx, Tr, To, 4, 4>(a, stream);
-        if (vecs <= 1024) return go<Tx, Tr, To, 8, 4>(a, stream);
+        if (vecs <= 256) return go<Tx, Tr, To, 2, 4>(a, stream, why);
+        if (vecs <= 512) return go<Tx, Tr, To, 4, 4>(a, stream, why);
+        if (vecs <= 1024) return go<Tx, Tr, To, 8, 4>(a, stream, why);
     }
-    if (vecs <= 2048) return go<Tx, Tr, To, 16, 4>(a, stream);
-    go<Tx, Tr, To, 32, 4>(a, stream);
+    if (vecs <= 2048) return go<Tx, Tr, To, 16, 4>(a, stream, why);
+    return go<Tx, Tr, To, 32, 4>(a, stream, why);
 }
 
 template <typename Tx, typename Tr>
-void launch_out(const NormArgs& a, cudaStream_t stream) {
-    if (a.out_type == SSM_I8) launch<Tx, Tr, int8_t>(a, stream);
-    else if (a.out_type == SSM_BF16) launch<Tx, Tr, __nv_bfloat16>(a, stream);
-    else launch<Tx, Tr, float>(a, stream);
+int launch_out(const NormArgs& a, cudaStream_t stream, const char** why) {
+    if (a.out_type == SSM_I8) return launch<Tx, Tr, int8_t>(a, stream, why);
+    if (a.out_type == SSM_BF16) return launch<Tx, Tr, __nv_bfloat16>(a, stream, why);
+    return launch<Tx, Tr, float>(a, stream, why);
 }
 
 }  // namespace
 
 int launch_norm_rms(const NormArgs& a, cudaStream_t stream, const char** why) {
-    if (a.in_type == SSM_BF16) {
-        if (a.res_type == SSM_BF16) launch_out<__nv_bfloat16, __nv_bfloat16>(a, stream);
-        else launch_out<__nv_bfloat16, float>(a, stream);
-    } else {
-        if (a.res_type == SSM_BF16) launch_out<float, __nv_bfloat16>(a, stream);
-        else launch_out<float, float>(a, stream);
-    }
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) return 0;
-    *why = cudaGetErrorString(e);
-    return -1;
+    if (a.in_type == SSM_BF16)
+        return a.res_type == SSM_BF16 ? launch_out<__nv_bfloat16, __nv_bfloat16>(a, stream, why) : launch_out<__nv_bfloat16, float>(a, stream, why);
+    return a.res_type == SSM_BF16 ? launch_out<float, __nv_bfloat16>(a, stream, why) : launch_out<float, float>(a, stream, why);
 }
 
 }  // namespace ssm

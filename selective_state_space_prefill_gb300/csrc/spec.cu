@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
     const int rank = blockIdx.x % (unsigned)ctas, vocab = (int)a.vocab;
     const T* x = reinterpret_cast<const T*>(a.logits) + row * a.ld_in;
     float* p = a.probs + row * a.ld_out;
+    after_previous();
     const float t = a.temperature ? a.temperature[row] : 1.f;
     int head = (int)((16 - reinterpret_cast<uintptr_t>(x) % 16) % 16 / sizeof(T));
     if (head > vocab) head = vocab;
@@ -161,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
             for (int k = 0; k < 8; ++k) l += ex2((v[i].at(k) - m) * f);
         inv = __fdiv_rn(1.f, row_wide<kSum, kWarps>(l, s_sum, &s_sum_cta, ctas));
     }
+    next_may_start();                                   // 64 x 32000 7.5 us, at the kernel's start 7.8
     all_read(ctas);
     const int start = head + 8 * first;
     const bool whole = reinterpret_cast<uintptr_t>(p + start) % 16 == 0;
@@ -196,6 +198,7 @@ __global__ void __launch_bounds__(512) k_spec_probs_long(const ProbsArgs a, int 
     const int rank = blockIdx.x % (unsigned)ctas, vocab = (int)a.vocab;
     const T* x = reinterpret_cast<const T*>(a.logits) + row * a.ld_in;
     float* p = a.probs + row * a.ld_out;
+    after_previous();
     const float t = a.temperature ? a.temperature[row] : 1.f;
     const int per = (vocab + ctas - 1) / ctas, lo = rank * per, hi = min(lo + per, vocab);
     float m = -INFINITY;
@@ -297,6 +300,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, vocab = (int)a.vocab;
     const int32_t* draft = a.draft + (int64_t)b * a.n_max;
     const float* u = a.u + (int64_t)b * (a.n_max + 1);
+    after_previous();
     const float draw = uniform(u[a.n_max]);             // asked for now, used at the end
     if (warp == 0) {
         const int d0 = lane < a.n_max ? draft[lane] : 0;                // as n_draft, not after it
@@ -405,6 +409,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
         w.q = nullptr, w.off = -1;                      // nothing left of p - q: p itself
         leave(ctas);
     }
+    next_may_start();
     // the first index whose running sum exceeds floor(u * total)
     const uint64_t border = __umul64hi(__float2ull_rz(draw * 0x1p64f), total);
     if (total == 0 || !(mags < 3.99f)) {                // no distribution
@@ -450,25 +455,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
     leave(ctas);
 }
 
-template <typename... P, typename... A>
-int launch(void (*kern)(P...), int threads, int64_t rows, int ctas, cudaStream_t stream, const char** why, const A&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)(rows * ctas));
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.stream = stream;
-    if (ctas > 1) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)ctas;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args..., ctas);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e == cudaSuccess) return 0;
-    *why = cudaGetErrorString(e);
-    return -1;
+// A cluster of `ctas` for each row.
+template <typename... P, typename A>
+int launch(void (*kern)(P...), int threads, int64_t rows, int ctas, cudaStream_t stream, const char** why, const A& a) {
+    return launch_in_turn(kern, dim3((unsigned)(rows * ctas)), threads, 0, ctas, stream, why, a, ctas);
 }
 
 // A row's CTAs: the fewest powers of two that hold it with kMost vectors a thread (up to eight CTAs), more while each

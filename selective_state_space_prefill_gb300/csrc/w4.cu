@@ -203,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a,
     }
     fence_barrier_init();
     __syncthreads();
+    after_previous();
+    next_may_start();
 
     if (warp < kWarps) {
         // ---- the products
@@ -404,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a,
 
 // The slices' sums of an output, in their order.
 __global__ void __launch_bounds__(256) k_w4_join(const W4LinearArgs a, int slices) {
-    cudaGridDependencySynchronize();                    // launched while the products still run
+    after_previous();
+    next_may_start();
     const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (n >= a.w.N) return;
     const int m = blockIdx.y;
@@ -462,11 +465,9 @@ int linear(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, con
     auto kern = k_w4_linear<NT, PG>;
     static ContextMemo attr_memo;
     if (!opt_in_dynamic_smem(attr_memo, kern, kMaxSmem, why)) return -1;
-    kern<<<dim3((unsigned)p.walkers, (unsigned)p.m_blocks, (unsigned)p.slices), kThreads, p.smem, stream>>>(a, p, status);
-    const cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) return p.slices > 1 ? launch_w4_join(a, p.slices, stream, why) : 0;
-    *why = cudaGetErrorString(e);
-    return -1;
+    if (launch_in_turn(kern, dim3((unsigned)p.walkers, (unsigned)p.m_blocks, (unsigned)p.slices), kThreads, p.smem, 1, stream, why, a, p, status))
+        return -1;
+    return p.slices > 1 ? launch_w4_join(a, p.slices, stream, why) : 0;
 }
 
 template <int NT>
@@ -504,20 +505,7 @@ int launch_w4_quantize(const W4Weight& w, const void* W, int64_t ldw, bool in_bf
 }
 
 int launch_w4_join(const W4LinearArgs& a, int slices, cudaStream_t stream, const char** why) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)((a.w.N + 255) / 256), (unsigned)a.M);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k_w4_join, a, slices);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e == cudaSuccess) return 0;
-    *why = cudaGetErrorString(e);
-    return -1;
+    return launch_in_turn(k_w4_join, dim3((unsigned)((a.w.N + 255) / 256), (unsigned)a.M), 256, 0, 1, stream, why, a, slices);
 }
 
 // Whether a call goes to the tiles of w4_tiles.cu: from nine rows of x on where the weight is large.  They unpack it

@@ -129,6 +129,8 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    after_previous();                                   // x in its order comes from the kernel before
+    next_may_start();
 
     if (warp < kUnpack) {
         // ---- codes to operands: a row of the weight each; the sets of four warps take the steps in turn
@@ -273,7 +275,6 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
             }
     } else if (warp == kUnpack + kScale + 1) {
         // ---- copies of x
-        asm volatile("griddepcontrol.wait;" ::: "memory");          // x in its order comes from the kernel before
         uint32_t r = 0;
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
             for (int s = 0; s < steps; ++s, ++r) {
@@ -331,6 +332,8 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
 
 // x as bf16, every eight elements in the order 0 4 1 5 2 6 3 7 in which a word's codes come out; rows from M on are 0.
 __global__ void __launch_bounds__(256) k_w4_order(const W4LinearArgs a, uint4* to, int64_t vecs) {
+    after_previous();
+    next_may_start();
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= vecs) return;
     const int per_row = a.w.K / 8, m = (int)(i / per_row), k = (int)(i % per_row) * 8;
@@ -340,7 +343,6 @@ __global__ void __launch_bounds__(256) k_w4_order(const W4LinearArgs a, uint4* t
         else x_pairs(*reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.x) + m * a.ldx + k), r);
     }
     to[i] = make_uint4(r[0], r[1], r[2], r[3]);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 bool encode(CUtensorMap* m, CUtensorMapDataType type, int size, const void* base, uint64_t inner, uint64_t rows, uint64_t stride,
@@ -398,28 +400,12 @@ int launch(const W4LinearArgs& a, unsigned int* status, cudaStream_t stream, con
     static ContextMemo attr_memo;
     if (!opt_in_dynamic_smem(attr_memo, kern, G::kSmem, why)) return -1;
     const int64_t vecs = padded(a.M) * a.w.K / 8;
-    k_w4_order<<<(unsigned)((vecs + 255) / 256), 256, 0, stream>>>(a, x, vecs);
-    cudaError_t e = cudaGetLastError();
+    if (launch_in_turn(k_w4_order, dim3((unsigned)((vecs + 255) / 256)), 256, 0, 1, stream, why, a, x, vecs)) return -1;
     int walkers = kSms / (cut.m_blocks * cut.slices);
     walkers = walkers < 1 ? 1 : walkers > cut.tiles ? cut.tiles : walkers;
-    if (e == cudaSuccess) {
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        cfg.gridDim = dim3((unsigned)walkers, (unsigned)cut.m_blocks, (unsigned)cut.slices);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = G::kSmem;
-        cfg.stream = stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        e = cudaLaunchKernelEx(&cfg, kern, mc, mx, b, cut, status);
-        if (e == cudaSuccess) e = cudaGetLastError();
-    }
-    if (e != cudaSuccess) {
-        *why = cudaGetErrorString(e);
+    if (launch_in_turn(kern, dim3((unsigned)walkers, (unsigned)cut.m_blocks, (unsigned)cut.slices), kThreads, G::kSmem, 1, stream, why, mc, mx,
+                       b, cut, status))
         return -1;
-    }
     return cut.slices > 1 ? launch_w4_join(b, cut.slices, stream, why) : 0;
 }
 

@@ -125,6 +125,65 @@ def test_captured_calls_replay_on_new_inputs(call):
             assert torch.equal(o, w)
 
 
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("rows,inner", [(3, 512), (20, 512), (200, 1024)])
+def test_each_call_reads_what_the_one_before_wrote(rows, inner, graph):
+    """Kernels start before the one before them ends.  Steps in which every call reads what the one before it wrote, and
+    writes over what others read, weights among it, with torch's kernels between them, give the bits that they
+    give one at a time."""
+    vocab, steps = 2600, 12
+    g = torch.Generator().manual_seed(rows)
+    x0 = torch.randn(rows, inner, generator=g).to(torch.bfloat16).to(DEV)
+    W0 = (torch.randn(vocab, inner, generator=g) / inner ** 0.5).to(DEV)
+    u = torch.rand(1, rows, generator=g).to(DEV)
+    fixed = dict(x=x0.clone(), W=W0.clone(), y=torch.empty_like(x0, dtype=torch.int8), s=torch.empty(rows, 1, device=DEV),
+                 l=torch.empty(rows, vocab, device=DEV), p=torch.empty(1, rows, vocab, device=DEV))
+    work = torch.empty(max(1, ssm.w4_linear_workspace_bytes(rows, vocab, inner, 64)), dtype=torch.uint8, device=DEV)
+
+    def step(wait):
+        f, seen = fixed, []
+        w = ssm.w4_quantize(f["W"], 64, True)
+        wait()
+        ssm.norm_rms(f["x"], out=f["y"], out_scale=f["s"], out_dtype=torch.int8)
+        wait()
+        ssm.w4_linear(f["y"], *w, x_scale=f["s"], out=f["l"], workspace=work)
+        wait()
+        ssm.spec_probs(f["l"], out=f["p"][0])
+        wait()
+        best = f["l"][:rows - 1].argmax(-1).to(torch.int32)[None].contiguous()
+        seen += [t.clone() for t in ssm.spec_verify(best, f["p"], u)]
+        wait()
+        f["W"].mul_(1.0 + f["p"][0, 0, :1])
+        nxt = ssm.w4_linear(f["x"], *ssm.w4_quantize(f["W"][:inner], 32), workspace=None)
+        wait()
+        ssm.norm_rms(nxt, residual=f["x"], out=f["x"], residual_out=False)      # over its own residual
+        wait()
+        return seen + [f["l"].clone(), f["x"].clone()]
+
+    def run(wait):
+        fixed["x"].copy_(x0), fixed["W"].copy_(W0)
+        return [t for _ in range(steps) for t in step(wait)]
+
+    want = [t.cpu() for t in run(torch.cuda.synchronize)]
+    assert all(torch.isfinite(t.float()).all() for t in want)
+    if not graph:
+        for _ in range(3):
+            got = run(lambda: None)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want))
+        return
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    captured = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(captured, stream=side):
+        got = run(lambda: None)
+    for _ in range(3):
+        captured.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.cpu(), b) for a, b in zip(got, want))
+    assert ssm.device_status() == 0
+
+
 def test_two_streams_at_once():
     """Calls that overlap share nothing: each gives what it gives alone."""
     s = [Setup(i, m=8, k=4096, n=5000) for i in range(2)]
