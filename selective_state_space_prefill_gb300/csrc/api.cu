@@ -1234,9 +1234,9 @@ int spec_probs(int64_t n_rows, int64_t vocab, ssm_dtype_t in_dtype, const void* 
     if (!aligned(logits, esize(in_dtype)) || !aligned(probs, 4) || (temperature && !aligned(temperature, 4)))
         return fail(SSM_ERR_MISALIGNED, "%s: a tensor is not element aligned", fn);
     int serr = 0;
-    status_ptr(&serr);
+    unsigned int* status = status_ptr(&serr);
     if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
-    const ssm::ProbsArgs a{n_rows, vocab, logits, ld_in, ld_out, temperature, probs};
+    const ssm::ProbsArgs a{n_rows, vocab, logits, ld_in, ld_out, temperature, probs, status};
     const char* why = "";
     if (ssm::launch_spec_probs(a, in_dtype == SSM_BF16, static_cast<cudaStream_t>(cuda_stream), &why) != 0)
         return fail(SSM_ERR_CUDA, "%s: %s", fn, why);

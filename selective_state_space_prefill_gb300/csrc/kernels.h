@@ -330,6 +330,7 @@ struct ProbsArgs {
     int64_t ld_in, ld_out;
     const float* temperature;
     float* probs;
+    unsigned int* status;
 };
 
 struct VerifyArgs {

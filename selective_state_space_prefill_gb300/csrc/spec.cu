@@ -6,6 +6,8 @@
 // memory.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "ssm.h"
@@ -30,7 +32,66 @@ __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7fc00000
 // branch, came out as one 16-byte store, which faults where the row is not aligned.
 __device__ __forceinline__ void store1(float* p, float v) { asm volatile("st.global.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory"); }
 
-// What a row's CTAs find out together: every CTA's value in its shared memory, combined by every thread.
+// What the warps of a row's CTAs tell each other, at most twice: each writes its words into the shared memory of every
+// CTA of the cluster, in 64 bits of which the upper half is the word and the lower half says that it is there, and
+// reads the others' from its own.  A word and its mark come as one, so nothing has to be ordered, and nobody waits
+// for anything but the words.  (A barrier of the cluster, and reads from the others behind it, waits for all that the
+// SM has under way, two microseconds where four CTAs of it write: 512 x 131072 95 us so, 86 with words; 64 x 32000 7.5
+// and 5.0.  Words of every warp instead of every CTA, polled by all: 107, 6.7.)  The two exchanges
+// have slots of their own, and a CTA that has all words of the last one is written to by nobody: it may leave.
+constexpr int kMostCtas = 8;
+template <int kWords, int kWarps> struct Exchange {
+    struct Box {                                        // in shared memory
+        uint64_t slot[2][kWords][kMostCtas * kWarps];
+    };
+    Box& box;
+    int ctas, rank;
+    unsigned int* status;
+    int turn = 0;
+    bool dead = false;
+
+    // By all threads; ready() before the first words are sent.
+    __device__ __forceinline__ Exchange(Box& box, int ctas, int rank, unsigned int* status) : box(box), ctas(ctas), rank(rank), status(status) {
+        for (int i = threadIdx.x; i < 2 * kWords * kMostCtas * kWarps; i += blockDim.x) (&box.slot[0][0][0])[i] = 0;
+        if (ctas > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    }
+    __device__ __forceinline__ void ready() {
+        if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        else __syncthreads();
+    }
+    // A warp's words (the CTA's where kWarps is 1), the same in all lanes.
+    __device__ __forceinline__ void send(const uint32_t (&words)[kWords]) {
+        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+        if (lane < ctas && warp < kWarps) {
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                uint64_t* to = &box.slot[turn][w][rank * kWarps + warp];
+                if (ctas > 1) to = cg::this_cluster().map_shared_rank(to, lane);
+                *reinterpret_cast<volatile uint64_t*>(to) = (uint64_t)words[w] << 32 | 1u;
+            }
+        }
+        ++turn;
+    }
+    // A word of the last exchange by warp and CTA; gives up after two seconds, like all waits here.
+    __device__ __forceinline__ uint32_t word(int w, int from) {
+        const volatile uint64_t* at = &box.slot[turn - 1][w][from];
+        uint64_t v = *at, t0 = 0;
+        for (uint32_t spin = 0; v == 0 && !dead; ++spin) {
+            if ((spin & 4095u) == 4095u) {
+                const uint64_t now = globaltimer_ns();
+                if (t0 == 0) t0 = now;
+                if (now - t0 > 2000000000ull) {
+                    dead = true;
+                    atomicOr(status, (unsigned)SSM_DEV_WAIT_TIMEOUT);
+                }
+            }
+            v = *at;
+        }
+        return (uint32_t)(v >> 32);
+    }
+};
+
+// A value of all threads of a row.
 enum Kind { kMax, kSum, kLeast };
 template <Kind K, typename T>
 __device__ __forceinline__ T two(T a, T b) {
@@ -38,8 +99,16 @@ __device__ __forceinline__ T two(T a, T b) {
     else if constexpr (K == kSum) return a + b;
     else return a < b ? a : b;
 }
+template <typename T> __device__ __forceinline__ uint32_t bits_of(T v) {
+    if constexpr (std::is_same_v<T, float>) return __float_as_uint(v);
+    else return (uint32_t)v;
+}
+template <typename T> __device__ __forceinline__ T from_bits(uint32_t v) {
+    if constexpr (std::is_same_v<T, float>) return __uint_as_float(v);
+    else return (T)v;
+}
 template <Kind K, int kWarps, typename T>
-__device__ T row_wide(T v, T* s_warp, T* s_cta, int ctas) {
+__device__ __forceinline__ T row_wide(Exchange<1, 1>& all, T* s_warp, T v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = two<K>(v, __shfl_xor_sync(~0u, v, o));
     if (threadIdx.x % 32 == 0) s_warp[threadIdx.x / 32] = v;
@@ -47,22 +116,12 @@ __device__ T row_wide(T v, T* s_warp, T* s_cta, int ctas) {
     v = s_warp[threadIdx.x % kWarps];
 #pragma unroll
     for (int o = kWarps / 2; o > 0; o >>= 1) v = two<K>(v, __shfl_xor_sync(~0u, v, o));
-    if (ctas == 1) return v;
-    auto cluster = cg::this_cluster();
-    if (threadIdx.x == 0) *s_cta = v;
-    cluster.sync();
-    v = *cluster.map_shared_rank(s_cta, threadIdx.x % ctas);
-    for (int o = ctas / 2; o > 0; o >>= 1) v = two<K>(v, __shfl_xor_sync(~0u, v, o));
+    if (all.ctas == 1) return v;
+    all.send({bits_of(v)});
+    v = from_bits<T>(all.word(0, threadIdx.x % all.ctas));
+    __syncwarp();
+    for (int o = all.ctas / 2; o > 0; o >>= 1) v = two<K>(v, __shfl_xor_sync(~0u, v, o));
     return v;
-}
-
-// The end of a cluster's exchanges, in two parts: all read; no CTA leaves while its values are read.  Outputs are
-// written between them, and nothing waits for those.
-__device__ __forceinline__ void all_read(int ctas) {
-    if (ctas > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-}
-__device__ __forceinline__ void leave(int ctas) {
-    if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Eight logits as they came.
@@ -113,10 +172,12 @@ template <> struct Raw<float> {
 template <typename T, int V, int kThreads>
 __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThreads : 1) k_spec_probs(const ProbsArgs a, int ctas) {
     constexpr int kWarps = kThreads / 32;
-    __shared__ float s_max[kWarps], s_sum[kWarps], s_max_cta, s_sum_cta;
-    __shared__ int s_at[kWarps], s_at_cta;
+    __shared__ Exchange<1, 1>::Box box;
+    __shared__ float s_max[kWarps], s_sum[kWarps];
+    __shared__ int s_at[kWarps];
     const int64_t row = blockIdx.x / (unsigned)ctas;
     const int rank = blockIdx.x % (unsigned)ctas, vocab = (int)a.vocab;
+    Exchange<1, 1> all(box, ctas, rank, a.status);
     const T* x = reinterpret_cast<const T*>(a.logits) + row * a.ld_in;
     float* p = a.probs + row * a.ld_out;
     after_previous();
@@ -138,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
     float m = w;
 #pragma unroll
     for (int i = 0; i < V; ++i) m = max_nan(m, v[i].most());
-    m = row_wide<kMax, kWarps>(m, s_max, &s_max_cta, ctas);
+    all.ready();
+    m = row_wide<kMax, kWarps>(all, s_max, m);
 
     // p = 2^((x - m) f) inv, or 1 at one place, or the same everywhere
     float f = 0.f, inv = quiet_nan();
@@ -155,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
                 for (int k = 0; k < 8; ++k)
                     if (v[i].at(k) == m) least = min(least, head + 8 * (first + (int)threadIdx.x + i * kThreads) + k);
         }
-        least = row_wide<kLeast, kWarps>(least, s_at, &s_at_cta, ctas);
+        least = row_wide<kLeast, kWarps>(all, s_at, least);
     } else {
         f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
         float l = ex2((w - m) * f);
@@ -163,10 +225,9 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
         for (int i = 0; i < V; ++i)
 #pragma unroll
             for (int k = 0; k < 8; ++k) l += ex2((v[i].at(k) - m) * f);
-        inv = __fdiv_rn(1.f, row_wide<kSum, kWarps>(l, s_sum, &s_sum_cta, ctas));
+        inv = __fdiv_rn(1.f, row_wide<kSum, kWarps>(all, s_sum, l));
     }
     next_may_start();                                   // 64 x 32000 7.5 us, at the kernel's start 7.8
-    all_read(ctas);
     const int start = head + 8 * first;
     const bool whole = reinterpret_cast<uintptr_t>(p + start) % 16 == 0;
     auto write = [&](auto prob) {
@@ -187,18 +248,18 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
     };
     if (f > 0.f) write([&](float x, int) { return ex2((x - m) * f) * inv; });
     else write([&](float, int at) { return at == least ? 1.f : inv; });
-    __syncwarp();
-    leave(ctas);
 }
 
 // Rows longer than a cluster's registers hold: read three times, from L2 after the first.
 template <typename T>
 __global__ void __launch_bounds__(512) k_spec_probs_long(const ProbsArgs a, int ctas) {
     constexpr int kThreads = 512, kWarps = kThreads / 32;
-    __shared__ float s_max[kWarps], s_sum[kWarps], s_max_cta, s_sum_cta;
-    __shared__ int s_at[kWarps], s_at_cta;
+    __shared__ Exchange<1, 1>::Box box;
+    __shared__ float s_max[kWarps], s_sum[kWarps];
+    __shared__ int s_at[kWarps];
     const int64_t row = blockIdx.x / (unsigned)ctas;
     const int rank = blockIdx.x % (unsigned)ctas, vocab = (int)a.vocab;
+    Exchange<1, 1> all(box, ctas, rank, a.status);
     const T* x = reinterpret_cast<const T*>(a.logits) + row * a.ld_in;
     float* p = a.probs + row * a.ld_out;
     after_previous();
@@ -207,31 +268,27 @@ __global__ void __launch_bounds__(512) k_spec_probs_long(const ProbsArgs a, int 
     float m = -INFINITY;
 #pragma unroll 8
     for (int i = lo + threadIdx.x; i < hi; i += kThreads) m = max_nan(m, to_f32(x[i]));
-    m = row_wide<kMax, kWarps>(m, s_max, &s_max_cta, ctas);
+    all.ready();
+    m = row_wide<kMax, kWarps>(all, s_max, m);
     if (!(m < INFINITY) || t != t) {
-        all_read(ctas);
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = quiet_nan();
     } else if (t <= 0x1p-100f || m == -INFINITY) {
         int least = 0x7fffffff;
 #pragma unroll 8
         for (int i = lo + threadIdx.x; i < hi; i += kThreads)
             if (to_f32(x[i]) == m && m > -INFINITY) least = min(least, i);
-        least = row_wide<kLeast, kWarps>(least, s_at, &s_at_cta, ctas);
-        all_read(ctas);
+        least = row_wide<kLeast, kWarps>(all, s_at, least);
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = i == least ? 1.f : 0.f;
     } else {
         const float f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
         float l = 0.f;
 #pragma unroll 8
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) l += ex2((to_f32(x[i]) - m) * f);
-        l = row_wide<kSum, kWarps>(l, s_sum, &s_sum_cta, ctas);
-        all_read(ctas);
+        l = row_wide<kSum, kWarps>(all, s_sum, l);
         const float inv = __fdiv_rn(1.f, l);
 #pragma unroll 8
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = ex2((to_f32(x[i]) - m) * f) * inv;
     }
-    __syncwarp();
-    leave(ctas);
 }
 
 // ------------------------------------------------------------------ verification
@@ -297,10 +354,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
     constexpr int kNotes = 8;                           // of a lane's sum on the way
     __shared__ int s_kept, s_n;
     __shared__ uint64_t s_note[kWarps][kNotes][32];
-    __shared__ uint64_t s_sum[kWarps], s_total;
-    __shared__ float s_mag[kWarps], s_mags;
+    __shared__ Exchange<3, kWarps>::Box box;
     const int b = blockIdx.x / (unsigned)ctas, rank = blockIdx.x % (unsigned)ctas;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, vocab = (int)a.vocab;
+    Exchange<3, kWarps> all(box, ctas, rank, a.status);
     const int32_t* draft = a.draft + (int64_t)b * a.n_max;
     const float* u = a.u + (int64_t)b * (a.n_max + 1);
     after_previous();
@@ -333,6 +390,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
         }
     }
     __syncthreads();
+    all.ready();
     const int kept = s_kept, n = s_n;
     int32_t* out = a.tokens + (int64_t)b * (a.n_max + 1);
     if (rank == 0) {
@@ -367,7 +425,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
         }
     };
     float pv[kEach], qv[kEach];
-    uint64_t total, before;
+    uint64_t total, before, mine;                       // the row's, what is before this warp's stretch, the stretch's
     float mags;
     int notes;
     for (int turn = 0;; ++turn) {
@@ -389,35 +447,24 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
         }
         sum = warp_sum(sum);
         mag = warp_sum(mag);
-        if (lane == 0) s_sum[warp] = sum, s_mag[warp] = mag;
-        __syncthreads();
-        total = before = 0, mags = 0.f;
-        for (int i = 0; i < kWarps; ++i) {
-            before += i < warp ? s_sum[i] : 0;
-            total += s_sum[i], mags += s_mag[i];
+        all.send({(uint32_t)sum, (uint32_t)(sum >> 32), __float_as_uint(mag)});
+        total = before = 0, mags = 0.f, mine = sum;
+        for (int i = lane; i < ctas * kWarps; i += 32) {
+            const uint64_t part = all.word(0, i) | (uint64_t)all.word(1, i) << 32;
+            total += part, mags += __uint_as_float(all.word(2, i));
+            before += i < rank * kWarps + warp ? part : 0;
         }
-        if (ctas > 1) {
-            auto cluster = cg::this_cluster();
-            if (threadIdx.x == 0) s_total = total, s_mags = mags;
-            cluster.sync();
-            const uint64_t v = lane < ctas ? *cluster.map_shared_rank(&s_total, lane) : 0;
-            mags = warp_sum(lane < ctas ? *cluster.map_shared_rank(&s_mags, lane) : 0.f);
-            total = warp_sum(v);
-            before += warp_sum(lane < rank ? v : 0);
-            all_read(ctas);
-        } else {
-            __syncthreads();
-        }
+        __syncwarp();
+        total = warp_sum(total), before = warp_sum(before), mags = warp_sum(mags);
         if (total > 0 || turn == 1 || (!w.q && w.off < 0)) break;
         w.q = nullptr, w.off = -1;                      // nothing left of p - q: p itself
-        leave(ctas);
     }
     next_may_start();
     // the first index whose running sum exceeds floor(u * total)
     const uint64_t border = __umul64hi(__float2ull_rz(draw * 0x1p64f), total);
     if (total == 0 || !(mags < 3.99f)) {                // no distribution
         if (rank == 0 && threadIdx.x == 0) out[kept] = -1;
-    } else if (before <= border && border < before + s_sum[warp]) {
+    } else if (before <= border && border < before + mine) {
         // the notes say between which two of them; that is read again (from L2)
         uint64_t at = 0;
         if (lane < notes) {
@@ -428,10 +475,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
         if (note > 0) before += __shfl_sync(~0u, at, note - 1);
         for (int i0 = lo + note * step; i0 < hi; i0 += kBlock) {
             load(i0, 1, pv, qv);
-            uint64_t m[kEach], mine = 0;
+            uint64_t m[kEach], own = 0;
 #pragma unroll
-            for (int k = 0; k < kEach; ++k) m[k] = less(pv[k], qv[k]), mine += m[k];
-            uint64_t to = mine;                         // of the lanes up to this one
+            for (int k = 0; k < kEach; ++k) m[k] = less(pv[k], qv[k]), own += m[k];
+            uint64_t to = own;                          // of the lanes up to this one
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint64_t t = __shfl_up_sync(~0u, to, o);
@@ -440,7 +487,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
             const unsigned over = __ballot_sync(~0u, before + to > border);
             if (over) {
                 if (lane == __ffs(over) - 1) {
-                    before += to - mine;
+                    before += to - own;
                     int k = 0;
 #pragma unroll
                     for (int j = 0; j + 1 < kEach; ++j) {
@@ -454,8 +501,6 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
             before += __shfl_sync(~0u, to, 31);
         }
     }
-    __syncwarp();
-    leave(ctas);
 }
 
 // A cluster of `ctas` for each row.
