@@ -166,9 +166,9 @@ template <> struct Raw<float> {
 // powers are taken twice: their unit would do three times as many in the time that the row's bytes take.)  V
 // vectors of eight logits a thread, from the row's first 16-byte border on; what lies before that and behind the
 // last whole vector (up to 14 logits) is one logit each for the first CTA's first threads.  512 x 131072 bf16 (403 MB)
-// 93 us, 4.3 TB/s, 0.64 of the copy rate: a CTA loads, waits for the row's maximum, takes powers, waits for the sum,
-// writes, and four of them an SM do not keep memory busy all the time (two of 512 threads 107 us).  5 x 50021 3.8 us
-// in a graph.
+// 84 us, 4.8 TB/s, 0.71 of the copy rate: a CTA loads, waits for the row's maximum, takes powers, waits for the sum,
+// writes, and four of them an SM do not keep memory busy all the time (2000 x 32000, shorter rows, 5.2 TB/s).  The
+// next rows asked for from L2 ahead of time make 2 to 4 % and are left out.  5 x 50021 3.3 us in a graph.
 template <typename T, int V, int kThreads>
 __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThreads : 1) k_spec_probs(const ProbsArgs a, int ctas) {
     constexpr int kWarps = kThreads / 32;
@@ -345,8 +345,8 @@ template <typename T> __device__ __forceinline__ T warp_sum(T v) {
 // warp sums a stretch of the row, its lanes note their sums up to eight times on the way, and the warp in whose
 // stretch the border falls reads again (from L2) what lies between two notes.  Without notes it read its stretch
 // from the start, block by block.  Of the 19 us of 64 requests x 131072 (67 MB, 9.9 us at the copy rate) the checks of the
-// drafted tokens take 2 (three reads, each waiting for the one before), the sums 9, the cluster's exchange and
-// its slowest CTA 3, the search 2, starting and ending the rest.  One request: 6.6 us, the same chain of waits.
+// drafted tokens take 2 (three reads, each waiting for the one before), the sums 9, the slowest of a cluster's CTAs 2
+// to 3, the search 2, starting and ending the rest.  One request: 5.8 us, the same chain of waits.
 constexpr int kVerifyThreads = 256;
 __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyArgs a, int ctas) {
     constexpr int kThreads = kVerifyThreads, kWarps = kThreads / 32;

@@ -8,7 +8,7 @@
 // accumulator of their own (four of them in turn), which other threads, a row each, multiply by the group's
 // scale and add up in fp32 registers.  Eight warps unpack (56 integer operations and 32 subtractions for 64 codes of
 // 32 rows), eight scale, one each issues copies of codes, copies of x and products.  Measured: 64 x 2560 -> 50021, groups
-// of 128 with zeros (67 MB, 16 GFLOP) 36 us on a stream, 0.35 us a step of 128 x 128 codes, at 0.55 instructions a
+// of 128 with zeros (67 MB, 16 GFLOP) 36 us on a stream, 0.35 us a step of 128 x 128 codes, at 0.54 instructions a
 // cycle and scheduler; bytes are 10 us of it, products 9, and a seventh is that 391 tiles are no multiple of 152
 // SMs.  With twelve unpacking warps 39, with sixteen (spilling) 135; steps of 64 elements 53.
 #include <type_traits>
