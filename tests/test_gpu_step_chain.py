@@ -184,6 +184,57 @@ def test_each_call_reads_what_the_one_before_wrote(rows, inner, graph):
     assert ssm.device_status() == 0
 
 
+@pytest.mark.parametrize("capture", [False, True])
+def test_branches_that_meet(capture):
+    """A step forked over two streams and joined: calls behind an event, behind two kernels, a copy and a fill."""
+    g = torch.Generator().manual_seed(21)
+    m, k, n = 40, 512, 3000
+    x = torch.randn(m, k, generator=g).to(torch.bfloat16).to(DEV)
+    pinned = torch.empty(m, k, dtype=torch.bfloat16, device=DEV)
+    w = [ssm.w4_quantize((torch.randn(n, k, generator=g) / 20).to(DEV), 64, z) for z in (True, False)]
+    other = torch.cuda.Stream()
+
+    def run(x):
+        main = torch.cuda.current_stream()
+        pinned.copy_(x)                                             # a copy, then a call
+        h = ssm.norm_rms(pinned)[0]
+        other.wait_stream(main)
+        with torch.cuda.stream(other):                              # behind an event
+            b = ssm.w4_linear(h[:6], *w[1], out_dtype=torch.float32)
+            p2 = ssm.spec_probs(b)
+        a = ssm.w4_linear(h, *w[0], out_dtype=torch.float32)
+        p1 = ssm.spec_probs(a)
+        main.wait_stream(other)
+        both = ssm.norm_rms(a[:6, :2992], residual=b[:, :2992])[0]  # behind two kernels
+        zero = torch.full((6, 2992), 9.0, device=DEV)
+        zero.zero_()                                                # a fill, then a call
+        z = ssm.norm_rms(zero, residual=both, out_dtype=torch.float32)[0]
+        other.wait_stream(main)
+        return h, a, b, p1, p2, both, z
+
+    want = [t.clone() for t in run(x)]
+    torch.cuda.synchronize()
+    check_linear(want[1], want[0], *w[0], None)
+    check_linear(want[2], want[0][:6], *w[1], None)
+    check_norm(want[5], None, want[1][:6, :2992], None, want[2][:, :2992], 1e-5, 1)
+    check_probs(want[4], want[2], None)
+    if capture:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = run(x)
+        for _ in range(3):
+            for o in outs:
+                o.zero_()
+            graph.replay()
+    else:
+        for _ in range(20):
+            outs = run(x)
+    torch.cuda.synchronize()
+    for a, b in zip(outs, want):
+        assert torch.equal(a, b)
+    assert ssm.device_status() == 0
+
+
 def test_two_streams_at_once():
     """Calls that overlap share nothing: each gives what it gives alone."""
     s = [Setup(i, m=8, k=4096, n=5000) for i in range(2)]
