@@ -97,6 +97,8 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // Of a kernel that is launched while the one before it in the stream still runs (launch_in_turn): before its threads
 // read or write memory they wait until that one is done.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Tensor copies go another way to memory than the stores of the kernel before: by the thread that issues them.
+__device__ __forceinline__ void before_copies() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 // Once all its CTAs have come here, such a kernel behind this one may start.
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

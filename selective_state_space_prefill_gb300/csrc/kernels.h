@@ -70,7 +70,11 @@ bool opt_in_dynamic_smem(ContextMemo& memo, K* kern, int bytes, const char** why
 
 // Launches a kernel that may start while the one before it in the stream still runs, so that its launch and first
 // instructions cost no time of their own.  Every thread of it that touches memory calls after_previous() first
-// (common.cuh); a kernel that was not launched so waits for all before it as ever.  `cluster` CTAs form a cluster.
+// (common.cuh), and no load of it is non-coherent (__ldg, ld.global.nc, a __restrict__ pointer to const): such a load wants
+// memory that nobody writes while the kernel runs, and here the kernel before may be writing it, weights included, when
+// this one starts.  What after_previous() waited for is there for ordinary loads; a thread that issues tensor copies of it
+// calls before_copies() in between.  A kernel that was not launched so waits for all before it as ever.  `cluster` CTAs
+// form a cluster.
 // Seven calls of a decode step on a stream 61.5 us launched behind one another, 49 so; in a graph 47 either way.
 template <typename... P, typename... A>
 int launch_in_turn(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, const char** why,

@@ -128,7 +128,7 @@ __device__ __forceinline__ T row_wide(Exchange<1, 1>& all, T* s_warp, T v) {
 template <typename T> struct Raw;
 template <> struct Raw<__nv_bfloat16> {
     uint4 q;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void none() { q = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }   // -inf
     __device__ __forceinline__ float most() const {     // of the eight; a NaN wins
         const uint32_t m = max2(max2(q.x, q.y), max2(q.z, q.w));
@@ -147,7 +147,7 @@ template <> struct Raw<__nv_bfloat16> {
 template <> struct Raw<float> {
     float4 q[2];
     __device__ __forceinline__ void load(const float* p) {
-        q[0] = __ldg(reinterpret_cast<const float4*>(p)), q[1] = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        q[0] = reinterpret_cast<const float4*>(p)[0], q[1] = reinterpret_cast<const float4*>(p)[1];
     }
     __device__ __forceinline__ void none() { q[0] = q[1] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
     __device__ __forceinline__ float most() const {

@@ -141,7 +141,7 @@ __device__ __forceinline__ void load_x(const W4LinearArgs& a, int m, int k, int 
         for (int i = 0; i < NT; ++i) {
             const bool there = c < n && m + 8 * i < a.M;
             const int64_t at = there ? (int64_t)(m + 8 * i) * a.ldx + k + 32 * c : 0;
-            q[c][i] = __ldg(reinterpret_cast<const Q*>(reinterpret_cast<const uint8_t*>(a.x) + at * kSize));
+            q[c][i] = *reinterpret_cast<const Q*>(reinterpret_cast<const uint8_t*>(a.x) + at * kSize);
         }
 #pragma unroll
     for (int c = 0; c < KC; ++c)
@@ -171,6 +171,12 @@ __device__ __forceinline__ uint32_t ld_u32(uint32_t at) {
 __device__ __forceinline__ float2 ld_f32x2(uint32_t at) {
     float2 v;
     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+// Of x's scales, inside the group loop: kept where it stands, else the loads of all groups are begun early and 16 rows spill.
+__device__ __forceinline__ float ld_global(const float* at) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(at) : "memory");
     return v;
 }
 __device__ __forceinline__ void st_f32(uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); }
@@ -299,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a,
                         p[n][2] = fmaf(-z1, xs[n].x, p[n][2]), p[n][3] = fmaf(-z1, xs[n].y, p[n][3]);
                         if (a.x_blocks > 1) {
                             const int m = m0 + 8 * n + 2 * t, blk = (g0 + w0 + j) / x_block;
-                            const float x0 = m < a.M ? __ldg(a.x_scale + (int64_t)m * a.x_blocks + blk) : 0.f;
-                            const float x1 = m + 1 < a.M ? __ldg(a.x_scale + (int64_t)(m + 1) * a.x_blocks + blk) : 0.f;
+                            const float x0 = m < a.M ? ld_global(a.x_scale + (int64_t)m * a.x_blocks + blk) : 0.f;
+                            const float x1 = m + 1 < a.M ? ld_global(a.x_scale + (int64_t)(m + 1) * a.x_blocks + blk) : 0.f;
                             p[n][0] *= x0, p[n][1] *= x1, p[n][2] *= x0, p[n][3] *= x1;
                         }
                         acc[r][n][0] = fmaf(p[n][0], s0, acc[r][n][0]), acc[r][n][1] = fmaf(p[n][1], s0, acc[r][n][1]);
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_linear(const W4LinearArgs a,
             auto finish = [&](int r, int m, int row, float v) {
                 const int64_t n = (int64_t)(tile + r) * kRows + row;
                 if (n >= a.w.N) return;
-                if (a.x_scale && a.x_blocks == 1) v *= __ldg(a.x_scale + m0 + m);
+                if (a.x_scale && a.x_blocks == 1) v *= a.x_scale[m0 + m];
                 if (plan.slices > 1) a.parts[((int64_t)slice * a.M + m0 + m) * a.w.N + n] = v;
                 else w4_store(a, m0 + m, n, v);
             };

@@ -146,7 +146,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
             // a row's zeros, 16 groups at a time, the next ones under way: one byte of a row at a time would be a
             // load of 32 sectors, and its wait, for every step
             const uint4* const zeros = reinterpret_cast<const uint4*>(a.w.zeros + n * a.w.ldz);
-            auto zeros_at = [&](int block) { return a.w.zeros && block * 16 < a.w.K / GK ? __ldg(zeros + block) : make_uint4(0, 0, 0, 0); };
+            auto zeros_at = [&](int block) { return a.w.zeros && block * 16 < a.w.K / GK ? zeros[block] : make_uint4(0, 0, 0, 0); };
             int z_block = j0 / 16;
             uint4 z_now = zeros_at(z_block), z_next = zeros_at(z_block + 1);
             auto zero_of = [&](int j) {
@@ -207,7 +207,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
             // sectors, and its wait, for every group (that took twice the time of all the rest)
             const uint4* const scales = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.w.scales) + n_in * a.w.lds * (a.w.scale_bf16 ? 2 : 4));
             const int shift = a.w.scale_bf16 ? 3 : 2, per = 1 << shift;     // scales in 16 bytes
-            auto scales_at = [&](int block) { return block << shift < a.w.K / GK ? __ldg(scales + block) : make_uint4(0, 0, 0, 0); };
+            auto scales_at = [&](int block) { return block << shift < a.w.K / GK ? scales[block] : make_uint4(0, 0, 0, 0); };
             uint4 next = scales_at(j0 >> shift);
             float2 acc[kMine / 2] = {};                 // of two columns
             for (int block = j0 >> shift; block << shift < j0 + groups; ++block) {
@@ -236,7 +236,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                             const float* xs = a.x_scale + ((block << shift) + k) / x_block;
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                if (m0 + c0 + c + i < a.M) d[i] *= __ldg(xs + (int64_t)(m0 + c0 + c + i) * a.x_blocks);
+                                if (m0 + c0 + c + i < a.M) d[i] *= xs[(int64_t)(m0 + c0 + c + i) * a.x_blocks];
                         }
 #pragma unroll
                         for (int i = 0; i < 16; i += 2)
@@ -249,7 +249,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                 if (a.x_scale && a.x_blocks == 1) {
 #pragma unroll
                     for (int i = 0; i < kMine; ++i)
-                        if (i < rows) (i % 2 ? acc[i / 2].y : acc[i / 2].x) *= __ldg(a.x_scale + m0 + c0 + i);
+                        if (i < rows) (i % 2 ? acc[i / 2].y : acc[i / 2].x) *= a.x_scale[m0 + c0 + i];
                 }
                 auto put = [&](auto* to, int64_t stride) {
 #pragma unroll
@@ -265,6 +265,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
         // ---- copies of codes.  Here and below the whole warp walks the loop, so that what an instruction wants in
         // uniform registers stays there, and one elected lane issues (nothing more after a wait that expired: by the
         // end of the CTA what it issued before is long done).
+        before_copies();
         Ring cs;
         const int stages = (steps + kStageK / kStep - 1) / (kStageK / kStep);
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
@@ -278,6 +279,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
             }
     } else if (warp == kUnpack + kScale + 1) {
         // ---- copies of x
+        before_copies();
         uint32_t r = 0;
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
             for (int s = 0; s < steps; ++s, ++r) {
