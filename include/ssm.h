@@ -66,7 +66,8 @@ enum {
 
 /* Bits of the device status word (see ssm_device_status). */
 enum {
-    SSM_DEV_WAIT_TIMEOUT = 1u,  /* a bounded wait on a TMA copy expired; the block stopped early */
+    SSM_DEV_WAIT_TIMEOUT = 1u,  /* a bounded wait (on a copy, on another CTA) expired; the block stopped early or
+                                   went on without: that call's outputs are not to be used */
     SSM_DEV_BAD_SLOT = 2u,      /* a decode request named a state slot outside [0, n_slots) */
     SSM_DEV_SMEM_ALIGN = 4u,    /* shared memory was not 128-byte aligned; the prefill did nothing */
     SSM_DEV_BAD_INDEX = 8u      /* an attention call met a position, slot, page or length outside its
@@ -692,7 +693,7 @@ int w4_linear(int64_t M, int64_t N, int64_t K, int group, ssm_dtype_t x_dtype, c
  * spec_probs -- probabilities of logits: p[r][i] = exp(x_i / t) / sum_j exp(x_j / t) with t = temperature[r].
  * A temperature of 2^-100 or less, negative ones included, is greedy: 1 at the first largest logit, 0 elsewhere.
  * A logit of -inf has probability 0; a row whose logits are all -inf gives zeros.  A NaN or +inf among a row's
- * logits, or a NaN temperature, gives a row of NaN.  A temperature of +inf counts as the largest finite one.
+ * logits, or a NaN temperature, gives a row of NaN.  (Where SSM_DEV_WAIT_TIMEOUT was set, so may be any part of a row.)  A temperature of +inf counts as the largest finite one.
  *
  *   n_rows, vocab        n_rows >= 0 (0 does nothing) < 2^28; vocab 1 .. 2^24
  *   in_dtype, logits     [n_rows][vocab] SSM_BF16 or SSM_F32, row stride ld_in >= vocab, element aligned
@@ -726,7 +727,7 @@ int spec_probs(int64_t n_rows, int64_t vocab, ssm_dtype_t in_dtype, const void* 
  *   tokens               [batch][n_max + 1] int32: the kept tokens, the next one, then -1
  *   n_kept               [batch] int32
  * Probabilities are >= 0 and sum up to about 1: a negative one or a NaN counts as 0, and a row p that is
- * drawn from and sums up to 0 or to 3.99 or more gives token -1.
+ * drawn from and sums up to 0 or to 3.99 or more gives token -1.  (Where SSM_DEV_WAIT_TIMEOUT was set, so may be any.)
  */
 int spec_verify(int batch, int n_max, int64_t vocab, const int32_t* draft, const int32_t* n_draft,
                 const float* target_probs, int64_t tp_stride_b, int64_t tp_stride_t,
@@ -742,6 +743,10 @@ int spec_verify(int batch, int n_max, int64_t vocab, const int32_t* draft, const
  * context stays usable, without faulting or hanging the GPU.
  */
 int ssm_selftest_expire_wait(int limit_us, void* cuda_stream);
+
+/* The same for each of the library's waits: which = 0 that one, 1 the waits of w4_linear, 2 the exchange between the
+ * CTAs of a cluster in spec_probs and spec_verify (two CTAs, each waiting for a word that the other does not send). */
+int ssm_selftest_expire_wait_of(int which, int limit_us, void* cuda_stream);
 
 /*
  * ssm_device_status -- read (and if `clear` is nonzero, reset) the device status

@@ -29,7 +29,7 @@ EXPORTS = ("ssm_abi_version", "ssm_prefill", "ssm_prefill_workspace_bytes", "ssm
            "attn_rope_table", "attn_append", "attn_cache_read", "attn_prefill", "attn_decode_workspace_bytes",
            "attn_decode_step", "norm_rms", "w4_quantize", "w4_linear_workspace_bytes", "w4_linear", "spec_probs",
            "spec_verify",
-           "ssm_selftest_expire_wait", "ssm_device_status", "ssm_last_error")
+           "ssm_selftest_expire_wait", "ssm_selftest_expire_wait_of", "ssm_device_status", "ssm_last_error")
 NOALLOC_SCRATCH_BYTES = 4 << 20     # SSM_NOALLOC_SCRATCH_BYTES
 
 
@@ -118,6 +118,8 @@ def load(path: Path | str | None = None):
     lib.spec_verify.restype = I
     lib.ssm_selftest_expire_wait.argtypes = [I, P]
     lib.ssm_selftest_expire_wait.restype = I
+    lib.ssm_selftest_expire_wait_of.argtypes = [I, I, P]
+    lib.ssm_selftest_expire_wait_of.restype = I
     lib.ssm_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), I]
     lib.ssm_device_status.restype = I
     if path is None:
@@ -503,10 +505,11 @@ def out_proj_partial(y, W, out=None, out_dtype=torch.bfloat16, block_amax=True, 
     return out, amax
 
 
-def selftest_expire_wait(limit_us: int = 50000, stream=None) -> None:
-    """ssm_selftest_expire_wait: one kernel whose bounded wait expires after limit_us."""
+def selftest_expire_wait(limit_us: int = 50000, stream=None, which: int = 0) -> None:
+    """ssm_selftest_expire_wait: one kernel whose bounded wait expires after limit_us.  ``which``
+    (ssm_selftest_expire_wait_of) 0: a copy's; 1: those of w4_linear; 2: spec_probs's and spec_verify's."""
     lib = load()
-    _check(lib, "ssm_selftest_expire_wait", lib.ssm_selftest_expire_wait(int(limit_us), _stream(stream)))
+    _check(lib, "ssm_selftest_expire_wait_of", lib.ssm_selftest_expire_wait_of(int(which), int(limit_us), _stream(stream)))
 
 
 # ------------------------------------------------------------------ SSD (Mamba-2-style) mixer

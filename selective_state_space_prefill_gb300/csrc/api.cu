@@ -456,17 +456,23 @@ int ssd_decode_step(int batch, int n_heads, int head_dim, int n_groups, int d_st
     return SSM_OK;
 }
 
-int ssm_selftest_expire_wait(int limit_us, void* cuda_stream) {
-    static const char* fn = "ssm_selftest_expire_wait";
+static int expire_wait(const char* fn, int which, int limit_us, void* cuda_stream) {
     g_err[0] = 0;
+    if (which < 0 || which > 2) return fail(SSM_ERR_INVALID_ARG, "%s: which %d not in [0, 2]", fn, which);
     if (limit_us < 1 || limit_us > 2000000) return fail(SSM_ERR_INVALID_ARG, "%s: limit_us %d not in [1, 2e6]", fn, limit_us);
     int serr = 0;
     unsigned int* status = status_ptr(&serr);
     if (serr) return fail(SSM_ERR_CUDA, "%s: no usable CUDA device", fn);
     const char* why = "";
-    if (ssm::launch_expire_wait(status, (uint64_t)limit_us * 1000u, static_cast<cudaStream_t>(cuda_stream), &why) != 0)
+    if (ssm::launch_expire_wait(which, status, (uint64_t)limit_us * 1000u, static_cast<cudaStream_t>(cuda_stream), &why) != 0)
         return fail(SSM_ERR_CUDA, "%s: %s", fn, why);
     return SSM_OK;
+}
+
+int ssm_selftest_expire_wait(int limit_us, void* cuda_stream) { return expire_wait("ssm_selftest_expire_wait", 0, limit_us, cuda_stream); }
+
+int ssm_selftest_expire_wait_of(int which, int limit_us, void* cuda_stream) {
+    return expire_wait("ssm_selftest_expire_wait_of", which, limit_us, cuda_stream);
 }
 
 size_t ssm_prefill_workspace_bytes(int batch, int seqlen, int d_inner, int seg_len) {

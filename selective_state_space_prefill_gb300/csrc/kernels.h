@@ -367,7 +367,7 @@ int launch_q8_quantize(const void* x, bool in_bf16, int64_t n, const float* amax
                        cudaStream_t stream, const char** why);
 int launch_q8_sum(int P, const int8_t* const* codes, const float* scales, int64_t n, void* out, bool out_bf16,
                   int32_t* sums, cudaStream_t stream, const char** why);
-int launch_expire_wait(unsigned int* status, uint64_t limit_ns, cudaStream_t stream, const char** why);
+int launch_expire_wait(int which, unsigned int* status, uint64_t limit_ns, cudaStream_t stream, const char** why);
 int launch_out_proj(const OutProjArgs& a, const void* y, const void* W, int64_t ldy, int64_t ldw, bool out_bf16,
                     cudaStream_t stream, const char** why);
 

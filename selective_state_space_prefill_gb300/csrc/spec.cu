@@ -4,15 +4,12 @@
 // Both read rows of the vocabulary's length, a few or hundreds of them: a row is a thread-block cluster's, cut into
 // a slice per CTA, and what the CTAs have to know of each other (a maximum, sums) goes through distributed shared
 // memory.
-#include <cooperative_groups.h>
-
 #include <type_traits>
 
 #include "common.cuh"
+#include "exchange.cuh"
 #include "kernels.h"
 #include "ssm.h"
-
-namespace cg = cooperative_groups;
 
 namespace ssm {
 namespace {
@@ -32,66 +29,7 @@ __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7fc00000
 // branch, came out as one 16-byte store, which faults where the row is not aligned.
 __device__ __forceinline__ void store1(float* p, float v) { asm volatile("st.global.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory"); }
 
-// What the warps of a row's CTAs tell each other, at most twice: each writes its words into the shared memory of every
-// CTA of the cluster, in 64 bits of which the upper half is the word and the lower half says that it is there, and
-// reads the others' from its own.  A word and its mark come as one, so nothing has to be ordered, and nobody waits
-// for anything but the words.  (A barrier of the cluster, and reads from the others behind it, waits for all that the
-// SM has under way, two microseconds where four CTAs of it write: 512 x 131072 95 us so, 86 with words; 64 x 32000 7.5
-// and 5.0.  Words of every warp instead of every CTA, polled by all: 107, 6.7.)  The two exchanges
-// have slots of their own, and a CTA that has all words of the last one is written to by nobody: it may leave.
-constexpr int kMostCtas = 8;
-template <int kWords, int kWarps> struct Exchange {
-    struct Box {                                        // in shared memory
-        uint64_t slot[2][kWords][kMostCtas * kWarps];
-    };
-    Box& box;
-    int ctas, rank;
-    unsigned int* status;
-    int turn = 0;
-    bool dead = false;
-
-    // By all threads; ready() before the first words are sent.
-    __device__ __forceinline__ Exchange(Box& box, int ctas, int rank, unsigned int* status) : box(box), ctas(ctas), rank(rank), status(status) {
-        for (int i = threadIdx.x; i < 2 * kWords * kMostCtas * kWarps; i += blockDim.x) (&box.slot[0][0][0])[i] = 0;
-        if (ctas > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    }
-    __device__ __forceinline__ void ready() {
-        if (ctas > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-        else __syncthreads();
-    }
-    // A warp's words (the CTA's where kWarps is 1), the same in all lanes.
-    __device__ __forceinline__ void send(const uint32_t (&words)[kWords]) {
-        const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-        if (lane < ctas && warp < kWarps) {
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                uint64_t* to = &box.slot[turn][w][rank * kWarps + warp];
-                if (ctas > 1) to = cg::this_cluster().map_shared_rank(to, lane);
-                *reinterpret_cast<volatile uint64_t*>(to) = (uint64_t)words[w] << 32 | 1u;
-            }
-        }
-        ++turn;
-    }
-    // A word of the last exchange by warp and CTA; gives up after two seconds, like all waits here.
-    __device__ __forceinline__ uint32_t word(int w, int from) {
-        const volatile uint64_t* at = &box.slot[turn - 1][w][from];
-        uint64_t v = *at, t0 = 0;
-        for (uint32_t spin = 0; v == 0 && !dead; ++spin) {
-            if ((spin & 4095u) == 4095u) {
-                const uint64_t now = globaltimer_ns();
-                if (t0 == 0) t0 = now;
-                if (now - t0 > 2000000000ull) {
-                    dead = true;
-                    atomicOr(status, (unsigned)SSM_DEV_WAIT_TIMEOUT);
-                }
-            }
-            v = *at;
-        }
-        return (uint32_t)(v >> 32);
-    }
-};
-
-// A value of all threads of a row.
+// A value of all threads of a row (of no use to a warp that gave up).
 enum Kind { kMax, kSum, kLeast };
 template <Kind K, typename T>
 __device__ __forceinline__ T two(T a, T b) {
@@ -119,9 +57,16 @@ __device__ __forceinline__ T row_wide(Exchange<1, 1>& all, T* s_warp, T v) {
     if (all.ctas == 1) return v;
     all.send({bits_of(v)});
     v = from_bits<T>(all.word(0, threadIdx.x % all.ctas));
-    __syncwarp();
+    all.settle();
     for (int o = all.ctas / 2; o > 0; o >>= 1) v = two<K>(v, __shfl_xor_sync(~0u, v, o));
     return v;
+}
+
+// Of a warp that has no part in a row's second value, be it that the row is NaN or that the warp gave up: what the
+// others of its CTA look for at their barrier there.
+__device__ __forceinline__ void none_of_row(float* s_sum, int* s_at) {
+    if (threadIdx.x % 32 == 0) s_sum[threadIdx.x / 32] = quiet_nan(), s_at[threadIdx.x / 32] = 0x7fffffff;
+    __syncthreads();
 }
 
 // Eight logits as they came.
@@ -205,7 +150,8 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
     // p = 2^((x - m) f) inv, or 1 at one place, or the same everywhere
     float f = 0.f, inv = quiet_nan();
     int least = -1;
-    if (!(m < INFINITY) || t != t) {                    // NaN or +inf among the logits: NaN
+    if (!(m < INFINITY) || t != t || all.dead) {        // NaN or +inf among the logits: NaN
+        none_of_row(s_sum, s_at);
     } else if (t <= 0x1p-100f || m == -INFINITY) {      // greedy: 1 at the first largest; nothing to choose from: zeros
         inv = 0.f;
         least = 0x7fffffff;
@@ -227,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
             for (int k = 0; k < 8; ++k) l += ex2((v[i].at(k) - m) * f);
         inv = __fdiv_rn(1.f, row_wide<kSum, kWarps>(all, s_sum, l));
     }
+    if (all.dead) f = 0.f, inv = quiet_nan(), least = -1;
     next_may_start();                                   // 64 x 32000 7.5 us, at the kernel's start 7.8
     const int start = head + 8 * first;
     const bool whole = reinterpret_cast<uintptr_t>(p + start) % 16 == 0;
@@ -248,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
     };
     if (f > 0.f) write([&](float x, int) { return ex2((x - m) * f) * inv; });
     else write([&](float, int at) { return at == least ? 1.f : inv; });
+    all.leave();
 }
 
 // Rows longer than a cluster's registers hold: read three times, from L2 after the first.
@@ -270,7 +218,8 @@ __global__ void __launch_bounds__(512) k_spec_probs_long(const ProbsArgs a, int 
     for (int i = lo + threadIdx.x; i < hi; i += kThreads) m = max_nan(m, to_f32(x[i]));
     all.ready();
     m = row_wide<kMax, kWarps>(all, s_max, m);
-    if (!(m < INFINITY) || t != t) {
+    if (!(m < INFINITY) || t != t || all.dead) {
+        none_of_row(s_sum, s_at);
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = quiet_nan();
     } else if (t <= 0x1p-100f || m == -INFINITY) {
         int least = 0x7fffffff;
@@ -278,17 +227,19 @@ __global__ void __launch_bounds__(512) k_spec_probs_long(const ProbsArgs a, int 
         for (int i = lo + threadIdx.x; i < hi; i += kThreads)
             if (to_f32(x[i]) == m && m > -INFINITY) least = min(least, i);
         least = row_wide<kLeast, kWarps>(all, s_at, least);
-        for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = i == least ? 1.f : 0.f;
+        const float rest = all.dead ? quiet_nan() : 0.f;
+        for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = i == least ? 1.f : rest;
     } else {
         const float f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
         float l = 0.f;
 #pragma unroll 8
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) l += ex2((to_f32(x[i]) - m) * f);
         l = row_wide<kSum, kWarps>(all, s_sum, l);
-        const float inv = __fdiv_rn(1.f, l);
+        const float inv = all.dead ? quiet_nan() : __fdiv_rn(1.f, l);
 #pragma unroll 8
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = ex2((to_f32(x[i]) - m) * f) * inv;
     }
+    all.leave();
 }
 
 // ------------------------------------------------------------------ verification
@@ -454,15 +405,17 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
             total += part, mags += __uint_as_float(all.word(2, i));
             before += i < rank * kWarps + warp ? part : 0;
         }
-        __syncwarp();
+        all.settle();
         total = warp_sum(total), before = warp_sum(before), mags = warp_sum(mags);
-        if (total > 0 || turn == 1 || (!w.q && w.off < 0)) break;
+        if (total > 0 || turn == 1 || (!w.q && w.off < 0) || all.dead) break;
         w.q = nullptr, w.off = -1;                      // nothing left of p - q: p itself
     }
     next_may_start();
     // the first index whose running sum exceeds floor(u * total)
     const uint64_t border = __umul64hi(__float2ull_rz(draw * 0x1p64f), total);
-    if (total == 0 || !(mags < 3.99f)) {                // no distribution
+    if (all.dead) {                                     // whose part may have been to find it
+        if (lane == 0) out[kept] = -1;
+    } else if (total == 0 || !(mags < 3.99f)) {         // no distribution
         if (rank == 0 && threadIdx.x == 0) out[kept] = -1;
     } else if (before <= border && border < before + mine) {
         // the notes say between which two of them; that is read again (from L2)
@@ -501,6 +454,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyA
             before += __shfl_sync(~0u, to, 31);
         }
     }
+    all.leave();
 }
 
 // A cluster of `ctas` for each row.

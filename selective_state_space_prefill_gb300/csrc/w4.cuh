@@ -27,6 +27,7 @@ __device__ __forceinline__ void x_pairs(uint2 q, uint32_t (&r)[4]) {    // whole
 // takes longer to read than most waits, so it is not looked at before 4096 tries.
 struct Waiter {
     unsigned int* status;
+    uint64_t limit_ns = 2000000000ull;
     bool dead = false;
     __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
         if (dead) return;
@@ -35,7 +36,7 @@ struct Waiter {
             if ((spin & 4095u) == 4095u) {
                 const uint64_t now = globaltimer_ns();
                 if (t0 == 0) t0 = now;
-                if (now - t0 > 2000000000ull) {
+                if (now - t0 > limit_ns) {
                     dead = true;
                     atomicOr(status, (unsigned)SSM_DEV_WAIT_TIMEOUT);
                     return;

@@ -37,7 +37,7 @@ def test_every_kernel_launched_so_waits_for_the_one_before(path):
     bodies = re.findall(r"__global__[^;{]*?\b(k_\w+)\([^{]*\{(.*?)\n\}\n", code, flags=re.S)
     assert bodies
     for name, body in bodies:
-        if name == "k_w4_quantize":                     # launched the usual way
+        if name in ("k_w4_quantize", "k_expire_wait"):   # launched the usual way
             assert "after_previous" not in body and "next_may_start" not in body
             continue
         assert body.count("after_previous()") == 1, name
@@ -54,3 +54,24 @@ def test_tensor_copies_come_behind_their_fence():
         for part in re.split(r"\} else if \(warp", code[code.index("after_previous()"):]):
             at = part.find("tma_load_2d(")
             assert at < 0 or 0 <= part.find("before_copies()") < at, path.name
+
+
+def test_who_exchanges_words_stays_as_long_as_they_may_come():
+    """Every kernel that makes an Exchange gives a warp up as a whole and ends by leave(), with no way out before it;
+    a warp that gave up sends nothing to CTAs that may have left."""
+    seen = 0
+    for path in _in_turn():
+        if path.suffix != ".cu":
+            continue
+        for name, body in re.findall(r"__global__[^;{]*?\b(k_\w+)\([^{]*\{(.*?)\n\}\n", _code(path), flags=re.S):
+            if "Exchange<" in body:
+                seen += 1
+                assert body.rstrip().endswith("all.leave();"), name
+                assert not re.search(r"^    (if [^\n]*)?return;", body, flags=re.M), name
+                assert body.rfind(".settle()") >= body.rfind(".word("), name
+    assert seen >= 4
+    code = _code(build.CSRC / "exchange.cuh")
+    send = code[code.index("void send("):code.index("uint32_t word(")]
+    assert "!dead" in send
+    row = _code(build.CSRC / "spec.cu")
+    assert row.count(".word(") == 4 and "all.settle();" in row[row.index("row_wide("):row.index("struct Raw")]
