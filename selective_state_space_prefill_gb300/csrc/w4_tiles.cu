@@ -109,6 +109,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
     // where a step is a group, one commit tells both that its operands are used and that its sums are there
     uint64_t *const d_full = full + kSteps, *const used = GK == kStep ? d_full : d_full + kD, *const d_empty = d_full + kD + kSteps;
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(d_empty + kD);
+    uint64_t* const done = d_empty + kD + 1;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int m0 = blockIdx.y * MP, slice = blockIdx.z;
@@ -123,6 +124,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
             if (GK != kStep) mbar_init(&d_full[i], 1);
             mbar_init(&d_empty[i], kScale);
         }
+        mbar_init(done, 1);
         fence_barrier_init();
         prefetch_tmap(&tm_codes);
         prefetch_tmap(&tm_x);
@@ -263,10 +265,12 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
         }
     } else if (warp == kUnpack + kScale) {
         // ---- copies of codes.  Here and below the whole warp walks the loop, so that what an instruction wants in
-        // uniform registers stays there, and one elected lane issues (nothing more after a wait that expired: by the
-        // end of the CTA what it issued before is long done).
+        // uniform registers stays there, and one elected lane issues, nothing more after a wait that expired.  In the end it
+        // waits for what it issued last: who reads it has waited for it, but goes on where that wait expired, and the CTA must
+        // not end before its copies.
         before_copies();
         Ring cs;
+        uint32_t issued = 0;
         const int stages = (steps + kStageK / kStep - 1) / (kStageK / kStep);
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
             for (int i = 0; i < stages; ++i, cs.next()) {
@@ -274,13 +278,16 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                 if (elect_one() && !wait.dead) {
                     mbar_arrive_expect_tx(&c_full[cs.at], kStageC);
                     tma_load_2d(smem + cs.at * kStageC, &tm_codes, &c_full[cs.at], k0 / 2 + i * (kStageK / 2), tile * kRows);
+                    ++issued;
                 }
                 __syncwarp();
             }
+        Waiter last{status};
+        for (uint32_t i = issued < kCodeStages ? 0 : issued - kCodeStages; i < issued; ++i) last(&c_full[i % kCodeStages], i / kCodeStages & 1);
     } else if (warp == kUnpack + kScale + 1) {
         // ---- copies of x
         before_copies();
-        uint32_t r = 0;
+        uint32_t r = 0, issued = 0;
         for (int tile = blockIdx.x; tile < cut.tiles; tile += gridDim.x)
             for (int s = 0; s < steps; ++s, ++r) {
                 const uint32_t buf = r % kSteps;
@@ -289,9 +296,12 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                     mbar_arrive_expect_tx(&full[buf], G::kStageX);
                     for (int h = 0; h < 2; ++h)
                         tma_load_2d(smem + G::kOffX + buf * G::kStageX + h * (G::kStageX / 2), &tm_x, &full[buf], k0 + s * kStep + 64 * h, m0);
+                    ++issued;
                 }
                 __syncwarp();
             }
+        Waiter last{status};
+        for (uint32_t i = issued < kSteps ? 0 : issued - kSteps; i < issued; ++i) last(&full[i % kSteps], i / kSteps & 1);
     } else {
         // ---- products
         const uint32_t tm = __shfl_sync(~0u, tmem, 0);
@@ -324,8 +334,14 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
                     __syncwarp();
                 }
             }
-        // the last commits have arrived before the CTA ends
+        // the last commits have arrived before the CTA ends; where the loop ended early, one for all that was issued
         for (uint32_t i = r < kSteps ? 0 : r - kSteps; i < r; ++i) wait(&used[i % kSteps], i / kSteps & 1);
+        if (__any_sync(~0u, wait.dead)) {
+            if (elect_one()) mma_commit(done);
+            __syncwarp();
+            Waiter last{status};
+            last(done, 0);
+        }
     }
     tc_fence_before();
     __syncthreads();

@@ -75,3 +75,16 @@ def test_who_exchanges_words_stays_as_long_as_they_may_come():
     assert "!dead" in send
     row = _code(build.CSRC / "spec.cu")
     assert row.count(".word(") == 4 and "all.settle();" in row[row.index("row_wide("):row.index("struct Raw")]
+
+
+def test_a_cta_does_not_end_before_its_copies():
+    """A warp that issues tensor copies into shared memory counts them and waits for the last ones by a wait of its own,
+    whatever waits expired before; the one that issues products has a commit for them then."""
+    code = _code(build.CSRC / "w4_tiles.cu")
+    parts = [p for p in re.split(r"\} else (?:if \(warp|\{)", code[code.index("k_w4_tiles("):])]
+    copies = [p for p in parts if "tma_load_2d(" in p]
+    assert len(copies) == 2
+    for p in copies:
+        assert "++issued" in p and p.index("Waiter last{status}") > p.index("tma_load_2d(") and "i < issued; ++i) last(" in p
+    products = [p for p in parts if "mma_from_tmem(" in p[:3000] and "mma_commit(&d_full" in p]
+    assert len(products) == 1 and "mma_commit(done)" in products[0] and "last(done, 0)" in products[0]
