@@ -622,7 +622,8 @@ int attn_decode_step(int batch, int n_q_heads, int n_kv_heads, int head_dim, ssm
  * out_dtype SSM_I8: a scale per row and group, the attention cache's rule: amax = max |y| over the group,
  * scale = amax / 127, code = round_half_even(y * (127 / amax)) clamped to [-127, 127], IEEE fp32; amax == 0
  * gives scale and codes 0, a NaN is ignored by amax and gets code 0, an infinite amax gives scale +inf and
- * codes 0.  Squares are summed in fp32: |r| from 2^60 on can overflow the mean.
+ * codes 0.  Squares are summed in fp32, from r times a power of two where they would leave its range: every finite r,
+ * small or large, gives its y.  A group of zeros with eps = 0 is 0 / 0: NaN.
  *
  *   n_rows               >= 0 (0 does nothing); n_rows * n_groups < 2^31
  *   width, n_groups      n_groups divides width; a group is a multiple of 8 channels, up to 32768

@@ -78,9 +78,39 @@ __device__ __forceinline__ float across(float v, float* s) {
     return __shfl_sync(~0u, v, 0);
 }
 
+// The mean of squares (with eps) of a group whose squares leave fp32's range, from its r (a thread's `count` in t, which
+// come back scaled) times a power of two that brings the larger of r and the root of eps near 1.  Groups of zeros
+// without eps and infinities keep the mean they have.  A call, with r in local memory, as it is hardly ever made: inlined it
+// took registers from every form, 16384 x 7168 fp32 101 us -> 109.
+template <int W>
+__device__ __noinline__ float mean_again(float* t, int count, int n, float eps, float mean, float* s_max, float* s_sum) {
+    float most = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) most = fmaxf(most, fabsf(t[i]));
+    most = fmaxf(across<W, true>(most, s_max), sqrtf(eps));
+    if (most > 0.f && most < INFINITY) {
+        const float by = __int_as_float((254 - min(__float_as_int(most) >> 23, 253)) << 23);    // 2^127 .. 2^-126
+        float sum = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < count; ++i) t[i] *= by, sum = fmaf(t[i], t[i], sum);
+        mean = across<W, false>(sum, s_sum) / n + eps * by * by;
+    }
+    if (W > 1) __syncthreads();                         // the maximum's place is used again
+    return mean;
+}
+
+// Blocks an SM that the registers of a form with int8 out are kept to (0: the compiler's choice, which would be one less):
+// 64 a thread, or 80 for fp32 x and residual and, up to 8192 channels, for an fp32 residual of bf16 x (4096 x 8192 60 us,
+// with 64 and spills 65; with fp32 x alone 64 are right: 16384 x 7168 105 us, with more 116).
+template <typename Tx, typename Tr, typename To, int W, int V>
+constexpr int blocks_per_sm() {
+    if (V == 1 || sizeof(To) != 1 || W == 32) return 0;
+    return (sizeof(Tr) == 4 && (sizeof(Tx) == 4 || W <= 8) ? 768 : 1024) / (W == 1 ? 128 : 32 * W);
+}
+
 // W warps for a group (1: four groups to a CTA), V vectors a thread.
 template <typename Tx, typename Tr, typename To, int W, int V>
-__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) k_norm_rms(const NormArgs a) {
+__global__ void __launch_bounds__(W == 1 ? 128 : 32 * W, blocks_per_sm<Tx, Tr, To, W, V>()) k_norm_rms(const NormArgs a) {
     constexpr bool kI8 = sizeof(To) == 1;
     constexpr int kStep = 8 * 32 * W;                   // channels of a group between a thread's vectors
     __shared__ float s_sum[W], s_max[W];
@@ -114,7 +144,22 @@ __global__ void __launch_bounds__(W == 1 ? 128 : 32 * W) k_norm_rms(const NormAr
 #pragma unroll
             for (int k = 0; k < 8; ++k) sum = fmaf(v[i][k], v[i][k], sum);
         }
-    const float f = rsqrtf(across<W, false>(sum, s_sum) / n + a.eps);
+    float mean = across<W, false>(sum, s_sum) / n + a.eps;
+    // Squares lose places below 2^-126, are gone below 2^-149, and pass fp32's range: a mean below 2^-100 (at which what is
+    // lost is 2^-49 of it) or infinite is taken again.  All threads of a group agree on that.
+    if (!(mean >= 0x1p-100f && mean < INFINITY) && mean == mean) {
+        float t[V * 8];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t[i * 8 + k] = first + i * kStep < n ? v[i][k] : 0.f;
+        mean = mean_again<W>(t, V * 8, n, a.eps, mean, s_max, s_sum);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = t[i * 8 + k];
+    }
+    const float f = rsqrtf(mean);
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
