@@ -25,6 +25,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7fc00000u); }
 
+// e^((x - m) / t) of half the maximum m and twice the rate log2(e) / t: halves of logits differ by no more than the largest
+// float, where logits may by twice that; all else is the same to the bit.
+__device__ __forceinline__ float twice_rate(float t) { return __fdiv_rn(1.f, fminf(t, 0x1.fffffep127f)) * kLog2e * 2.f; }
+__device__ __forceinline__ float power(float x, float half, float f) { return ex2(fmaf(x, 0.5f, -half) * f); }
+
 // One float, whatever stands beside it: plain stores of four neighbours, next to one of them as a float4 in the other
 // branch, came out as one 16-byte store, which faults where the row is not aligned.
 __device__ __forceinline__ void store1(float* p, float v) { asm volatile("st.global.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory"); }
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
     m = row_wide<kMax, kWarps>(all, s_max, m);
 
     // p = 2^((x - m) f) inv, or 1 at one place, or the same everywhere
-    float f = 0.f, inv = quiet_nan();
+    float f = 0.f, half = 0.f, inv = quiet_nan();
     int least = -1;
     if (!(m < INFINITY) || t != t || all.dead) {        // NaN or +inf among the logits: NaN
         none_of_row(s_sum, s_at);
@@ -165,12 +170,12 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
         }
         least = row_wide<kLeast, kWarps>(all, s_at, least);
     } else {
-        f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
-        float l = ex2((w - m) * f);
+        f = twice_rate(t), half = 0.5f * m;
+        float l = power(w, half, f);
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) l += ex2((v[i].at(k) - m) * f);
+            for (int k = 0; k < 8; ++k) l += power(v[i].at(k), half, f);
         inv = __fdiv_rn(1.f, row_wide<kSum, kWarps>(all, s_sum, l));
     }
     if (all.dead) f = 0.f, inv = quiet_nan(), least = -1;
@@ -193,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
             }
         }
     };
-    if (f > 0.f) write([&](float x, int) { return ex2((x - m) * f) * inv; });
+    if (f > 0.f) write([&](float x, int) { return power(x, half, f) * inv; });
     else write([&](float, int at) { return at == least ? 1.f : inv; });
     all.leave();
 }
@@ -230,14 +235,14 @@ __global__ void __launch_bounds__(512) k_spec_probs_long(const ProbsArgs a, int 
         const float rest = all.dead ? quiet_nan() : 0.f;
         for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = i == least ? 1.f : rest;
     } else {
-        const float f = __fdiv_rn(1.f, fminf(t, 3.0e38f)) * kLog2e;
+        const float f = twice_rate(t), half = 0.5f * m;
         float l = 0.f;
 #pragma unroll 8
-        for (int i = lo + threadIdx.x; i < hi; i += kThreads) l += ex2((to_f32(x[i]) - m) * f);
+        for (int i = lo + threadIdx.x; i < hi; i += kThreads) l += power(to_f32(x[i]), half, f);
         l = row_wide<kSum, kWarps>(all, s_sum, l);
         const float inv = all.dead ? quiet_nan() : __fdiv_rn(1.f, l);
 #pragma unroll 8
-        for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = ex2((to_f32(x[i]) - m) * f) * inv;
+        for (int i = lo + threadIdx.x; i < hi; i += kThreads) p[i] = power(to_f32(x[i]), half, f) * inv;
     }
     all.leave();
 }
