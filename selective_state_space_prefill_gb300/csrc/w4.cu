@@ -43,7 +43,8 @@ __global__ void __launch_bounds__(256) k_w4_quantize(const W4Weight w, const Tin
         lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
     }
-    float s = w.zeros ? __fdiv_rn(hi - lo, 15.f) : __fdiv_rn(fmaxf(-lo, hi), 7.f);
+    // (hi - lo) / 15 by halves, whose difference is always finite
+    float s = w.zeros ? __fdiv_rn(fmaf(hi, 0.5f, -0.5f * lo), 7.5f) : __fdiv_rn(fmaxf(-lo, hi), 7.f);
     if (w.scale_bf16) s = __bfloat162float(__float2bfloat16_rn(s));
     float zero = 8.f, least = 1.f, most = 15.f;
     if (w.zeros) {
