@@ -380,13 +380,15 @@ constexpr int kSms = 152;
 
 int rows_of(int M) { return M <= 32 ? 32 : 64; }
 
-// Slices of the rows where the tiles alone leave SMs idle, by the CTA with most work at 24 bytes of codes a nanosecond
-// (0.35 us a step), and for the second kernel two microseconds and the slices' sums at 4 TB/s.  64 x 4096 -> 8192: one
-// slice 19.4 us, two 16.
+// Slices of the rows where the tiles alone leave SMs idle, by the CTA with most work, and for the second kernel two
+// microseconds and the slices' sums at 4 TB/s.  A step takes 0.35 us with groups of 128, which is 24 bytes of codes a
+// nanosecond, more with the two or four accumulators of groups of 64 or 32: 20, 12.  64 x 4096 -> 8192, groups of 128:
+// one slice 19.4 us, two 16.  Counted at 24, groups of 32 and 64 had one slice for 128 x 2048 -> 2048: 20.8 and 13.3 us,
+// now 11.1 and 9.4; 20 x 5120 -> 13824 in groups of 32 40.9, now 36.3; 48 other sizes measured the same.
 Cut cut_of(int M, const W4Weight& w) {
     Cut best{};
     int64_t least = 0;
-    const int stages = (w.K + kStageK - 1) / kStageK;
+    const int stages = (w.K + kStageK - 1) / kStageK, rate = w.group == 32 ? 12 : w.group == 64 ? 20 : 24;
     for (int s = 1; s <= 32 && s <= stages; ++s) {
         Cut c;
         c.tiles = (w.N + kRows - 1) / kRows;
@@ -396,7 +398,7 @@ Cut cut_of(int M, const W4Weight& w) {
         int walkers = kSms / (c.m_blocks * c.slices);
         walkers = walkers < 1 ? 1 : walkers > c.tiles ? c.tiles : walkers;
         const int64_t bytes = (int64_t)((c.tiles + walkers - 1) / walkers) * c.slice_k * (kRows / 2);
-        const int64_t ns = bytes / 24 + (c.slices > 1 ? 2000 + (int64_t)c.slices * M * w.N * 8 / 4000 : 0);
+        const int64_t ns = bytes / rate + (c.slices > 1 ? 2000 + (int64_t)c.slices * M * w.N * 8 / 4000 : 0);
         if (s == 1 || ns < least) best = c, least = ns;
     }
     return best;

@@ -233,3 +233,27 @@ def test_no_output_of_a_row_with_an_infinity_or_nan_is_finite(m, group, zeros):
             assert not torch.isfinite(got[row]).any()
             rest = torch.arange(m, device=DEV) != row
             assert torch.equal(got[rest], clean[rest])
+
+
+@pytest.mark.parametrize("m,k,n", [(128, 2048, 2048), (100, 2080, 2100), (20, 5120, 13824), (256, 1024, 3000)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_many_rows_whose_slices_go_by_the_group(m, k, n, group):
+    """More slices for smaller groups, which take longer; the workspace is what the call's own plan asks for."""
+    k = k // group * group
+    g = torch.Generator(device=DEV).manual_seed(m)
+    codes = torch.randint(0, 256, (n, -(-k // 32) * 16), generator=g, dtype=U8, device=DEV)[:, :k // 2]
+    groups = k // group
+    scales = torch.nn.functional.pad(0.02 * torch.randn(n, groups, generator=g, device=DEV), (0, -groups % 4))[:, :groups]
+    zeros = torch.nn.functional.pad(torch.randint(0, 16, (n, groups), generator=g, dtype=U8, device=DEV), (0, -groups % 16))[:, :groups]
+    x = torch.randn(m, k, generator=g, device=DEV).to(BF16)
+    need = ssm.w4_linear_workspace_bytes(m, n, k, group)
+    work = torch.full((need + 64,), 77, device=DEV, dtype=U8)
+    got = ssm.w4_linear(x, codes, scales, zeros, out_dtype=F32, workspace=work[:need])
+    check_linear(got, x, codes, scales, zeros, None)
+    assert (work[need:] == 77).all()
+    assert torch.equal(got, ssm.w4_linear(x, codes, scales, zeros, out_dtype=F32))
+
+
+def test_smaller_groups_have_at_least_as_many_slices():
+    bytes_of = [ssm.w4_linear_workspace_bytes(128, 2048, 2048, group) for group in (128, 64, 32)]
+    assert bytes_of == sorted(bytes_of) and bytes_of[1] > bytes_of[0]
