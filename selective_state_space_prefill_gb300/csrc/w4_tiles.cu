@@ -71,6 +71,13 @@ __device__ __forceinline__ uint4 ld_u128(uint32_t at) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
 }
+// Sixteen zeros of a row, where they stand in the loop: left to move, the load cost groups of 128 three hundredths (64 x 2560 ->
+// 50021 36.0 us, so 34.9), and the same for scales costs groups of 64 a fiftieth.
+__device__ __forceinline__ uint4 ld_global(const uint4* at) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+    return v;
+}
 // bf16 128 + zero twice, of a group's zero
 __device__ __forceinline__ uint32_t zero_pair(uint32_t z) { return (0x4300u | (z & 15u)) * 0x10001u; }
 // Two codes, 16 bits apart, as bf16 128 + code (its last place is 1 there), less 128 + zero: exact.
@@ -148,7 +155,7 @@ k_w4_tiles(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__
             // a row's zeros, 16 groups at a time, the next ones under way: one byte of a row at a time would be a
             // load of 32 sectors, and its wait, for every step
             const uint4* const zeros = reinterpret_cast<const uint4*>(a.w.zeros + n * a.w.ldz);
-            auto zeros_at = [&](int block) { return a.w.zeros && block * 16 < a.w.K / GK ? zeros[block] : make_uint4(0, 0, 0, 0); };
+            auto zeros_at = [&](int block) { return a.w.zeros && block * 16 < a.w.K / GK ? ld_global(zeros + block) : make_uint4(0, 0, 0, 0); };
             int z_block = j0 / 16;
             uint4 z_now = zeros_at(z_block), z_next = zeros_at(z_block + 1);
             auto zero_of = [&](int j) {
