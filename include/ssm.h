@@ -622,8 +622,10 @@ int attn_decode_step(int batch, int n_q_heads, int n_kv_heads, int head_dim, ssm
  * out_dtype SSM_I8: a scale per row and group, the attention cache's rule: amax = max |y| over the group,
  * scale = amax / 127, code = round_half_even(y * (127 / amax)) clamped to [-127, 127], IEEE fp32; amax == 0
  * gives scale and codes 0, a NaN is ignored by amax and gets code 0, an infinite amax gives scale +inf and
- * codes 0.  Squares are summed in fp32, from r times a power of two where they would leave its range: every finite r,
- * small or large, gives its y.  A group of zeros with eps = 0 is 0 / 0: NaN.
+ * codes 0.  So a group whose r holds a NaN or an infinity reads as zeros, and a projection of it is finite: residual_out
+ * and the other types of out show it, this one does not.  (An amax below 2^-121 has no finite 127 / amax: codes are
+ * 127, -127 and 0.)  Squares are summed in fp32, from r times a power of two where they would leave its range: every finite
+ * r, small or large, gives its y.  A group of zeros with eps = 0 is 0 / 0: NaN.
  *
  *   n_rows               >= 0 (0 does nothing); n_rows * n_groups < 2^31
  *   width, n_groups      n_groups divides width; a group is a multiple of 8 channels, up to 32768
@@ -694,7 +696,8 @@ int w4_linear(int64_t M, int64_t N, int64_t K, int group, ssm_dtype_t x_dtype, c
  * spec_probs -- probabilities of logits: p[r][i] = exp(x_i / t) / sum_j exp(x_j / t) with t = temperature[r].
  * A temperature of 2^-100 or less, negative ones included, is greedy: 1 at the first largest logit, 0 elsewhere.
  * A logit of -inf has probability 0; a row whose logits are all -inf gives zeros.  A NaN or +inf among a row's
- * logits, or a NaN temperature, gives a row of NaN.  (Where SSM_DEV_WAIT_TIMEOUT was set, so may be any part of a row.)  A temperature of +inf counts as the largest finite one.
+ * logits, or a NaN temperature, gives a row of NaN.  (Where SSM_DEV_WAIT_TIMEOUT was set, so may be any part of a row.)
+ * A temperature of +inf counts as the largest finite one.  Results below 2^-126 may be 0.
  *
  *   n_rows, vocab        n_rows >= 0 (0 does nothing) < 2^28; vocab 1 .. 2^24
  *   in_dtype, logits     [n_rows][vocab] SSM_BF16 or SSM_F32, row stride ld_in >= vocab, element aligned
@@ -712,6 +715,8 @@ int spec_probs(int64_t n_rows, int64_t vocab, ssm_dtype_t in_dtype, const void* 
  * max(p_a - q_a, 0) (from p_a, if that is 0 everywhere); if all n are kept, from p_n.  Tokens so chosen have the
  * target's distribution.  With draft_probs NULL the drafts were certain: q_i is 1 at d_i and 0 elsewhere.
  *   drawn from w at v = u[b][n_max]: the smallest index whose running sum of w exceeds v * (sum of w)
+ * It chooses tokens only.  The mixers' states are those after the whole block (ssm_decode_tokens moves all requests by the
+ * same count): a caller that goes on from fewer tokens has kept the states of before and runs the kept ones again.
  * Running sums are taken in integers of 2^-62 (exact for values from 2^-38 on), so the token depends on nothing
  * but the values.
  *

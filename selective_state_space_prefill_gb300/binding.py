@@ -753,8 +753,8 @@ def norm_rms(x, weight=None, residual=None, eps=1e-5, n_groups=1, out=None, out_
     x [rows, width] bfloat16 or float32; weight [width] float32; residual like x, bfloat16 or float32.
     ``residual_out`` takes r in residual's dtype: allocated when not given, residual itself for in place, False to
     skip it.  ``out_dtype`` bfloat16, float32, or int8 with a scale per row and group (out_scale [rows, n_groups]
-    float32), which is what w4_linear takes as x and x_scale.  Returns (out, residual_out, out_scale), None for
-    what there is not."""
+    float32), which is what w4_linear takes as x and x_scale; with int8 a group that holds a NaN or an infinity
+    reads as zeros.  Returns (out, residual_out, out_scale), None for what there is not."""
     return _outcome((_steps or step_calls()).norm(x, weight, residual, eps, n_groups, out, out_dtype, residual_out, out_scale,
                                                   _raw(stream)), "norm_rms")
 

@@ -325,7 +325,7 @@ struct W4LinearArgs {
     int x_blocks;
     void* out;
     int64_t ldo;
-    float* parts;                   // [slices of K][M][N], where the plan has several
+    float* parts;                   // the workspace: [slices of K][M][N], where the plan has several; for tiles, x in its order first
 };
 
 struct ProbsArgs {

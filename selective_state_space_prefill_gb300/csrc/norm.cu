@@ -7,7 +7,7 @@
 // barrier; larger ones a CTA's of 64 .. 1024 threads, with as few vectors a thread as that allows for few rows
 // (latency) and four for many (loads in flight, fewer threads at the barriers).  Measured: 8192 x 5120 fp32 in 8
 // groups to bf16 38 us (6.6 TB/s, 0.97 of the copy rate), 16384 x 7168 with an fp32 residual 201 us (7.0 TB/s);
-// one row of 1536 1.4 us in a graph, which is a launch and a load.
+// one row of 1536 1.6 us in a graph, which is a launch and a load.
 #include "common.cuh"
 #include "kernels.h"
 #include "ssm.h"

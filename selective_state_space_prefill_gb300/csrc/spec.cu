@@ -116,7 +116,7 @@ template <> struct Raw<float> {
 // powers are taken twice: their unit would do three times as many in the time that the row's bytes take.)  V
 // vectors of eight logits a thread, from the row's first 16-byte border on; what lies before that and behind the
 // last whole vector (up to 14 logits) is one logit each for the first CTA's first threads.  512 x 131072 bf16 (403 MB)
-// 84 us, 4.8 TB/s, 0.71 of the copy rate: a CTA loads, waits for the row's maximum, takes powers, waits for the sum,
+// 82 us, 4.9 TB/s, 0.72 of the copy rate: a CTA loads, waits for the row's maximum, takes powers, waits for the sum,
 // writes, and four of them an SM do not keep memory busy all the time (2000 x 32000, shorter rows, 5.2 TB/s).  The
 // next rows asked for from L2 ahead of time make 2 to 4 % and are left out.  5 x 50021 3.3 us in a graph.
 template <typename T, int V, int kThreads>
@@ -203,7 +203,9 @@ __global__ void __launch_bounds__(kThreads, V * sizeof(T) <= 16 ? 1024 / kThread
     all.leave();
 }
 
-// Rows longer than a cluster's registers hold: read three times, from L2 after the first.
+// Rows longer than a cluster's registers hold: read three times, from L2 after the first, a logit a load, by eight CTAs: 64 x
+// 300001 bf16 (115 MB) 45 us, 0.38 of the copy rate, 8 x 300001 12.7; few very long rows leave most of the GPU idle (4 x
+// 2^24 2.4 ms, 0.17 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(512) k_spec_probs_long(const ProbsArgs a, int ctas) {
     constexpr int kThreads = 512, kWarps = kThreads / 32;
@@ -302,7 +304,9 @@ template <typename T> __device__ __forceinline__ T warp_sum(T v) {
 // stretch the border falls reads again (from L2) what lies between two notes.  Without notes it read its stretch
 // from the start, block by block.  Of the 19 us of 64 requests x 131072 (67 MB, 9.9 us at the copy rate) the checks of the
 // drafted tokens take 2 (three reads, each waiting for the one before), the sums 9, the slowest of a cluster's CTAs 2
-// to 3, the search 2, starting and ending the rest.  One request: 5.8 us, the same chain of waits.
+// to 3, the search 2, starting and ending the rest.  One request: 6.0 us, the same chain of waits.  Without q half of the bytes
+// go and little of the time, as q's arithmetic is done with zeros: 64 x 131072 18.8 us, without drafts 15.8, 128 x 151937
+// 33 (11.5 of bytes).
 constexpr int kVerifyThreads = 256;
 __global__ void __launch_bounds__(kVerifyThreads, 4) k_spec_verify(const VerifyArgs a, int ctas) {
     constexpr int kThreads = kVerifyThreads, kWarps = kThreads / 32;

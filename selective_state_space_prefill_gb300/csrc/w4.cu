@@ -9,10 +9,13 @@
 // being held in the same order), and become bf16 numbers 16 + code in two operations for two codes.  The group's
 // sum is multiplied by its scale in fp32.  The warps' sums of a block meet in shared memory; where a row of x is
 // more than 16 warps hold, slices of the rows go to different CTAs and a second kernel adds their sums.
-// Measured: 1 x 4096 -> 16384, groups of 128 (34.7 MB), 11.7 us a call on a stream, of which the bytes are 5.1: about six
-// are the first loads' way, the last block's and the warps' exchange, whatever the size, and in between rows come
-// at 5.3 TB/s, which is what the half-rate integer pipe unpacks.  8 x 8192 -> 4096, groups of 32 with zeros and two
-// kernels, 13.2 us; 1 x 1536 -> 768 3.1 us in a graph.
+// Measured, in a graph: 1 x 4096 -> 16384, groups of 128 (34.7 MB), 11.9 us, of which the bytes are 5.1.  With N it is 4.8 us
+// and 0.435 for every 1000 rows (4.9 TB/s, 0.72 of the copy rate; N = 768 takes 3.5, 77824 38.7).  Neither part is
+// accounted for in full: no unit is busy (integer pipe 45 %, 0.48 instructions a cycle and scheduler), so it is waits,
+// at the ring, at the warps' exchange and for the first loads.  8 x 8192 -> 4096, groups of 32 with zeros, 13.2 us,
+// 6.3 of it fixed (four slices, so two kernels) and 1.7 for every 1000 rows (2.9 TB/s: a scale, a zero and eight
+// multiply-adds for every two products); 1 x 1536 -> 768 3.1 us.  x with several scales a row reads them inside the group
+// loop: 8 x 4096 -> 16384 12.8 us with one, 15.2 with four; 8 x 8192 -> 4096 in groups of 32 13.3 and 18.2.
 #include <type_traits>
 
 #include "common.cuh"
@@ -24,8 +27,9 @@ namespace ssm {
 namespace {
 
 // ------------------------------------------------------------------ quantisation
-// A warp per group: a lane holds group / 32 consecutive elements.  Read once, at the rate of memory; the
-// weight is made once and kept.
+// A warp per group: a lane holds group / 32 consecutive elements, loaded one by one.  The weight is made once and kept, so
+// this is the simple kernel: 50021 x 2560 bf16 in groups of 128 246 us, of 32 738 (1.3 and 0.5 TB/s of what it reads and
+// writes; fp32 takes the same time, so a group's instructions are what counts, not its bytes).
 template <typename Tin, int E>
 __global__ void __launch_bounds__(256) k_w4_quantize(const W4Weight w, const Tin* W, int64_t ldw, int64_t n_groups) {
     const int64_t id = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
@@ -521,9 +525,17 @@ int launch_w4_join(const W4LinearArgs& a, int slices, cudaStream_t stream, const
 
 // Whether a call goes to the tiles of w4_tiles.cu: from nine rows of x on where the weight is large.  They unpack it
 // once for 64 rows and cost two or three kernels; here it is unpacked for every 16 rows, and sums of 16 columns
-// are what a turn waits for.  Measured (us, here / tiles, groups of 128): 16 rows x 4096 x 4096 10.0 / 10.4, 8192 x
-// 4096 12.2 / 14.3, 16384 x 4096 28 / 20, 50021 x 2560 81 / 33; 17 rows x 2048 x 2048 5.6 / 6.6, 4096 x 4096 11.9 / 10.3;
-// 64 rows x 768 x 1536 5.2 / 9.2, 2048 x 2048 7.9 / 7.9, 4096 x 4096 19.6 / 11.4.
+// are what a turn waits for.  One border does for all groups; measured (us in a graph, here / tiles, with zeros):
+//                                groups of 128     of 64         of 32
+//     9 rows,  4096 x 4096        10.4 /  9.8      10.6 / 10.7   11.9 / 13.3
+//    16 rows,  8192 x 4096        12.7 / 14.8      14.0 / 16.2   16.1 / 21.9
+//    16 rows, 16384 x 4096        31   / 21        32   / 23     34   / 34
+//    16 rows, 50021 x 2560        89   / 35        91   / 39     94   / 61
+//    17 rows,  2048 x 2048         5.1 /  6.8       5.5 /  7.2    5.9 /  7.9
+//    17 rows,  4096 x 4096        11.9 /  9.9      12.5 / 10.6   15.2 / 13.3
+//    64 rows,  2048 x 2048         7.2 /  8.1       7.7 /  8.6    9.2 / 10.3
+//    64 rows,  4096 x 4096        20   / 12        21   / 13     25   / 16
+//   128 rows,  2048 x 2048        10.4 / 11.4      10.8 /  9.4   13.7 / 11.1
 static bool in_tiles(int M, const W4Weight& w) {
     const int64_t work = (int64_t)((M + 15) / 16) * w.N * w.K;
     return M > 16 ? work > (1 << 24) : M > 8 && work > 3 * (1 << 24);

@@ -8,9 +8,13 @@
 // accumulator of their own (four of them in turn), which other threads, a row each, multiply by the group's
 // scale and add up in fp32 registers.  Eight warps unpack (56 integer operations and 32 subtractions for 64 codes of
 // 32 rows), eight scale, one each issues copies of codes, copies of x and products.  Measured: 64 x 2560 -> 50021, groups
-// of 128 with zeros (67 MB, 16 GFLOP) 36 us on a stream, 0.35 us a step of 128 x 128 codes, at 0.54 instructions a
-// cycle and scheduler; bytes are 10 us of it, products 9, and a seventh is that 391 tiles are no multiple of 152
-// SMs.  With twelve unpacking warps 39, with sixteen (spilling) 135; steps of 64 elements 53.
+// of 128 with zeros (67 MB, 16 GFLOP) 35 us, 0.34 us a step of 128 x 128 codes, at 0.54 instructions a cycle and
+// scheduler; bytes are 10 us of it, products 9, and a seventh is that 391 tiles are no multiple of 152 SMs.  What bounds it
+// is the way of a step from warp to warp (copies, unpacking, products, scaling): with nothing but its waits, arrivals and
+// commits left the loop took 33 us of then 38.  With twelve unpacking warps 39, with sixteen (spilling) 135; steps of 64
+// elements 53.  Groups of 64, two accumulators to hand over in a step, 44 us, of 32, four of them, 72.  More rows of x
+// unpack the weight again for every 64: 128 rows 64 us, 256 112.  Several scales a row of x are read inside the scaling loop:
+// 96 us with four where one takes 36.
 #include <type_traits>
 
 #include "kernels.h"
